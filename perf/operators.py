@@ -183,7 +183,7 @@ def _quantize_f32(y, layout):
         y = _pad(y, rb * BLOCK, kb * BLOCK).view(rb, BLOCK, kb, BLOCK)
         amax = y.abs().amax((1, 3), keepdim=True)
     live = amax >= 2.0 ** -100
-    inv = torch.where(live, 448.0 / torch.where(live, amax, 1.0), 0.0)
+    inv = torch.where(live, torch.full_like(amax, 448.0) / torch.where(live, amax, 1.0), 0.0)
     codes = (y * inv).to(torch.float8_e4m3fn).view(-1, kb * BLOCK)[:rows]
     scale = torch.where(live, amax / 448.0, 0.0)
     # activations' scales are kept with the blocks outermost: [blocks, rows]
