@@ -551,6 +551,82 @@ int hdq_dq_linear(const hdq_dq_grid* g, const uint8_t* core_codes, const void* c
   return hip_status(launch_dq_combine(yd, yc, core_scale, w_fp4->tensor_scale, d, N, y, y_dtype, s));
 }
 
+// ---- FP8 block-128 -------------------------------------------------------
+static_assert(HDQ_FP8_ROWS == kFp8Rows && HDQ_FP8_BLOCKS == kFp8Blocks, "the header's layouts are the kernels'");
+
+static int64_t fp8_kb(int64_t cols) { return (cols + 127) / 128; }
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// cols of a tensor the quantizers and GEMMs take.
+static bool fp8_cols_ok(int64_t cols) { return cols > 0 && cols <= HDQ_FP8_MAX_COLS && cols % 8 == 0; }
+
+static int check_fp8_tensor(const hdq_fp8_tensor& t, int32_t layout, int64_t rows, int64_t cols) {
+  if (t.layout != layout) return HDQ_ERR_UNSUPPORTED;
+  if (t.rows != rows || t.cols != cols || !valid_block(t.had_block) || cols % t.had_block != 0) return HDQ_ERR_SHAPE;
+  if (t.codes == nullptr || t.scale == nullptr) return HDQ_ERR_INVALID;
+  if (!aligned16(t.codes) || reinterpret_cast<uintptr_t>(t.scale) % 4 != 0) return HDQ_ERR_SHAPE;
+  return HDQ_OK;
+}
+
+int hdq_fp8_quantize(const void* x, int64_t rows, int64_t cols, int32_t had_block, int32_t layout,
+                     hdq_fp8_tensor* out, void* stream) {
+  if (x == nullptr || out == nullptr || (layout != HDQ_FP8_ROWS && layout != HDQ_FP8_BLOCKS)) return HDQ_ERR_INVALID;
+  if (rows <= 0 || rows > 0x7fffffff || !fp8_cols_ok(cols) || !aligned16(x)) return HDQ_ERR_SHAPE;
+  hdq_fp8_tensor t = *out;
+  t.layout = layout;
+  t.had_block = had_block;
+  t.rows = rows;
+  t.cols = cols;
+  const int st = check_fp8_tensor(t, layout, rows, cols);
+  if (st != HDQ_OK) return st;
+  *out = t;
+  return hip_status(launch_fp8_quant(static_cast<const uint16_t*>(x), rows, cols, had_block, layout, t.codes, t.scale,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y_dtype) {
+  if (M <= 0 || N <= 0 || M > 0x7fffffff || N > 0x7fffffff || !fp8_cols_ok(K)) return 0;
+  if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return 0;
+  const size_t kb = (size_t)fp8_kb(K);
+  return align_up((size_t)M * kb * 128) + align_up((size_t)M * kb * 4);
+}
+
+int hdq_fp8_linear(const void* x, const hdq_fp8_tensor* xq, int64_t M, int64_t K, const hdq_fp8_tensor* w, void* y,
+                   int32_t y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (w == nullptr || y == nullptr || (x == nullptr && xq == nullptr)) return HDQ_ERR_INVALID;
+  if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
+  const int64_t N = w->rows;
+  if (M <= 0 || M > 0x7fffffff || N <= 0 || N > 0x7fffffff || !fp8_cols_ok(K)) return HDQ_ERR_SHAPE;
+  int st;
+  if ((st = check_fp8_tensor(*w, HDQ_FP8_BLOCKS, N, K)) != HDQ_OK) return st;
+  if (!aligned16(y)) return HDQ_ERR_SHAPE;
+  if (xq != nullptr) {
+    if ((st = check_fp8_tensor(*xq, HDQ_FP8_ROWS, M, K)) != HDQ_OK) return st;
+    if (xq->had_block != w->had_block) return HDQ_ERR_SHAPE;
+  } else if (!aligned16(x)) {
+    return HDQ_ERR_SHAPE;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t kb = fp8_kb(K);
+  const uint8_t* xc;
+  const float* xs;
+  if (xq != nullptr) {
+    xc = xq->codes;
+    xs = xq->scale;
+  } else {
+    const size_t need = hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype);
+    if (ws == nullptr || ws_bytes < need) return HDQ_ERR_WORKSPACE;
+    if (!aligned16(ws)) return HDQ_ERR_SHAPE;
+    uint8_t* codes = static_cast<uint8_t*>(ws);
+    float* scale = reinterpret_cast<float*>(codes + align_up((size_t)(M * kb) * 128));
+    if (launch_fp8_quant(static_cast<const uint16_t*>(x), M, K, w->had_block, kFp8Rows, codes, scale, s) != hipSuccess)
+      return HDQ_ERR_HIP;
+    xc = codes;
+    xs = scale;
+  }
+  return hip_status(launch_gemm_fp8(xc, xs, w->codes, w->scale, y, y_dtype, M, N, kb, s));
+}
+
 int hdq_quantize(const void* x, int64_t rows, int64_t cols, int32_t had_block, int32_t fmt,
                  const float* tensor_amax, const int32_t* decision_dev, hdq_qtensor* out,
                  void* ws, size_t ws_bytes, void* stream) {

@@ -207,6 +207,35 @@ __device__ __forceinline__ float fwht128_w32(float (&x)[32], int lane) {
   }
   return (((lane ^ (lane >> 1)) & 1) != 0) ? -1.0f : 1.0f;
 }
+// The same with Hadamard blocks of HB = 1..128: strides 1..16 in the lane,
+// 32 (HB 64, 128) and 64 (HB 128) across lanes; returns the lane's sign.
+template <int HB>
+__device__ __forceinline__ float fwht_w32(float (&x)[32], int lane) {
+  if constexpr (HB == 128) {
+    return fwht128_w32(x, lane);
+  } else {
+#pragma unroll
+    for (int h = 1; h < 32 && h < HB; h <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if ((i & h) == 0) {
+          const float u = x[i], v = x[i + h];
+          x[i] = u + v;
+          x[i + h] = u - v;
+        }
+      }
+    }
+    if constexpr (HB == 64) {
+      const float s = (lane & 1) ? -1.0f : 1.0f;
+      HDQ_FMAC_DPP8_AT("quad_perm:[1,0,3,2]", "s_nop 1\n\t", 0);
+      HDQ_FMAC_DPP8_AT("quad_perm:[1,0,3,2]", "s_nop 1\n\t", 8);
+      HDQ_FMAC_DPP8_AT("quad_perm:[1,0,3,2]", "s_nop 1\n\t", 16);
+      HDQ_FMAC_DPP8_AT("quad_perm:[1,0,3,2]", "s_nop 1\n\t", 24);
+      return s;
+    }
+    return 1.0f;
+  }
+}
 #undef HDQ_FMAC_DPP8_AT
 #undef HDQ_FMAC_DPP8
 

@@ -218,6 +218,16 @@ hipError_t launch_gemm_fp4_core_add(const uint8_t* xc, const uint8_t* xs, const 
 // y = yd + (yc of the token's cube) x s_c x s_tw (N a multiple of 4).
 hipError_t launch_dq_combine(const float* yd, const float* yc, const float* cscale, const float* wts,
                              const DqGrid& g, int64_t N, void* y, int out_dtype, hipStream_t s);
+// ---- FP8 block-128 (fp8_quant.hip, gemm_fp8.hip) ----
+constexpr int kFp8Rows = 0, kFp8Blocks = 1;  // scale layouts
+// Rotation + quantization: codes uint8 [rows, 128 kb], scale fp32 [kb, rows]
+// (rows) or [ceil(rows / 128), kb] (blocks), kb = ceil(cols / 128).
+hipError_t launch_fp8_quant(const uint16_t* x, int64_t rows, int64_t cols, int hb, int layout, uint8_t* codes,
+                            float* scale, hipStream_t s);
+// y [M, N] (kOutF32 or kOutBf16) from row-scaled activations and
+// block-scaled weights of kb blocks.
+hipError_t launch_gemm_fp8(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
+                           int out_dtype, int64_t M, int64_t N, int64_t kb, hipStream_t s);
 // bf16 x bf16 (full-precision fallback).
 hipError_t launch_gemm_bf16(const uint16_t* x, const uint16_t* w, void* y, int out_dtype,
                             int64_t M, int64_t N, int64_t K, const int32_t* decision,

@@ -26,11 +26,16 @@ PREC_NVFP4, PREC_INT8, PREC_BF16 = 0, 1, 2
 DTYPE_F32, DTYPE_BF16, DTYPE_I32 = 0, 1, 2
 # workspace ops
 OP_SELECT, OP_QUANTIZE, OP_LINEAR, OP_SELECT_Q8, OP_DQ_QUANTIZE, OP_DQ_LINEAR = 0, 1, 2, 3, 4, 5
+# FP8 scale layouts: per 128 elements of a row, per 128 x 128 block
+FP8_ROWS, FP8_BLOCKS = 0, 1
+FP8_BLOCK = 128
+FP8_MAX_COLS = 1 << 22       # HDQ_FP8_MAX_COLS
 
 EXPORTS = ("hdq_select_precision", "hdq_delta_sums", "hdq_select_precision_sums",
            "hdq_select_quantize_int8", "hdq_select_quantize_int8_noalloc", "hdq_linear_dispatch", "hdq_linear_dispatch_delta",
            "hdq_tdc_decide", "hdq_quantize", "hdq_dq_cubes", "hdq_dq_quantize", "hdq_dq_decode_weights",
            "hdq_dq_linear", "hdq_dq_linear_workspace_bytes",
+           "hdq_fp8_quantize", "hdq_fp8_linear_workspace_bytes", "hdq_fp8_linear",
            "hdq_linear", "hdq_workspace_bytes",
            "hdq_status_string", "hdq_version")
 
@@ -64,6 +69,12 @@ class DqGridDesc(_c.Structure):
     """hdq_dq_grid."""
     _fields_ = [("frames", _c.c_int64), ("height", _c.c_int64), ("width", _c.c_int64),
                 ("cube_f", _c.c_int32), ("cube_h", _c.c_int32), ("cube_w", _c.c_int32)]
+
+
+class Fp8TensorDesc(_c.Structure):
+    """hdq_fp8_tensor."""
+    _fields_ = [("layout", _c.c_int32), ("had_block", _c.c_int32), ("rows", _c.c_int64), ("cols", _c.c_int64),
+                ("codes", _p), ("scale", _p)]
 
 
 class WeightsDesc(_c.Structure):
@@ -119,6 +130,13 @@ def _load():
                                 _c.POINTER(QTensorDesc), _p, _p, _c.c_int32, _p, _c.c_size_t, _p]
     L.hdq_dq_linear_workspace_bytes.restype = _c.c_size_t
     L.hdq_dq_linear_workspace_bytes.argtypes = [_c.POINTER(DqGridDesc), _c.c_int64, _c.c_int64, _c.c_int32]
+    L.hdq_fp8_quantize.restype = _c.c_int
+    L.hdq_fp8_quantize.argtypes = [_p, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.POINTER(Fp8TensorDesc), _p]
+    L.hdq_fp8_linear_workspace_bytes.restype = _c.c_size_t
+    L.hdq_fp8_linear_workspace_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
+    L.hdq_fp8_linear.restype = _c.c_int
+    L.hdq_fp8_linear.argtypes = [_p, _c.POINTER(Fp8TensorDesc), _c.c_int64, _c.c_int64, _c.POINTER(Fp8TensorDesc), _p,
+                                 _c.c_int32, _p, _c.c_size_t, _p]
     L.hdq_workspace_bytes.restype = _c.c_size_t
     L.hdq_workspace_bytes.argtypes = [_c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
     L.hdq_status_string.restype = _c.c_char_p
@@ -522,4 +540,103 @@ def linear(precision, x, w, decision=None, xq=None, x_amax=None, y=None, y_dtype
                         _ptr(x_amax), M, K, _c.byref(wd), _ptr(y), y_dtype, _ptr(ws),
                         0 if ws is None else ws.numel(), _stream(stream))
     _check("hdq_linear", st)
+    return y
+
+
+# ---- FP8 block-128 linear layers ----------------------------------------------
+
+def _on(dev, stream):
+    """A context in which `dev` is the current device and `stream` (None: the
+    device's current stream) the current stream, so that what a call
+    allocates belongs to the stream its kernels run on."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev)
+
+
+def _operand(t, name, dtype, shape, dev):
+    """Checks a tensor the library reads or writes in place."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: expected a contiguous {dtype} {shape} tensor on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+class Fp8Tensor:
+    """An FP8 (E4M3) tensor with one float32 scale per block of 128: torch
+    buffers plus the hdq_fp8_tensor fields.  codes uint8 (or float8_e4m3fn)
+    [rows, 128 * kb] with zeros past cols, kb = ceil(cols / 128); scale float32
+    [kb, rows] (FP8_ROWS) or [ceil(rows / 128), kb] (FP8_BLOCKS).  Buffers that
+    are not given are allocated on `device`; given ones (an FP8 checkpoint's
+    weights and block scales) are used as they are."""
+
+    def __init__(self, rows, cols, had_block=1, layout=FP8_ROWS, device=None, codes=None, scale=None):
+        if layout not in (FP8_ROWS, FP8_BLOCKS):
+            raise ValueError(f"unknown FP8 layout {layout}")
+        self.rows, self.cols, self.had_block, self.layout = rows, cols, had_block, layout
+        kb = -(-cols // FP8_BLOCK)
+        dev = codes.device if codes is not None else scale.device if scale is not None else device
+        cshape = (rows, kb * FP8_BLOCK)
+        sshape = (kb, rows) if layout == FP8_ROWS else (-(-rows // FP8_BLOCK), kb)
+        if codes is None:
+            codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+        elif codes.dtype == torch.float8_e4m3fn:
+            codes = codes.view(torch.uint8)
+        if scale is None:
+            scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+        self.codes = _operand(codes, "codes", torch.uint8, cshape, codes.device)
+        self.scale = _operand(scale, "scale", torch.float32, sshape, codes.device)
+
+    def desc(self):
+        return Fp8TensorDesc(self.layout, self.had_block, self.rows, self.cols, self.codes.data_ptr(),
+                             self.scale.data_ptr())
+
+
+def fp8_quantize(x, had_block=1, layout=FP8_ROWS, out=None, stream=None):
+    """hdq_fp8_quantize: rotate a bf16 [rows, cols] tensor and quantize it to
+    FP8 with one scale per 128 elements of a row (activations) or per
+    128 x 128 block (FP8_BLOCKS, weights)."""
+    x = _bf16(x, "x")
+    rows, cols = x.shape
+    with _on(x.device, stream):
+        if out is None:
+            out = Fp8Tensor(rows, cols, had_block, layout, x.device)
+        elif (out.rows, out.cols, out.layout) != (rows, cols, layout) or out.codes.device != x.device:
+            raise ValueError("out does not fit x")
+        d = out.desc()
+        st = lib.hdq_fp8_quantize(_ptr(x), rows, cols, had_block, layout, _c.byref(d), _stream(stream))
+    _check("hdq_fp8_quantize", st)
+    out.had_block = had_block
+    return out
+
+
+def fp8_linear_workspace_bytes(M, K, N, y_dtype=DTYPE_BF16):
+    """hdq_fp8_linear_workspace_bytes: the scratch fp8_linear needs without xq."""
+    return lib.hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype)
+
+
+def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
+    """hdq_fp8_linear: Y[M, N] = X[M, K] @ W[N, K]^T for FP8_BLOCKS weights;
+    x bf16 is quantized within the call (with the weights' had_block), or
+    xq holds the activations already quantized (FP8_ROWS; x is then unused)."""
+    if xq is None:
+        x = _bf16(x, "x")
+        (M, K), dev = x.shape, x.device
+    else:
+        M, K, dev = xq.rows, xq.cols, xq.codes.device
+    if w.codes.device != dev:
+        raise ValueError(f"the weights are on {w.codes.device}, the activations on {dev}")
+    with _on(dev, stream):
+        dt = torch.float32 if y_dtype == DTYPE_F32 else torch.bfloat16
+        y = torch.empty(M, w.rows, dtype=dt, device=dev) if y is None else _operand(y, "y", dt, (M, w.rows), dev)
+        wd = w.desc()
+        if xq is None:
+            ws = _workspace(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, w.rows, y_dtype), dev)
+            st = lib.hdq_fp8_linear(x.data_ptr(), None, M, K, _c.byref(wd), y.data_ptr(), y_dtype, _ptr(ws),
+                                    0 if ws is None else ws.numel(), _stream(stream))
+        else:
+            xd = xq.desc()
+            st = lib.hdq_fp8_linear(None, _c.byref(xd), M, K, _c.byref(wd), y.data_ptr(), y_dtype, None, 0,
+                                    _stream(stream))
+    _check("hdq_fp8_linear", st)
     return y

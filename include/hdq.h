@@ -510,6 +510,74 @@ int hdq_dq_linear(const hdq_dq_grid *g, const uint8_t *core_codes, const void *c
                   const hdq_qtensor *delta, const hdq_qtensor *w_fp4, const void *w_dec, void *y, int32_t y_dtype,
                   void *ws, size_t ws_bytes, void *stream);
 
+/* ---- FP8 block-128 linear layers -------------------------------------------
+ * y = x W^T with both operands in FP8 (OCP E4M3) and one fp32 scale for each
+ * block of 128: of a row for activations (HDQ_FP8_ROWS), of 128 x 128 elements
+ * for weights (HDQ_FP8_BLOCKS, the layout of FP8 checkpoints with block
+ * scales).  Neither the summary nor the explainer has this format; it stands
+ * between the INT8 x INT4 layer and the bf16 fallback.
+ *
+ * A tensor [rows, cols], kb = ceil(cols / 128) blocks per row:
+ *   codes : device uint8 [rows, 128 * kb], 16-byte aligned; E4M3, columns
+ *           past cols hold zeros.
+ *   scale : device fp32, ROWS: [kb, rows] (a block column's scales are
+ *           contiguous over the rows); BLOCKS: [ceil(rows / 128), kb].
+ * With y the (rotated) values and a = max|y| over a block:
+ *   s = fl32(a / 448), code = E4M3 nearest to fl32(y * fl32(448 / a)), ties
+ *   to even, so value = code * s.  A block with a < 2^-100 gets s = 0 and
+ *   zero codes; a block holding a NaN or an infinity gets s = NaN and zero
+ *   codes, so that the outputs that read it are NaN. */
+#define HDQ_FP8_ROWS 0
+#define HDQ_FP8_BLOCKS 1
+#define HDQ_FP8_MAX_COLS (1 << 22)
+typedef struct hdq_fp8_tensor {
+  int32_t layout;    /* HDQ_FP8_*                                     */
+  int32_t had_block; /* Hadamard block the rows were rotated with     */
+  int64_t rows;      /* logical shape of the unquantized tensor       */
+  int64_t cols;
+  uint8_t *codes;    /* device, see above                             */
+  float *scale;      /* device, see above                             */
+} hdq_fp8_tensor;
+
+/*
+ * hdq_fp8_quantize -- rotation fused with FP8 quantization.
+ *   x        : device bf16 [rows, cols], 16-byte aligned; cols a multiple of
+ *              8 and of had_block, at most HDQ_FP8_MAX_COLS.
+ *   had_block: power of two in [1, 128]; 1 rotates nothing.
+ *   out      : host struct with caller-allocated codes and scale; layout,
+ *              had_block, rows, cols are written.
+ */
+int hdq_fp8_quantize(const void *x, int64_t rows, int64_t cols, int32_t had_block, int32_t layout,
+                     hdq_fp8_tensor *out, void *stream);
+
+/* Scratch bytes hdq_fp8_linear needs when xq is NULL (the quantized
+ * activations; 0 when the layer quantizes them in its own kernel); with xq
+ * given it needs none.  0 on bad arguments. */
+size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y_dtype);
+
+/*
+ * hdq_fp8_linear -- Y[M, N] = X[M, K] W[N, K]^T.
+ *   x       : device bf16 [M, K] (unrotated), quantized as hdq_fp8_quantize
+ *             does with the weights' had_block; ignored when xq is given.
+ *   xq      : NULL, or the activations as HDQ_FP8_ROWS [M, K] with the
+ *             weights' had_block.
+ *   w       : HDQ_FP8_BLOCKS [N, K].  K as hdq_fp8_quantize's cols; M and N
+ *             any size.
+ *   y       : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32.
+ *   ws      : device scratch, 256-byte aligned, ws_bytes >=
+ *             hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype) unless xq is
+ *             given.  Nothing in it needs a value before the call; calls that
+ *             may overlap need their own.
+ * y = sum over 128-blocks b of sx[b, m] sw[n / 128, b] sum_{k in b} cx cw, each
+ * scale pair and block sum combined in float32.  With a bf16 output the block
+ * sums run on the FP8 matrix instructions, whose products are aligned to the
+ * largest one of an instruction (at least 14 fraction bits: about 1.3e-5 of
+ * the result in the 2-norm, where rounding to bf16 costs 1.7e-3); with an fp32
+ * output on the bf16 ones (codes are exact in bf16), with float32 sums.
+ */
+int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K, const hdq_fp8_tensor *w,
+                   void *y, int32_t y_dtype, void *ws, size_t ws_bytes, void *stream);
+
 /* Scratch bytes an entry point needs.  op = HDQ_OP_SELECT: (M = rows,
  * K = cols, N = prev_numel); HDQ_OP_SELECT_Q8: (M = rows, K = cols);
  * HDQ_OP_QUANTIZE: (M = rows, K = cols, fmt);
