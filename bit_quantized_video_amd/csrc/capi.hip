@@ -627,6 +627,65 @@ int hdq_fp8_linear(const void* x, const hdq_fp8_tensor* xq, int64_t M, int64_t K
   return hip_status(launch_gemm_fp8(xc, xs, w->codes, w->scale, y, y_dtype, M, N, kb, s));
 }
 
+// ---- group norm ------------------------------------------------------------
+static_assert(HDQ_GROUP_NORM_MAX_CHANNELS == kGnMaxChannels, "the header's limit is the kernel's");
+
+static bool gn_shape_ok(int64_t n, int64_t length, int64_t channels, int32_t groups) {
+  return n > 0 && length > 0 && channels > 0 && channels <= HDQ_GROUP_NORM_MAX_CHANNELS && groups > 0 &&
+         channels % groups == 0 && n <= 0x7fffffff && length <= 0x7fffffff && n * length <= 0x7fffffff;
+}
+
+// The checks both group norms share; fills `g`.
+static int check_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels,
+                            int32_t groups, const float* weight, const float* bias, float eps, int32_t act,
+                            const void* ws, size_t ws_bytes, GroupNormArgs& g) {
+  if (x == nullptr) return HDQ_ERR_INVALID;
+  if (x_dtype != HDQ_DTYPE_F32 && x_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
+  if (act != HDQ_ACT_NONE && act != HDQ_ACT_SILU) return HDQ_ERR_INVALID;
+  if (!(eps >= 0.0f) || eps > 1e30f) return HDQ_ERR_INVALID;
+  if (!gn_shape_ok(n, length, channels, groups)) return HDQ_ERR_SHAPE;
+  if (!aligned16(x) || reinterpret_cast<uintptr_t>(weight) % 4 != 0 || reinterpret_cast<uintptr_t>(bias) % 4 != 0)
+    return HDQ_ERR_SHAPE;
+  if (ws == nullptr || ws_bytes < group_norm_ws_bytes(n, length, channels, groups)) return HDQ_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HDQ_ERR_SHAPE;
+  g = GroupNormArgs{x, x_dtype == HDQ_DTYPE_F32, n, length, channels, groups, weight, bias, eps, act == HDQ_ACT_SILU};
+  return HDQ_OK;
+}
+
+size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups) {
+  return gn_shape_ok(n, length, channels, groups) ? group_norm_ws_bytes(n, length, channels, groups) : 0;
+}
+
+int hdq_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
+                   const float* weight, const float* bias, float eps, int32_t act, void* y, int32_t y_dtype, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (y == nullptr) return HDQ_ERR_INVALID;
+  if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
+  GroupNormArgs g;
+  const int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, g);
+  if (st != HDQ_OK) return st;
+  if (!aligned16(y) || (y == x && y_dtype != x_dtype)) return HDQ_ERR_SHAPE;
+  return hip_status(launch_group_norm(g, y, y_dtype == HDQ_DTYPE_F32, ws, static_cast<hipStream_t>(stream)));
+}
+
+int hdq_group_norm_fp8(const void* x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
+                       const float* weight, const float* bias, float eps, int32_t act, int32_t had_block,
+                       hdq_fp8_tensor* out, void* ws, size_t ws_bytes, void* stream) {
+  if (out == nullptr) return HDQ_ERR_INVALID;
+  GroupNormArgs g;
+  int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, g);
+  if (st != HDQ_OK) return st;
+  if (!fp8_cols_ok(channels)) return HDQ_ERR_SHAPE;
+  hdq_fp8_tensor t = *out;
+  t.layout = HDQ_FP8_ROWS;
+  t.had_block = had_block;
+  t.rows = n * length;
+  t.cols = channels;
+  if ((st = check_fp8_tensor(t, HDQ_FP8_ROWS, t.rows, t.cols)) != HDQ_OK) return st;
+  *out = t;
+  return hip_status(launch_group_norm_fp8(g, had_block, t.codes, t.scale, ws, static_cast<hipStream_t>(stream)));
+}
+
 int hdq_quantize(const void* x, int64_t rows, int64_t cols, int32_t had_block, int32_t fmt,
                  const float* tensor_amax, const int32_t* decision_dev, hdq_qtensor* out,
                  void* ws, size_t ws_bytes, void* stream) {

@@ -30,7 +30,8 @@ __global__ __launch_bounds__(256) void k_fp8_quant_rows(const uint16_t* __restri
   float s, inv;
   fp8_scales(quad_max(absmax32(y)), s, inv);
   uint4 out[2];
-  fp8_encode32(y, inv, out);
+  // lanes past the row (whole Hadamard blocks) hold rotated zeros of either sign
+  fp8_encode32(y, b * kFp8Block + part * 32 < cols ? inv : 0.0f, out);
   uint4* dst = reinterpret_cast<uint4*>(codes + row * ((int64_t)kb * kFp8Block) + b * kFp8Block + part * 32);
   dst[0] = out[0];
   dst[1] = out[1];
@@ -64,7 +65,8 @@ __global__ __launch_bounds__(512) void k_fp8_quant_blocks(const uint16_t* __rest
   if (tid == 0) scale[rb * kb + b] = s;
   if (!in) return;
   uint4 out[2];
-  fp8_encode32(y, inv, out);
+  // lanes past the row (whole Hadamard blocks) hold rotated zeros of either sign
+  fp8_encode32(y, b * kFp8Block + part * 32 < cols ? inv : 0.0f, out);
   uint4* dst = reinterpret_cast<uint4*>(codes + row * ((int64_t)kb * kFp8Block) + b * kFp8Block + part * 32);
   dst[0] = out[0];
   dst[1] = out[1];

@@ -228,6 +228,22 @@ hipError_t launch_fp8_quant(const uint16_t* x, int64_t rows, int64_t cols, int h
 // block-scaled weights of kb blocks.
 hipError_t launch_gemm_fp8(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
                            int out_dtype, int64_t M, int64_t N, int64_t kb, hipStream_t s);
+// ---- group norm (group_norm.hip) ----
+struct GroupNormArgs {
+  const void* x;  // [n, length, C], bf16 or (x_f32) float
+  bool x_f32;
+  int64_t n, length, C, groups;
+  const float* weight;  // [C] or null (1)
+  const float* bias;    // [C] or null (0)
+  float eps;
+  int act;  // 0 none, 1 SiLU
+};
+constexpr int64_t kGnMaxChannels = 8192;  // a row's (mean, M2) pairs fit 64 KB of LDS
+size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups);
+hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* ws, hipStream_t s);
+// The result rotated in blocks of hb and coded as [n * length, C] FP8 rows; C % 8 == 0.
+hipError_t launch_group_norm_fp8(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,
+                                 hipStream_t s);
 // bf16 x bf16 (full-precision fallback).
 hipError_t launch_gemm_bf16(const uint16_t* x, const uint16_t* w, void* y, int out_dtype,
                             int64_t M, int64_t N, int64_t K, const int32_t* decision,

@@ -30,12 +30,16 @@ OP_SELECT, OP_QUANTIZE, OP_LINEAR, OP_SELECT_Q8, OP_DQ_QUANTIZE, OP_DQ_LINEAR = 
 FP8_ROWS, FP8_BLOCKS = 0, 1
 FP8_BLOCK = 128
 FP8_MAX_COLS = 1 << 22       # HDQ_FP8_MAX_COLS
+# activations of the group norms
+ACT_NONE, ACT_SILU = 0, 1
+GROUP_NORM_MAX_CHANNELS = 8192   # HDQ_GROUP_NORM_MAX_CHANNELS
 
 EXPORTS = ("hdq_select_precision", "hdq_delta_sums", "hdq_select_precision_sums",
            "hdq_select_quantize_int8", "hdq_select_quantize_int8_noalloc", "hdq_linear_dispatch", "hdq_linear_dispatch_delta",
            "hdq_tdc_decide", "hdq_quantize", "hdq_dq_cubes", "hdq_dq_quantize", "hdq_dq_decode_weights",
            "hdq_dq_linear", "hdq_dq_linear_workspace_bytes",
            "hdq_fp8_quantize", "hdq_fp8_linear_workspace_bytes", "hdq_fp8_linear",
+           "hdq_group_norm_workspace_bytes", "hdq_group_norm", "hdq_group_norm_fp8",
            "hdq_linear", "hdq_workspace_bytes",
            "hdq_status_string", "hdq_version")
 
@@ -137,6 +141,13 @@ def _load():
     L.hdq_fp8_linear.restype = _c.c_int
     L.hdq_fp8_linear.argtypes = [_p, _c.POINTER(Fp8TensorDesc), _c.c_int64, _c.c_int64, _c.POINTER(Fp8TensorDesc), _p,
                                  _c.c_int32, _p, _c.c_size_t, _p]
+    L.hdq_group_norm_workspace_bytes.restype = _c.c_size_t
+    L.hdq_group_norm_workspace_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
+    norm = [_p, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _p, _p, _c.c_float, _c.c_int32]
+    L.hdq_group_norm.restype = _c.c_int
+    L.hdq_group_norm.argtypes = norm + [_p, _c.c_int32, _p, _c.c_size_t, _p]
+    L.hdq_group_norm_fp8.restype = _c.c_int
+    L.hdq_group_norm_fp8.argtypes = norm + [_c.c_int32, _c.POINTER(Fp8TensorDesc), _p, _c.c_size_t, _p]
     L.hdq_workspace_bytes.restype = _c.c_size_t
     L.hdq_workspace_bytes.argtypes = [_c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
     L.hdq_status_string.restype = _c.c_char_p
@@ -640,3 +651,61 @@ def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
                                     _stream(stream))
     _check("hdq_fp8_linear", st)
     return y
+
+
+# ---- group norm, channels last --------------------------------------------------
+
+def group_norm_workspace_bytes(n, length, channels, groups):
+    """hdq_group_norm_workspace_bytes."""
+    return lib.hdq_group_norm_workspace_bytes(n, length, channels, groups)
+
+
+_NORM_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _norm_input(x, weight, bias):
+    """(x's dtype code, n, length, channels, weight and bias pointers)."""
+    if x.dtype not in _NORM_DTYPES or not x.is_cuda or not x.is_contiguous() or x.dim() < 2:
+        raise ValueError("x must be a contiguous bfloat16 or float32 CUDA tensor [n, ..., channels]")
+    n, C = x.shape[0], x.shape[-1]
+    if x.numel() == 0:
+        raise ValueError("x is empty")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _operand(t, name, torch.float32, (C,), x.device)
+    return _NORM_DTYPES[x.dtype], n, x.numel() // (n * C), C, _ptr(weight), _ptr(bias)
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None, y_dtype=None, ws=None, stream=None):
+    """hdq_group_norm of x [n, ..., channels] (bf16 or float32, channels last)
+    with float32 weight and bias [channels] (None: 1 and 0), and a SiLU for
+    ACT_SILU.  y (may be x) or a new tensor of y_dtype (DTYPE_*; None: x's)."""
+    xt, n, length, C, wp, bp = _norm_input(x, weight, bias)
+    yt = (xt if y is None else _NORM_DTYPES.get(y.dtype)) if y_dtype is None else y_dtype
+    dt = torch.float32 if yt == DTYPE_F32 else torch.bfloat16
+    with _on(x.device, stream):
+        y = torch.empty(x.shape, dtype=dt, device=x.device) if y is None else _operand(y, "y", dt, tuple(x.shape), x.device)
+        ws = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), x.device)
+        st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, y.data_ptr(), yt, _ptr(ws),
+                                0 if ws is None else ws.numel(), _stream(stream))
+    _check("hdq_group_norm", st)
+    return y
+
+
+def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, had_block=1, out=None, ws=None,
+                   stream=None):
+    """hdq_group_norm_fp8: group_norm's float32 result rotated and quantized
+    to an FP8_ROWS tensor [n * length, channels], an fp8_linear's xq."""
+    xt, n, length, C, wp, bp = _norm_input(x, weight, bias)
+    with _on(x.device, stream):
+        if out is None:
+            out = Fp8Tensor(n * length, C, had_block, FP8_ROWS, x.device)
+        elif (out.rows, out.cols, out.layout) != (n * length, C, FP8_ROWS) or out.codes.device != x.device:
+            raise ValueError("out does not fit x")
+        ws = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), x.device)
+        d = out.desc()
+        st = lib.hdq_group_norm_fp8(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, had_block, _c.byref(d),
+                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    _check("hdq_group_norm_fp8", st)
+    out.had_block = had_block
+    return out

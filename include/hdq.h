@@ -578,6 +578,51 @@ size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y
 int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K, const hdq_fp8_tensor *w,
                    void *y, int32_t y_dtype, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- group norm, channels last -----------------------------------------------
+ * x [n, length, channels], a group being channels / groups adjacent channels
+ * of one sample (the norm of video decoders' residual and attention blocks,
+ * whose projections are the linear layers above):
+ *   t = (x - mean) / sqrt(var + eps) * weight + bias,
+ * mean and (biased) variance over the group's length x channels / groups
+ * elements, joined in float64; y = t (HDQ_ACT_NONE) or t / (1 + e^-t)
+ * (HDQ_ACT_SILU).  A NaN or an infinity makes its group's outputs NaN. */
+#define HDQ_ACT_NONE 0
+#define HDQ_ACT_SILU 1
+#define HDQ_GROUP_NORM_MAX_CHANNELS 8192
+
+/* Scratch bytes of both group norms; 0 on bad arguments. */
+size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups);
+
+/*
+ * hdq_group_norm
+ *   x, y        : device [n, length, channels], 16-byte aligned, each
+ *                 HDQ_DTYPE_BF16 or HDQ_DTYPE_F32; y may be x (same type).
+ *   groups      : divides channels (at most HDQ_GROUP_NORM_MAX_CHANNELS);
+ *                 n * length < 2^31.
+ *   weight, bias: device fp32 [channels], or NULL for 1 and 0.
+ *   eps         : >= 0.
+ *   ws, ws_bytes: device scratch, 256-byte aligned, >=
+ *                 hdq_group_norm_workspace_bytes(n, length, channels, groups).
+ *                 Nothing in it needs a value before the call; calls that may
+ *                 overlap need their own.
+ */
+int hdq_group_norm(const void *x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
+                   const float *weight, const float *bias, float eps, int32_t act, void *y, int32_t y_dtype,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * hdq_group_norm_fp8 -- the same norm with its float32 result rotated and
+ * quantized in registers, as hdq_fp8_quantize does with a bf16 tensor: the
+ * activations of an hdq_fp8_linear without a round trip through memory.
+ *   channels    : also a multiple of 8 and of had_block.
+ *   out         : codes and scale for HDQ_FP8_ROWS [n * length, channels];
+ *                 layout, had_block, rows, cols are written.
+ *   the other arguments are hdq_group_norm's.
+ */
+int hdq_group_norm_fp8(const void *x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
+                       const float *weight, const float *bias, float eps, int32_t act, int32_t had_block,
+                       hdq_fp8_tensor *out, void *ws, size_t ws_bytes, void *stream);
+
 /* Scratch bytes an entry point needs.  op = HDQ_OP_SELECT: (M = rows,
  * K = cols, N = prev_numel); HDQ_OP_SELECT_Q8: (M = rows, K = cols);
  * HDQ_OP_QUANTIZE: (M = rows, K = cols, fmt);

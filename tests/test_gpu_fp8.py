@@ -38,7 +38,7 @@ def check_quantized(q, x, had, layout):
 @pytest.mark.parametrize("layout", ["rows", "blocks"])
 @pytest.mark.parametrize("rows,cols,had", [
     (1, 8, 1), (1, 8, 8), (3, 16, 2), (5, 24, 4), (17, 120, 8), (16, 128, 128), (129, 128, 64), (40, 136, 8),
-    (33, 384, 128), (130, 1000, 8), (257, 1920, 128), (64, 2080, 32), (31, 656, 16), (300, 520, 1)])
+    (33, 384, 128), (130, 1000, 8), (257, 1920, 128), (64, 2080, 32), (31, 656, 16), (300, 520, 1), (5, 192, 64), (140, 320, 64)])
 def test_quantize_matches_reference(rows, cols, had, layout):
     x = activations(rows, cols, 7 * rows + cols)
     check_quantized(hdq.fp8_quantize(x.to(DEV), had, LAYOUT[layout]), x, had, layout)
