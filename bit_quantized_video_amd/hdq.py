@@ -556,13 +556,19 @@ def linear(precision, x, w, decision=None, xq=None, x_amax=None, y=None, y_dtype
 
 # ---- FP8 block-128 linear layers ----------------------------------------------
 
-def _on(dev, stream):
-    """A context in which `dev` is the current device and `stream` (None: the
-    device's current stream) the current stream, so that what a call
+def _launch(dev, stream, call):
+    """call(raw stream) with `dev` the current device and `stream` (None: the
+    device's current stream) the current stream, so that what the call
     allocates belongs to the stream its kernels run on."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev)
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(dev):
+            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _operand(t, name, dtype, shape, dev):
@@ -586,17 +592,19 @@ class Fp8Tensor:
             raise ValueError(f"unknown FP8 layout {layout}")
         self.rows, self.cols, self.had_block, self.layout = rows, cols, had_block, layout
         kb = -(-cols // FP8_BLOCK)
-        dev = codes.device if codes is not None else scale.device if scale is not None else device
         cshape = (rows, kb * FP8_BLOCK)
         sshape = (kb, rows) if layout == FP8_ROWS else (-(-rows // FP8_BLOCK), kb)
+        dev = codes.device if codes is not None else scale.device if scale is not None else device
         if codes is None:
             codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
-        elif codes.dtype == torch.float8_e4m3fn:
-            codes = codes.view(torch.uint8)
+        else:
+            codes = codes.view(torch.uint8) if codes.dtype == torch.float8_e4m3fn else codes
+            _operand(codes, "codes", torch.uint8, cshape, dev)
         if scale is None:
             scale = torch.empty(sshape, dtype=torch.float32, device=dev)
-        self.codes = _operand(codes, "codes", torch.uint8, cshape, codes.device)
-        self.scale = _operand(scale, "scale", torch.float32, sshape, codes.device)
+        else:
+            _operand(scale, "scale", torch.float32, sshape, dev)
+        self.codes, self.scale = codes, scale
 
     def desc(self):
         return Fp8TensorDesc(self.layout, self.had_block, self.rows, self.cols, self.codes.data_ptr(),
@@ -609,16 +617,17 @@ def fp8_quantize(x, had_block=1, layout=FP8_ROWS, out=None, stream=None):
     128 x 128 block (FP8_BLOCKS, weights)."""
     x = _bf16(x, "x")
     rows, cols = x.shape
-    with _on(x.device, stream):
-        if out is None:
-            out = Fp8Tensor(rows, cols, had_block, layout, x.device)
-        elif (out.rows, out.cols, out.layout) != (rows, cols, layout) or out.codes.device != x.device:
-            raise ValueError("out does not fit x")
-        d = out.desc()
-        st = lib.hdq_fp8_quantize(_ptr(x), rows, cols, had_block, layout, _c.byref(d), _stream(stream))
-    _check("hdq_fp8_quantize", st)
-    out.had_block = had_block
-    return out
+    dev = x.device
+    if out is not None and ((out.rows, out.cols, out.layout) != (rows, cols, layout) or out.codes.device != dev):
+        raise ValueError("out does not fit x")
+
+    def call(s):
+        q = Fp8Tensor(rows, cols, had_block, layout, dev) if out is None else out
+        d = q.desc()
+        _check("hdq_fp8_quantize", lib.hdq_fp8_quantize(x.data_ptr(), rows, cols, had_block, layout, _c.byref(d), s))
+        q.had_block = had_block
+        return q
+    return _launch(dev, stream, call)
 
 
 def fp8_linear_workspace_bytes(M, K, N, y_dtype=DTYPE_BF16):
@@ -637,20 +646,24 @@ def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
         M, K, dev = xq.rows, xq.cols, xq.codes.device
     if w.codes.device != dev:
         raise ValueError(f"the weights are on {w.codes.device}, the activations on {dev}")
-    with _on(dev, stream):
-        dt = torch.float32 if y_dtype == DTYPE_F32 else torch.bfloat16
-        y = torch.empty(M, w.rows, dtype=dt, device=dev) if y is None else _operand(y, "y", dt, (M, w.rows), dev)
+    N = w.rows
+    dt = torch.float32 if y_dtype == DTYPE_F32 else torch.bfloat16
+    if y is not None:
+        _operand(y, "y", dt, (M, N), dev)
+
+    def call(s):
+        out = torch.empty((M, N), dtype=dt, device=dev) if y is None else y
         wd = w.desc()
         if xq is None:
-            ws = _workspace(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, w.rows, y_dtype), dev)
-            st = lib.hdq_fp8_linear(x.data_ptr(), None, M, K, _c.byref(wd), y.data_ptr(), y_dtype, _ptr(ws),
-                                    0 if ws is None else ws.numel(), _stream(stream))
+            scratch = _workspace(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype), dev)
+            st = lib.hdq_fp8_linear(x.data_ptr(), None, M, K, _c.byref(wd), out.data_ptr(), y_dtype, _ptr(scratch),
+                                    0 if scratch is None else scratch.numel(), s)
         else:
             xd = xq.desc()
-            st = lib.hdq_fp8_linear(None, _c.byref(xd), M, K, _c.byref(wd), y.data_ptr(), y_dtype, None, 0,
-                                    _stream(stream))
-    _check("hdq_fp8_linear", st)
-    return y
+            st = lib.hdq_fp8_linear(None, _c.byref(xd), M, K, _c.byref(wd), out.data_ptr(), y_dtype, None, 0, s)
+        _check("hdq_fp8_linear", st)
+        return out
+    return _launch(dev, stream, call)
 
 
 # ---- group norm, channels last --------------------------------------------------
@@ -683,13 +696,18 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None
     xt, n, length, C, wp, bp = _norm_input(x, weight, bias)
     yt = (xt if y is None else _NORM_DTYPES.get(y.dtype)) if y_dtype is None else y_dtype
     dt = torch.float32 if yt == DTYPE_F32 else torch.bfloat16
-    with _on(x.device, stream):
-        y = torch.empty(x.shape, dtype=dt, device=x.device) if y is None else _operand(y, "y", dt, tuple(x.shape), x.device)
-        ws = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), x.device)
-        st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, y.data_ptr(), yt, _ptr(ws),
-                                0 if ws is None else ws.numel(), _stream(stream))
-    _check("hdq_group_norm", st)
-    return y
+    dev = x.device
+    if y is not None:
+        _operand(y, "y", dt, tuple(x.shape), dev)
+
+    def call(s):
+        out = torch.empty(x.shape, dtype=dt, device=dev) if y is None else y
+        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), dev)
+        st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, out.data_ptr(), yt,
+                                _ptr(scratch), 0 if scratch is None else scratch.numel(), s)
+        _check("hdq_group_norm", st)
+        return out
+    return _launch(dev, stream, call)
 
 
 def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, had_block=1, out=None, ws=None,
@@ -697,15 +715,17 @@ def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, ha
     """hdq_group_norm_fp8: group_norm's float32 result rotated and quantized
     to an FP8_ROWS tensor [n * length, channels], an fp8_linear's xq."""
     xt, n, length, C, wp, bp = _norm_input(x, weight, bias)
-    with _on(x.device, stream):
-        if out is None:
-            out = Fp8Tensor(n * length, C, had_block, FP8_ROWS, x.device)
-        elif (out.rows, out.cols, out.layout) != (n * length, C, FP8_ROWS) or out.codes.device != x.device:
-            raise ValueError("out does not fit x")
-        ws = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), x.device)
-        d = out.desc()
+    dev = x.device
+    if out is not None and ((out.rows, out.cols, out.layout) != (n * length, C, FP8_ROWS) or out.codes.device != dev):
+        raise ValueError("out does not fit x")
+
+    def call(s):
+        q = Fp8Tensor(n * length, C, had_block, FP8_ROWS, dev) if out is None else out
+        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), dev)
+        d = q.desc()
         st = lib.hdq_group_norm_fp8(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, had_block, _c.byref(d),
-                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
-    _check("hdq_group_norm_fp8", st)
-    out.had_block = had_block
-    return out
+                                    _ptr(scratch), 0 if scratch is None else scratch.numel(), s)
+        _check("hdq_group_norm_fp8", st)
+        q.had_block = had_block
+        return q
+    return _launch(dev, stream, call)

@@ -94,7 +94,9 @@ def check_linear(y, xq, wq):
 
 SHAPES = [(1, 8, 1, 8), (1, 128, 16, 128), (1, 1920, 577, 128), (2, 1000, 130, 8), (7, 264, 64, 1), (16, 4096, 96, 64),
           (17, 384, 100, 32), (33, 128, 257, 128), (65, 640, 33, 128), (64, 1928, 200, 8), (130, 776, 129, 8),
-          (226, 2048, 192, 128), (300, 256, 520, 64), (513, 512, 384, 128), (700, 1160, 301, 8), (1000, 256, 1030, 128)]
+          (226, 2048, 192, 128), (300, 256, 520, 64), (513, 512, 384, 128), (700, 1160, 301, 8), (1000, 256, 1030, 128),
+          (2100, 392, 2050, 8), (4200, 128, 1030, 128), (2304, 640, 4096, 64), (16500, 264, 260, 8),
+          (4100, 264, 4200, 8), (4353, 136, 4104, 8), (33, 4224, 100, 128), (1100, 1032, 1000, 8), (20, 40, 6000, 8)]
 
 
 @pytest.mark.parametrize("y_dtype", [hdq.DTYPE_BF16, hdq.DTYPE_F32])
