@@ -638,7 +638,7 @@ static bool gn_shape_ok(int64_t n, int64_t length, int64_t channels, int32_t gro
 // The checks both group norms share; fills `g`.
 static int check_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels,
                             int32_t groups, const float* weight, const float* bias, float eps, int32_t act,
-                            const void* ws, size_t ws_bytes, GroupNormArgs& g) {
+                            const void* ws, size_t ws_bytes, bool fp8, GroupNormArgs& g) {
   if (x == nullptr) return HDQ_ERR_INVALID;
   if (x_dtype != HDQ_DTYPE_F32 && x_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
   if (act != HDQ_ACT_NONE && act != HDQ_ACT_SILU) return HDQ_ERR_INVALID;
@@ -646,14 +646,15 @@ static int check_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t l
   if (!gn_shape_ok(n, length, channels, groups)) return HDQ_ERR_SHAPE;
   if (!aligned16(x) || reinterpret_cast<uintptr_t>(weight) % 4 != 0 || reinterpret_cast<uintptr_t>(bias) % 4 != 0)
     return HDQ_ERR_SHAPE;
-  if (ws == nullptr || ws_bytes < group_norm_ws_bytes(n, length, channels, groups)) return HDQ_ERR_WORKSPACE;
-  if (!aligned16(ws)) return HDQ_ERR_SHAPE;
+  const size_t need = group_norm_ws_bytes(n, length, channels, groups, fp8);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return HDQ_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return HDQ_ERR_SHAPE;
   g = GroupNormArgs{x, x_dtype == HDQ_DTYPE_F32, n, length, channels, groups, weight, bias, eps, act == HDQ_ACT_SILU};
   return HDQ_OK;
 }
 
-size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups) {
-  return gn_shape_ok(n, length, channels, groups) ? group_norm_ws_bytes(n, length, channels, groups) : 0;
+size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups, int32_t fp8) {
+  return gn_shape_ok(n, length, channels, groups) ? group_norm_ws_bytes(n, length, channels, groups, fp8 != 0) : 0;
 }
 
 int hdq_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
@@ -662,7 +663,7 @@ int hdq_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t length, in
   if (y == nullptr) return HDQ_ERR_INVALID;
   if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
   GroupNormArgs g;
-  const int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, g);
+  const int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, false, g);
   if (st != HDQ_OK) return st;
   if (!aligned16(y) || (y == x && y_dtype != x_dtype)) return HDQ_ERR_SHAPE;
   return hip_status(launch_group_norm(g, y, y_dtype == HDQ_DTYPE_F32, ws, static_cast<hipStream_t>(stream)));
@@ -673,7 +674,7 @@ int hdq_group_norm_fp8(const void* x, int32_t x_dtype, int64_t n, int64_t length
                        hdq_fp8_tensor* out, void* ws, size_t ws_bytes, void* stream) {
   if (out == nullptr) return HDQ_ERR_INVALID;
   GroupNormArgs g;
-  int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, g);
+  int st = check_group_norm(x, x_dtype, n, length, channels, groups, weight, bias, eps, act, ws, ws_bytes, true, g);
   if (st != HDQ_OK) return st;
   if (!fp8_cols_ok(channels)) return HDQ_ERR_SHAPE;
   hdq_fp8_tensor t = *out;

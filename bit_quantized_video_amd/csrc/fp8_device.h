@@ -24,6 +24,15 @@ __device__ __forceinline__ float quad_max(float v) {
   return v;
 }
 
+// Maximum over the 16 lanes of a DPP row; NaN wins.
+__device__ __forceinline__ float row16_max(float v) {
+  v = __builtin_elementwise_maximum(
+      v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xF, 0xF, true)));  // row_ror:8
+  v = __builtin_elementwise_maximum(
+      v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x124, 0xF, 0xF, true)));  // row_ror:4
+  return quad_max(v);
+}
+
 // max |y| of the lane's 32 values; NaN wins.
 __device__ __forceinline__ float absmax32(const float (&y)[32]) {
   float m = 0.0f;
@@ -40,6 +49,18 @@ __device__ __forceinline__ void fp8_scales(float a, float& scale, float& inv) {
   const bool live = finite && a >= kTiny;
   scale = live ? a / kFp8Max : (finite ? 0.0f : __builtin_nanf(""));
   inv = live ? kFp8Max / a : 0.0f;
+}
+
+// Eight codes (two words), as fp8_encode32.
+__device__ __forceinline__ uint2 fp8_encode8(const float (&y)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q] * inv, y[4 * q + 1] * inv, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q + 2] * inv, y[4 * q + 3] * inv, v, true);
+    w[q] = inv != 0.0f ? (uint32_t)v : 0u;
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 // E4M3 codes of y * inv (|y * inv| <= 448 (1 + 2^-23), which rounds to 448);

@@ -7,102 +7,89 @@
 // mean and var over the group's length x channels / groups elements.
 //
 // Bound by HBM: x has to be read for the statistics before the first output,
-// and again unless it is still in a cache.  Three kernels: partial statistics
-// per chunk of rows, their join per group, and the normalization.
+// and again unless it is kept.  Three ways, by the size of a sample's slab (the
+// channels of a few groups, see gn_slab): a slab that fits a workgroup's
+// registers is read once, normalized and written in one launch; a slab that one
+// workgroup can still stream takes one launch for the statistics and one for
+// the normalization; else partial statistics per chunk of rows, their join and
+// the normalization.
 //
-// Statistics: a thread sums d = x - s and d^2 in float32 over its rows, s its
-// own first value of each channel, so neither a large mean nor an outlier in
-// another thread's rows cancels digits; the (mean, sum of squared deviations)
-// pairs are joined in float64, in a fixed order:
-//   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2.
+// Statistics: a thread takes up to 16 rows at a time into registers, sums each
+// channel's values (relative to the first) and then the squared deviations from
+// their mean, in float32, so neither a large mean nor an outlier cancels
+// digits; (mean, sum of squared deviations) pairs are joined by
+//   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2,
+// a thread's own in float32, those of threads and workgroups in float64, in a
+// fixed order.
 #include "fp8_device.h"
 #include "hdq_internal.h"
 
+#include <type_traits>
+
 namespace hdq {
 
-constexpr int kGnThreads = 512;
+constexpr int kGnThreads = 512, kGnSlabThreads = 512;
+// a slab's pairs (one per thread and channel of its vector) and groups
+constexpr int kGnSlabLds = kGnSlabThreads * 8 * 8 + 8 * 8192;
 
-// V consecutive elements of bf16 or float data as float.
-template <typename T, int V>
-__device__ __forceinline__ void gn_load(const T* p, float (&v)[V]) {
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (V == 8) {
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
-    } else if constexpr (V == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-    } else {
-      v[0] = bf16_lo(*p);
-    }
-  } else {
-    if constexpr (V == 1) {
-      v[0] = *p;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p + i);
-        v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
-      }
-    }
-  }
-}
-template <typename T, int V>
+// NT: 16-byte stores that do not stay in the caches.
+template <typename T, int V, bool NT = false>
 __device__ __forceinline__ void gn_store(T* p, const float (&v)[V]) {
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else if constexpr (V == 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    } else {
-      *p = (uint16_t)pack_bf16x2(v[0], 0.0f);
-    }
-  } else {
-    if constexpr (V == 1) {
-      *p = v[0];
-    } else {
+  constexpr int WORDS = (V * (int)sizeof(T) + 3) / 4;
+  uint32_t w[WORDS];
 #pragma unroll
-      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  for (int i = 0; i < WORDS; ++i)
+    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : pack_bf16x2(v[(2 * i) % V], v[(2 * i + 1) % V]);
+  if constexpr (sizeof(T) == 2 && V == 1) {
+    *p = (T)w[0];
+  } else if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const v4i q = v4i{(int)w[i], (int)w[i + 1], (int)w[i + 2], (int)w[i + 3]};
+      v4i* d = reinterpret_cast<v4i*>(reinterpret_cast<uint32_t*>(p) + i);
+      if constexpr (NT)
+        __builtin_nontemporal_store(q, d);
+      else
+        *d = q;
     }
+  } else if constexpr (WORDS == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = w[0];
   }
 }
+
+// V elements as loaded (bf16 stay packed).
+template <typename T, int V>
+struct GnRaw {
+  static constexpr int WORDS = (V * (int)sizeof(T) + 3) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(T) == 2 && V == 1) {
+      w[0] = *p;
+    } else if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+      }
+    } else if constexpr (WORDS == 2) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x; w[1] = q.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      v[e] = sizeof(T) == 4 ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+};
 
 // t / (1 + e^-t); e^-t past the float range gives 0.
 __device__ __forceinline__ float gn_silu(float t) {
   return t * __builtin_amdgcn_rcpf(1.0f + __expf(-t));
-}
-
-// Joins `count` (mean, M2) pairs, pair i of weight n(i), over the P lanes of
-// an aligned lane group (lane p takes pairs p, p + P, ...).
-template <typename Pair, typename Weight>
-__device__ __forceinline__ void gn_join(int count, int p, int P, Pair pair, Weight weight, double& n, double& mean,
-                                        double& m2) {
-  double sn = 0.0, sm = 0.0;
-  for (int i = p; i < count; i += P) {
-    const double w = weight(i);
-    if (w > 0.0) {
-      sn += w;
-      sm += w * (double)pair(i).x;
-    }
-  }
-  for (int o = 1; o < P; o <<= 1) {
-    sn += __shfl_xor(sn, o);
-    sm += __shfl_xor(sm, o);
-  }
-  const double mu = sm / sn;
-  double s2 = 0.0;
-  for (int i = p; i < count; i += P) {
-    const double w = weight(i);
-    if (w > 0.0) {
-      const auto q = pair(i);
-      const double d = (double)q.x - mu;
-      s2 += (double)q.y + w * d * d;
-    }
-  }
-  for (int o = 1; o < P; o <<= 1) s2 += __shfl_xor(s2, o);
-  n = sn;
-  mean = mu;
-  m2 = s2;
 }
 
 // Lanes that share a group's join: the largest power of two that leaves every
@@ -113,14 +100,143 @@ __device__ __forceinline__ int gn_lanes(int groups, int threads) {
   return p;
 }
 
+// A thread's (mean, M2) of each channel of one vector over n rows.
+template <int V>
+struct GnSums {
+  float n, mean[V], m2[V];
+  __device__ __forceinline__ void clear() {
+    n = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) mean[e] = m2[e] = 0.0f;
+  }
+  // Joins the first cnt (1 .. K) of K rows held in q.
+  template <typename T, int K>
+  __device__ __forceinline__ void add(const GnRaw<T, V> (&q)[K], int cnt) {
+    float x0[V], m[V], d2[V];
+    q[0].get(x0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = d2[e] = 0.0f;
+#pragma unroll
+    for (int u = 1; u < K; ++u)
+      if (u < cnt) {
+        float v[V];
+        q[u].get(v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) m[e] += v[e] - x0[e];
+      }
+    const float k = (float)cnt, inv = 1.0f / k;
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = __builtin_fmaf(m[e], inv, x0[e]);
+#pragma unroll
+    for (int u = 0; u < K; ++u)
+      if (u < cnt) {
+        float v[V];
+        q[u].get(v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) d2[e] = __builtin_fmaf(v[e] - m[e], v[e] - m[e], d2[e]);
+      }
+    const float f = k / (n + k), g = n * f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float d = m[e] - mean[e];
+      m2[e] += __builtin_fmaf(d * d, g, d2[e]);
+      mean[e] = __builtin_fmaf(d, f, mean[e]);
+    }
+    n += k;
+  }
+  // (mean, M2) of all V channels together (one group's).
+  __device__ __forceinline__ float2 all() const {
+    float m = 0.0f, s = 0.0f, d2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) m += mean[e] - mean[0];
+    m = __builtin_fmaf(m, 1.0f / V, mean[0]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s += m2[e];
+      d2 = __builtin_fmaf(mean[e] - m, mean[e] - m, d2);
+    }
+    return make_float2(m, __builtin_fmaf(n, d2, s));
+  }
+};
+
+// Sums cnt vectors at p, p + step, ...; eight loads are in flight at a time.
+template <typename T, int V>
+__device__ __forceinline__ void gn_stream(const T* p, int64_t step, int cnt, GnSums<V>& t) {
+  int i = 0;
+  GnRaw<T, V> q[8];
+  for (; i + 8 <= cnt; i += 8) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) q[u].load(p + (i + u) * step);
+    t.add(q, 8);
+  }
+  if (i < cnt) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u < cnt) q[u].load(p + (i + u) * step);
+    t.add(q, cnt - i);
+  }
+}
+
+// Puts a thread's sums (row slot pr, channel vector c of cv) among a
+// workgroup's pairs: one pair per thread when a vector lies in one group
+// (MERGE), else one per channel.
+template <bool MERGE, int V>
+__device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, int pr, int c, int cv) {
+  if constexpr (MERGE) {
+    pairs[pr * cv + c] = t.all();
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) pairs[(pr * cv + c) * V + e] = make_float2(t.mean[e], t.m2[e]);
+  }
+}
+// Joins group g's pairs of row slots 0 .. slots - 1 (slot r: rows(r) rows) over
+// the P lanes of an aligned lane group, in one pass: sums of n, n d and
+// M2 + n d^2 in float64, d the distance of a pair's mean from the first one's.
+template <bool MERGE, int V, typename Rows>
+__device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg, int cv, int slots, int p, int P,
+                                              Rows rows, double& n, double& mean, double& m2) {
+  const int per = MERGE ? cg / V : cg, pitch = MERGE ? cv : cv * V;
+  const float2* base = pairs + g * per;
+  const double ref = (double)base[0].x;
+  double sn = 0.0, sd = 0.0, s2 = 0.0;
+  // lane p takes pairs p, p + P, ... of the group's slots x per
+  int r = p / per, c = p - r * per;
+  const int dr = P / per, dc = P - dr * per;
+  while (r < slots) {
+    const float2 q = base[r * pitch + c];
+    const double w = (double)(rows(r) * (MERGE ? V : 1)), d = (double)q.x - ref;
+    sn += w;
+    sd += w * d;
+    s2 += (double)q.y + w * d * d;
+    r += dr;
+    c += dc;
+    if (c >= per) {
+      c -= per;
+      ++r;
+    }
+  }
+  for (int o = 1; o < P; o <<= 1) {
+    sn += __shfl_xor(sn, o);
+    sd += __shfl_xor(sd, o);
+    s2 += __shfl_xor(s2, o);
+  }
+  n = sn;
+  mean = ref + sd / sn;
+  m2 = fmax(s2 - sd * (sd / sn), 0.0) + 0.0 * s2;  // NaN stays NaN
+}
+
+__device__ __forceinline__ float gn_rstd(double m2, double n, float eps) {
+  return (float)(1.0 / sqrt(m2 / n + (double)eps));
+}
+
 // Chunk `c` of sample `s` (blockIdx = s * chunks + c): partial (mean, M2) of
 // every group to part[blockIdx][group].  Thread t of the first cv * rpar owns
 // channel vector t % cv of rows t / cv, t / cv + rpar, ... (cv channel vectors
 // a row, rpar rows at a time; rows of more than 512 vectors in several turns).
-template <typename T, int V>
+template <typename T, int V, bool MERGE>
 __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__ x, int64_t length, int C, int groups,
                                                            int chunks, int64_t rows_per, double2* __restrict__ part) {
-  extern __shared__ float2 pair_s[];  // [rpar][C]
+  extern __shared__ float2 pair_s[];  // [rpar][C], or with MERGE [rpar][cv]
   const int64_t sample = blockIdx.x / (unsigned)chunks;
   const int chunk = (int)(blockIdx.x % (unsigned)chunks);
   const int64_t r0 = chunk * rows_per;
@@ -132,30 +248,13 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__
   auto slot_rows = [&](int r) { return r < rows ? (rows - r + rpar - 1) / rpar : 0; };
   if (pr < rpar) {
     for (int c = (int)threadIdx.x - pr * cv; c < cv; c += kGnThreads) {
-      float s[V], s1[V], s2[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[e] = s1[e] = s2[e] = 0.0f;
       const T* p = xr + (int64_t)pr * C + c * V;
       const int64_t step = (int64_t)rpar * C;
       const int cnt = slot_rows(pr);
-      if (cnt > 0) gn_load<T, V>(p, s);
-#pragma unroll 4
-      for (int i = 1; i < cnt; ++i) {
-        float v[V];
-        gn_load<T, V>(p + i * step, v);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = v[e] - s[e];
-          s1[e] += d;
-          s2[e] = __builtin_fmaf(d, d, s2[e]);
-        }
-      }
-      const float inv = cnt > 0 ? 1.0f / (float)cnt : 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float dm = s1[e] * inv;
-        pair_s[pr * C + c * V + e] = make_float2(s[e] + dm, fmaxf(s2[e] - s1[e] * dm, 0.0f) + 0.0f * s2[e]);
-      }
+      GnSums<V> t;
+      t.clear();
+      gn_stream<T, V>(p, step, cnt, t);
+      gn_put<MERGE, V>(pair_s, t, pr, c, cv);
     }
   }
   __syncthreads();
@@ -164,37 +263,92 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__
     const int g = g0 + (int)threadIdx.x / P;
     if (g >= groups) continue;  // lane groups of P leave together
     double n, mean, m2;
-    gn_join(
-        rpar * cg, (int)threadIdx.x % P, P, [&](int i) { return pair_s[(i / cg) * C + g * cg + i % cg]; },
-        [&](int i) { return (double)slot_rows(i / cg); }, n, mean, m2);
+    gn_join_group<MERGE, V>(pair_s, g, cg, cv, min(rpar, rows), (int)threadIdx.x % P, P, slot_rows, n, mean, m2);
     if (threadIdx.x % P == 0) part[(int64_t)blockIdx.x * groups + g] = make_double2(mean, m2);
   }
 }
 
-// Group g of sample s (one wave each): mean and 1 / sqrt(var + eps) from the
-// chunks' pairs.
+// What the normalization reads per sample and channel, three rows of C floats:
+// mean, a = rstd * weight, b = bias, so t = (x - mean) a + b.
+__device__ __forceinline__ void gn_write_coef(float* __restrict__ coef, int C, int ch, float mean, float rstd,
+                                              const float* __restrict__ weight, const float* __restrict__ bias) {
+  coef[ch] = mean;
+  coef[C + ch] = weight != nullptr ? rstd * weight[ch] : rstd;
+  coef[2 * C + ch] = bias != nullptr ? bias[ch] : 0.0f;
+}
+
+// Group g of sample s (one wave each): the join of at most 512 chunks' pairs,
+// and its channels' coefficients.
+constexpr int kGnMaxChunks = 512;
 __global__ __launch_bounds__(256) void k_gn_final(const double2* __restrict__ part, int64_t total, int64_t length,
                                                   int cg, int groups, int chunks, int64_t rows_per, float eps,
-                                                  float2* __restrict__ stat) {
+                                                  const float* __restrict__ weight, const float* __restrict__ bias,
+                                                  float* __restrict__ coef) {
   const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (id >= total) return;
   const int64_t sample = id / groups;
   const int g = (int)(id - sample * groups), lane = threadIdx.x & 63;
-  double n, mean, m2;
-  gn_join(
-      chunks, lane, 64, [&](int i) { return part[(sample * chunks + i) * groups + g]; },
-      [&](int i) { return (double)min(rows_per, length - i * rows_per) * cg; }, n, mean, m2);
-  if (lane == 0) stat[id] = make_float2((float)mean, (float)(1.0 / sqrt(m2 / n + (double)eps)));
+  // all of the lane's pairs are loaded before the first is used
+  constexpr int PER = kGnMaxChunks / 64;
+  double2 q[PER];
+  double w[PER];
+  double sn = 0.0, sm = 0.0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = lane + 64 * k;
+    w[k] = i < chunks ? (double)min(rows_per, length - i * rows_per) * cg : 0.0;
+    q[k] = i < chunks ? part[(sample * chunks + i) * groups + g] : make_double2(0.0, 0.0);
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    sn += w[k];
+    sm += w[k] * q[k].x;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    sn += __shfl_xor(sn, o);
+    sm += __shfl_xor(sm, o);
+  }
+  const double mean = sm / sn;
+  double m2 = 0.0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const double d = q[k].x - mean;
+    m2 += w[k] > 0.0 ? q[k].y + w[k] * d * d : 0.0;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m2 += __shfl_xor(m2, o);
+  const float rstd = gn_rstd(m2, sn, eps);
+  const int C = cg * groups;
+  for (int c = lane; c < cg; c += 64)
+    gn_write_coef(coef + sample * 3 * C, C, g * cg + c, (float)mean, rstd, weight, bias);
+}
+
+// V consecutive coefficients (16-byte aligned when V is 4 or 8: C is then a multiple of 4).
+template <int V>
+__device__ __forceinline__ void gn_load_coef(const float* __restrict__ p, float (&v)[V]) {
+  GnRaw<float, V> q;
+  q.load(p);
+  q.get(v);
+}
+
+template <int V>
+__device__ __forceinline__ void gn_normalize(float (&v)[V], const float (&mean)[V], const float (&a)[V],
+                                             const float (&b)[V], int act) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float t = __builtin_fmaf(v[e] - mean[e], a[e], b[e]);
+    v[e] = act ? gn_silu(t) : t;
+  }
 }
 
 // Rows [r0, r0 + rows_per) of a sample, one channel vector per thread as in
 // k_gn_partial; the workgroups run through the rows from the end, so that
 // what the statistics read last is still in the memory-side cache.
 template <typename TI, typename TO, int V>
-__global__ __launch_bounds__(kGnThreads) void k_gn_apply(const TI* x, int64_t length, int C, int groups, int chunks,
-                                                         int64_t rows_per, const float2* __restrict__ stat,
-                                                         const float* __restrict__ weight,
-                                                         const float* __restrict__ bias, int act, TO* y) {
+__global__ __launch_bounds__(kGnThreads) void k_gn_apply(const TI* x, int64_t length, int C, int chunks,
+                                                         int64_t rows_per, const float* __restrict__ coef, int act,
+                                                         TO* y) {
   const unsigned blk = gridDim.x - 1 - blockIdx.x;
   const int64_t sample = blk / (unsigned)chunks;
   const int64_t r0 = (blk % (unsigned)chunks) * rows_per;
@@ -203,44 +357,118 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply(const TI* x, int64_t le
   const int cv = C / V, rpar = cv >= kGnThreads ? 1 : kGnThreads / cv;
   const int pr = rpar > 1 ? (int)threadIdx.x / cv : 0;
   if (pr >= rpar) return;
-  const int cg = C / groups;
+  const float* cf = coef + sample * 3 * C;
   for (int c = (int)threadIdx.x - pr * cv; c < cv; c += kGnThreads) {
     float mean[V], a[V], b[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int ch = c * V + e;
-      const float2 st = stat[sample * groups + ch / cg];
-      mean[e] = st.x;
-      a[e] = weight != nullptr ? st.y * weight[ch] : st.y;
-      b[e] = bias != nullptr ? bias[ch] : 0.0f;
-    }
+    gn_load_coef<V>(cf + c * V, mean);
+    gn_load_coef<V>(cf + C + c * V, a);
+    gn_load_coef<V>(cf + 2 * C + c * V, b);
     const int64_t o = base + (int64_t)pr * C + c * V, step = (int64_t)rpar * C;
     const int cnt = pr < rows ? (rows - pr + rpar - 1) / rpar : 0;
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      float v[V];
-      gn_load<TI, V>(x + o + i * step, v);
+    // four rows are loaded before the first is stored (y may be x)
+    for (int i = 0; i < cnt; i += 4) {
+      GnRaw<TI, V> q[4];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float t = __builtin_fmaf(v[e] - mean[e], a[e], b[e]);
-        v[e] = act ? gn_silu(t) : t;
-      }
-      gn_store<TO, V>(y + o + i * step, v);
+      for (int u = 0; u < 4; ++u)
+        if (i + u < cnt) q[u].load(x + o + (i + u) * step);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u < cnt) {
+          float v[V];
+          q[u].get(v);
+          gn_normalize<V>(v, mean, a, b, act);
+          gn_store<TO, V, true>(y + o + (i + u) * step, v);
+        }
     }
   }
 }
 
-// The normalization to FP8 codes: a wave owns one block of 128 channels (lane
-// l: rows l / 4, l / 4 + 16, ... of its chunk, 32 channels of the block's
-// quarter l % 4), keeping its channels' factors in registers over the rows.
+// A slab: `width` channels (whole groups and vectors) of one sample, one
+// workgroup.  Thread t owns channel vector t % cv of rows t / cv, + rpar, ...
+// (cv vectors a slab row).  ROWS > 0: the thread's at most ROWS vectors stay in
+// registers, and the slab is normalized and written from them.  ROWS 0: the
+// slab is streamed and its channels' coefficients are written.
+template <typename TI, typename TO, int V, bool MERGE, int T, int ROWS>
+__global__ __launch_bounds__(T) void k_gn_slab(const TI* x, int64_t length, int C, int cg, int width,
+                                                            int slabs, float eps, const float* __restrict__ weight,
+                                                            const float* __restrict__ bias, int act, TO* y,
+                                                            float* __restrict__ coef) {
+  extern __shared__ float2 pair_s[];  // [rpar][width or cv], then one (mean, rstd) per group of the slab
+  // neighbouring slabs on one XCD at a time: they share the rows' cache lines
+  int lo, hi;
+  xcd_range((int)gridDim.x, blockIdx.x & 7, lo, hi);
+  const unsigned id = (unsigned)lo + (blockIdx.x >> 3);
+  const int64_t sample = id / (unsigned)slabs;
+  const int c0 = (int)(id % (unsigned)slabs) * width, w = min(width, C - c0);
+  const int cv = w / V, rpar = T / cv, groups = w / cg, rows = (int)length;
+  const int pr = (int)threadIdx.x / cv, c = (int)threadIdx.x - pr * cv;
+  float2* const stat_s = pair_s + rpar * (MERGE ? cv : w);
+  auto slot_rows = [&](int r) { return r < rows ? (rows - r + rpar - 1) / rpar : 0; };
+  const int cnt = pr < rpar ? slot_rows(pr) : 0;
+  const int64_t o = (sample * length + pr) * C + c0 + c * V, step = (int64_t)rpar * C;
+  constexpr int KEEP = ROWS > 0 ? ROWS : 1;
+  GnRaw<TI, V> keep[KEEP];
+  GnSums<V> t;
+  t.clear();
+  if constexpr (ROWS > 0) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i < cnt) keep[i].load(x + o + i * step);
+    if (cnt > 0) t.add(keep, cnt);
+  } else {
+    gn_stream<TI, V>(x + o, step, cnt, t);
+  }
+  if (pr < rpar) gn_put<MERGE, V>(pair_s, t, pr, c, cv);
+  __syncthreads();
+  const int P = gn_lanes(groups, T);
+  for (int g0 = 0; g0 < groups; g0 += T / P) {
+    const int g = g0 + (int)threadIdx.x / P;
+    if (g >= groups) continue;  // lane groups of P leave together
+    double n, mean, m2;
+    gn_join_group<MERGE, V>(pair_s, g, cg, cv, min(rpar, rows), (int)threadIdx.x % P, P, slot_rows, n, mean, m2);
+    if (threadIdx.x % P == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, eps));
+  }
+  __syncthreads();
+  if constexpr (ROWS == 0) {
+    for (int ch = threadIdx.x; ch < w; ch += T) {
+      const float2 st = stat_s[ch / cg];
+      gn_write_coef(coef + sample * 3 * C, C, c0 + ch, st.x, st.y, weight, bias);
+    }
+  } else {
+    if (cnt == 0) return;
+    float mean[V], a[V], b[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 st = stat_s[(c * V + (MERGE ? 0 : e)) / cg];
+      const int ch = c0 + c * V + e;
+      mean[e] = st.x;
+      a[e] = weight != nullptr ? st.y * weight[ch] : st.y;
+      b[e] = bias != nullptr ? bias[ch] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i < cnt) {
+        float v[V];
+        keep[i].get(v);
+        gn_normalize<V>(v, mean, a, b, act);
+        gn_store<TO, V>(y + o + i * step, v);
+      }
+  }
+}
+
+// The normalization to FP8 codes: a wave owns one block of 128 channels of four
+// rows at a time, a lane one 8-channel chunk (the one the rotation's lane
+// numbering gives it), whose coefficients it keeps over the rows of its chunk.
+// The loads of kGnRows row groups are in flight together.  (32 channels a lane,
+// as in the quantizer, take 96 registers of coefficients: 20.1 us for 13 x 1350
+// x 512, this form 8.)
+constexpr int kGnRows = 4;
 template <typename TI, int HB>
-__global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int groups,
-                                                      int chunks, int64_t rows_per, const float2* __restrict__ stat,
-                                                      const float* __restrict__ weight,
-                                                      const float* __restrict__ bias, int act, float c_b, int kb,
-                                                      int64_t total_rows, uint8_t* __restrict__ codes,
-                                                      float* __restrict__ scale) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = lane & 3;
+__global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int chunks,
+                                                      int64_t rows_per, const float* __restrict__ coef, int act,
+                                                      float c_b, int kb, int64_t total_rows,
+                                                      uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
   const int kgroups = (kb + 3) >> 2;
   const unsigned blk = gridDim.x - 1 - blockIdx.x;
   const int b = (int)(blk % (unsigned)kgroups) * 4 + wave;
@@ -249,166 +477,253 @@ __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, 
   const int64_t r0 = (rest % (unsigned)chunks) * rows_per;
   const int rows = (int)min(rows_per, length - r0);
   if (b >= kb) return;
-  const int ch0 = b * kFp8Block + part * 32, cg = C / groups;
-  float mean[32], a[32], bs[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const int ch = min(ch0 + e, C - 1);
-    const float2 st = stat[sample * groups + ch / cg];
-    const bool in = ch0 + e < C;
-    mean[e] = st.x;
-    a[e] = in ? (weight != nullptr ? st.y * weight[ch] : st.y) : 0.0f;
-    bs[e] = in && bias != nullptr ? bias[ch] : 0.0f;
+  constexpr int NL = HB >= 16 ? HB / 8 : 1;
+  const int chunk = (l16 & ~(NL - 1)) + fwht_chunk(lane, HB);
+  const int ch = b * kFp8Block + 8 * chunk;
+  const bool in = ch < C;  // C is a multiple of 8
+  const int64_t row0 = sample * length + r0;
+  const TI* p = x + row0 * C + (in ? ch : 0);
+  float mean[8], a[8], bs[8];
+  {
+    const float* cf = coef + sample * 3 * C + (in ? ch : 0);
+    gn_load_coef<8>(cf, mean);
+    gn_load_coef<8>(cf + C, a);
+    gn_load_coef<8>(cf + 2 * C, bs);
   }
-  for (int r = lane >> 2; r < rows; r += 16) {  // whole quads stay together
-    const int64_t row = sample * length + r0 + r;
-    float y[32];
-    const TI* p = x + row * C + ch0;
+  for (int r = lane >> 4; r < rows; r += 4 * kGnRows) {  // 16 lanes stay together
+    GnRaw<TI, 8> q[kGnRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float t[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      const bool in = ch0 + 8 * i < C;  // C is a multiple of 8
-      if (in) gn_load<TI, 8>(p + 8 * i, t);
+    for (int u = 0; u < kGnRows; ++u)
+      if (r + 4 * u < rows) q[u].load(p + (int64_t)(r + 4 * u) * C);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = __builtin_fmaf(t[e] - mean[8 * i + e], a[8 * i + e], bs[8 * i + e]);
-        y[8 * i + e] = in ? (act ? gn_silu(u) : u) : 0.0f;
+    for (int u = 0; u < kGnRows; ++u)
+      if (r + 4 * u < rows) {
+        float y[8];
+        q[u].get(y);
+        gn_normalize<8>(y, mean, a, bs, act);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = in ? y[e] : 0.0f;
+        if constexpr (HB > 1) {
+          const float sc = fwht8(y, lane, HB) * c_b;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = y[e] * sc;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(y[e]));
+        float s, inv;
+        fp8_scales(row16_max(m), s, inv);
+        const int64_t row = row0 + r + 4 * u;
+        // lanes past the channels (whole Hadamard blocks) hold rotated zeros of either sign
+        *reinterpret_cast<uint2*>(codes + row * ((int64_t)kb * kFp8Block) + b * kFp8Block + 8 * chunk) =
+            fp8_encode8(y, in ? inv : 0.0f);
+        if (l16 == 0) scale[(int64_t)b * total_rows + row] = s;
       }
-    }
-    rotate32<HB>(y, lane, c_b);
-    float s, inv;
-    fp8_scales(quad_max(absmax32(y)), s, inv);
-    uint4 out[2];
-    // lanes past the channels (whole Hadamard blocks) hold rotated zeros of either sign
-    fp8_encode32(y, ch0 < C ? inv : 0.0f, out);
-    uint4* dst = reinterpret_cast<uint4*>(codes + row * ((int64_t)kb * kFp8Block) + ch0);
-    dst[0] = out[0];
-    dst[1] = out[1];
-    if (part == 0) scale[(int64_t)b * total_rows + row] = s;
   }
 }
 
-// Chunks of a sample's rows for a pass of about 2048 workgroups that take `per`
-// rows at least.
-static void gn_chunks(int64_t n, int64_t length, int64_t per, int64_t& chunks, int64_t& rows_per) {
-  int64_t want = (2048 + n - 1) / n;
+// Chunks of a sample's rows for a pass of about `total` workgroups that take
+// `per` rows at least.  The statistics take 512, the two per CU that run at a
+// time (1 x 691200 x 256: 88 us, 1024 of them 94); the normalization 8192 (172
+// us with the statistics, 1024 of them 182).
+static void gn_chunks(int64_t total, int64_t n, int64_t length, int64_t per, int64_t& chunks, int64_t& rows_per) {
+  int64_t want = (total + n - 1) / n;
   if (want > (length + per - 1) / per) want = (length + per - 1) / per;
   if (want < 1) want = 1;
   rows_per = (length + want - 1) / want;
   chunks = (length + rows_per - 1) / rows_per;
 }
 
-static int64_t gn_vec(int64_t C) { return C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : 1; }
-static int64_t gn_rpar(int64_t C) {
-  const int64_t cv = C / gn_vec(C);
+// 16-byte vectors where the channels allow, else 8 bytes of bf16, else one channel
+static int64_t gn_vec(int64_t C, bool f32) { return C % 8 == 0 && !f32 ? 8 : C % 4 == 0 ? 4 : 1; }
+static int64_t gn_rpar(int64_t C, int64_t vec) {
+  const int64_t cv = C / vec;
   return cv >= kGnThreads ? 1 : kGnThreads / cv;
 }
 
-static void gn_stat_chunks(int64_t n, int64_t length, int64_t C, int64_t& chunks, int64_t& rows_per) {
-  gn_chunks(n, length, 8 * gn_rpar(C), chunks, rows_per);
+// How a call runs (a rule on its sizes alone; the workspace follows it).
+constexpr int64_t kGnKeep = 16, kGnStream = 64;  // rows a thread keeps / streams at most
+struct GnPlan {
+  int64_t vec;
+  bool merge;            // a vector lies in one group
+  int64_t width, slabs;  // channels of a slab, slabs per sample
+  int64_t threads, rows; // of a slab: threads, and rows per thread
+  bool keep;             // the slab is kept in registers (not for the FP8 form)
+  bool slab;             // the statistics are a slab's
+  int64_t chunks, rows_per;
+};
+
+static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool f32) {
+  GnPlan p;
+  p.vec = gn_vec(C, f32);
+  const int64_t cg = C / groups;
+  p.merge = cg % p.vec == 0;
+  int64_t unit = cg;  // channels of the fewest whole groups that are whole vectors
+  while (unit % p.vec != 0) unit += cg;
+  // slabs of at least 64 channels, fewer where that leaves CUs without work
+  int64_t k = 1;
+  while (k * unit < 64 && n * (C / ((k + 1) * unit)) >= 256) ++k;
+  p.width = k * unit < C ? k * unit : C;
+  p.slabs = (C + p.width - 1) / p.width;
+  const int64_t cv = p.width / p.vec;
+  // the fewest threads whose registers hold the slab: fewer pairs to join
+  p.rows = kGnStream + 1;
+  for (const int64_t t : {(int64_t)256, (int64_t)kGnSlabThreads}) {
+    if (cv > t) continue;
+    p.threads = t;
+    p.rows = (length + t / cv - 1) / (t / cv);
+    if (p.rows <= kGnKeep) break;
+  }
+  // Kept in registers: up to 16 rows of 128 bytes or more; 8 of narrower ones,
+  // whose lines several workgroups share (13 x 675 x 512, 6 rows of 32 bytes:
+  // 11.9 us, with two launches 13.6; 13 x 4000 x 512, 16 rows: 53.9 and 40.1).
+  p.keep = p.threads == 256 && p.rows <= (p.width * (f32 ? 4 : 2) >= 128 ? kGnKeep : kGnKeep / 2);
+  // A larger slab is streamed by one workgroup only where there is one for every
+  // CU: with few of them the chunks' three launches are faster (1 x 16384 x 128:
+  // 15.5 us against 47.0).
+  p.slab = p.keep || (p.threads == 256 && p.rows <= kGnKeep) || (p.rows <= kGnStream && n * p.slabs >= 256);
+  gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
+  return p;
 }
 
 static size_t gn_align(size_t v) { return (v + 255) / 256 * 256; }
+static size_t gn_coef_bytes(int64_t n, int64_t C) { return gn_align((size_t)(n * C) * 3 * sizeof(float)); }
 
-size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups) {
-  int64_t chunks, rows_per;
-  gn_stat_chunks(n, length, C, chunks, rows_per);
-  return gn_align((size_t)(n * chunks * groups) * sizeof(double2)) + gn_align((size_t)(n * groups) * sizeof(float2));
-}
-
-template <typename TI, int V>
-static hipError_t gn_partial(const GroupNormArgs& g, double2* part, int64_t chunks, int64_t rows_per, hipStream_t s) {
-  const size_t lds = (size_t)(gn_rpar(g.C) * g.C) * sizeof(float2);
-  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
-  k_gn_partial<TI, V><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(
-      static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)chunks, rows_per, part);
-  return hipGetLastError();
-}
-
-// The statistics of every (sample, group) into ws; *stat points at them.
-static hipError_t gn_statistics(const GroupNormArgs& g, void* ws, float2** stat, hipStream_t s) {
-  int64_t chunks, rows_per;
-  gn_stat_chunks(g.n, g.length, g.C, chunks, rows_per);
-  double2* part = static_cast<double2*>(ws);
-  *stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) +
-                                    gn_align((size_t)(g.n * chunks * g.groups) * sizeof(double2)));
-  hipError_t e;
-  switch (gn_vec(g.C)) {
-    case 8: e = g.x_f32 ? gn_partial<float, 8>(g, part, chunks, rows_per, s) : gn_partial<uint16_t, 8>(g, part, chunks, rows_per, s); break;
-    case 4: e = g.x_f32 ? gn_partial<float, 4>(g, part, chunks, rows_per, s) : gn_partial<uint16_t, 4>(g, part, chunks, rows_per, s); break;
-    default: e = g.x_f32 ? gn_partial<float, 1>(g, part, chunks, rows_per, s) : gn_partial<uint16_t, 1>(g, part, chunks, rows_per, s); break;
+// Enough for either input type: nothing when the slabs are kept (not the FP8
+// form), else the coefficients, and the chunks' pairs unless the statistics are
+// a slab's.
+size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups, bool fp8) {
+  size_t most = 0;
+  for (const bool f32 : {false, true}) {
+    const GnPlan p = gn_plan(n, length, C, groups, f32);
+    if (p.keep && !fp8) continue;
+    const size_t b = gn_coef_bytes(n, C) + (p.slab ? 0 : gn_align((size_t)(n * p.chunks * groups) * sizeof(double2)));
+    if (b > most) most = b;
   }
+  return most;
+}
+
+// Calls f with the vector length and the merge flag as constants.
+template <typename TI, typename F>
+static hipError_t gn_dispatch(const GnPlan& p, F f) {
+  using std::integral_constant;
+  if constexpr (sizeof(TI) == 2) {
+    if (p.vec == 8)
+      return p.merge ? f(integral_constant<int, 8>{}, std::true_type{}) : f(integral_constant<int, 8>{}, std::false_type{});
+  }
+  if (p.vec == 4)
+    return p.merge ? f(integral_constant<int, 4>{}, std::true_type{}) : f(integral_constant<int, 4>{}, std::false_type{});
+  return f(integral_constant<int, 1>{}, std::true_type{});  // one channel is in one group
+}
+
+template <typename TI, typename TO, int T, int ROWS>
+static hipError_t gn_launch_slab(const GroupNormArgs& g, const GnPlan& p, void* y, float* coef, hipStream_t s) {
+  if (g.n * p.slabs > 0x7fffffff) return hipErrorInvalidValue;
+  return gn_dispatch<TI>(p, [&](auto v, auto merge) {
+    constexpr int V = decltype(v)::value;
+    constexpr bool MERGE = decltype(merge)::value;
+    const int64_t cg = g.C / g.groups;
+    // row slots x vectors are at most one per thread, in a narrower last slab too
+    const size_t lds = ((size_t)T * (MERGE ? 1 : V) + (size_t)(p.width / cg)) * sizeof(float2);
+    const hipError_t e = set_dynamic_lds_once<&k_gn_slab<TI, TO, V, MERGE, T, ROWS>>(kGnSlabLds);
+    if (e != hipSuccess) return e;
+    k_gn_slab<TI, TO, V, MERGE, T, ROWS><<<dim3((unsigned)(g.n * p.slabs)), dim3(T), lds, s>>>(
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)cg, (int)p.width, (int)p.slabs, g.eps, g.weight, g.bias,
+        g.act, static_cast<TO*>(y), coef);
+    return hipGetLastError();
+  });
+}
+
+// The coefficients of every sample and channel into ws.
+template <typename TI>
+static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* ws, hipStream_t s) {
+  float* coef = static_cast<float*>(ws);
+  if (p.slab)
+    return p.threads == 256 ? gn_launch_slab<TI, TI, 256, 0>(g, p, nullptr, coef, s)
+                            : gn_launch_slab<TI, TI, kGnSlabThreads, 0>(g, p, nullptr, coef, s);
+  double2* part = reinterpret_cast<double2*>(static_cast<uint8_t*>(ws) + gn_coef_bytes(g.n, g.C));
+  if (g.n * p.chunks > 0x7fffffff) return hipErrorInvalidValue;
+  const hipError_t e = gn_dispatch<TI>(p, [&](auto v, auto merge) {
+    constexpr int V = decltype(v)::value;
+    constexpr bool MERGE = decltype(merge)::value;
+    const size_t lds = (size_t)(gn_rpar(g.C, V) * g.C) * sizeof(float2) / (MERGE ? V : 1);
+    k_gn_partial<TI, V, MERGE><<<dim3((unsigned)(g.n * p.chunks)), dim3(kGnThreads), lds, s>>>(
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)p.chunks, p.rows_per, part);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
   const int64_t total = g.n * g.groups;
+  if ((total + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
   k_gn_final<<<dim3((unsigned)((total + 3) / 4)), dim3(256), 0, s>>>(part, total, g.length, (int)(g.C / g.groups),
-                                                                     (int)g.groups, (int)chunks, rows_per, g.eps, *stat);
-  return hipGetLastError();
-}
-
-template <typename TI, typename TO, int V>
-static hipError_t gn_apply(const GroupNormArgs& g, const float2* stat, void* y, hipStream_t s) {
-  int64_t chunks, rows_per;
-  gn_chunks(g.n, g.length, 4 * gn_rpar(g.C), chunks, rows_per);
-  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
-  k_gn_apply<TI, TO, V><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), 0, s>>>(
-      static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)chunks, rows_per, stat, g.weight, g.bias,
-      g.act, static_cast<TO*>(y));
+                                                                     (int)g.groups, (int)p.chunks, p.rows_per, g.eps,
+                                                                     g.weight, g.bias, coef);
   return hipGetLastError();
 }
 
 template <typename TI, typename TO>
-static hipError_t gn_apply_v(const GroupNormArgs& g, const float2* stat, void* y, hipStream_t s) {
-  switch (gn_vec(g.C)) {
-    case 8: return gn_apply<TI, TO, 8>(g, stat, y, s);
-    case 4: return gn_apply<TI, TO, 4>(g, stat, y, s);
-    default: return gn_apply<TI, TO, 1>(g, stat, y, s);
+static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStream_t s) {
+  const GnPlan p = gn_plan(g.n, g.length, g.C, g.groups, g.x_f32);
+  if (p.keep) {
+    if (p.rows <= 4) return gn_launch_slab<TI, TO, 256, 4>(g, p, y, nullptr, s);
+    if (p.rows <= 8) return gn_launch_slab<TI, TO, 256, 8>(g, p, y, nullptr, s);
+    return gn_launch_slab<TI, TO, 256, 16>(g, p, y, nullptr, s);
   }
+  const hipError_t e = gn_statistics<TI>(g, p, ws, s);
+  if (e != hipSuccess) return e;
+  int64_t chunks, rows_per;
+  gn_chunks(8192, g.n, g.length, 4 * gn_rpar(g.C, p.vec), chunks, rows_per);
+  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
+  return gn_dispatch<TI>(p, [&](auto v, auto) {
+    constexpr int V = decltype(v)::value;
+    k_gn_apply<TI, TO, V><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), 0, s>>>(
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, static_cast<const float*>(ws), g.act,
+        static_cast<TO*>(y));
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* ws, hipStream_t s) {
-  float2* stat;
-  const hipError_t e = gn_statistics(g, ws, &stat, s);
-  if (e != hipSuccess) return e;
-  if (g.x_f32) return y_f32 ? gn_apply_v<float, float>(g, stat, y, s) : gn_apply_v<float, uint16_t>(g, stat, y, s);
-  return y_f32 ? gn_apply_v<uint16_t, float>(g, stat, y, s) : gn_apply_v<uint16_t, uint16_t>(g, stat, y, s);
+  if (g.x_f32) return y_f32 ? group_norm_t<float, float>(g, y, ws, s) : group_norm_t<float, uint16_t>(g, y, ws, s);
+  return y_f32 ? group_norm_t<uint16_t, float>(g, y, ws, s) : group_norm_t<uint16_t, uint16_t>(g, y, ws, s);
 }
 
 template <typename TI, int HB>
-static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float2* stat, uint8_t* codes, float* scale,
+static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float* coef, uint8_t* codes, float* scale,
                                hipStream_t s) {
   const int64_t kb = fp8_blocks(g.C), kgroups = (kb + 3) / 4;
-  int64_t chunks, rows_per;
-  gn_chunks(g.n * kgroups, g.length, 16, chunks, rows_per);
+  // one pass of a wave's loop: more rows a workgroup were slower (13 x 1350 x
+  // 512 with its statistics: 21.3 us, 32 rows 23.2; 17776 x 1280: 46.0 and 51.9)
+  const int64_t rows_per = 4 * kGnRows, chunks = (g.length + rows_per - 1) / rows_per;
   if (g.n * chunks * kgroups > 0x7fffffff) return hipErrorInvalidValue;
   k_gn_apply_fp8<TI, HB><<<dim3((unsigned)(g.n * chunks * kgroups)), dim3(256), 0, s>>>(
-      static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)chunks, rows_per, stat, g.weight, g.bias,
-      g.act, hadamard_scale(HB), (int)kb, g.n * g.length, codes, scale);
+      static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, coef, g.act, hadamard_scale(HB), (int)kb,
+      g.n * g.length, codes, scale);
   return hipGetLastError();
 }
 
 template <typename TI>
-static hipError_t gn_apply_fp8_hb(const GroupNormArgs& g, int hb, const float2* stat, uint8_t* codes, float* scale,
-                                  hipStream_t s) {
+static hipError_t group_norm_fp8_t(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,
+                                   hipStream_t s) {
+  const hipError_t e = gn_statistics<TI>(g, gn_plan(g.n, g.length, g.C, g.groups, g.x_f32), ws, s);
+  if (e != hipSuccess) return e;
+  const float* coef = static_cast<const float*>(ws);
   switch (hb) {
-    case 1: return gn_apply_fp8<TI, 1>(g, stat, codes, scale, s);
-    case 2: return gn_apply_fp8<TI, 2>(g, stat, codes, scale, s);
-    case 4: return gn_apply_fp8<TI, 4>(g, stat, codes, scale, s);
-    case 8: return gn_apply_fp8<TI, 8>(g, stat, codes, scale, s);
-    case 16: return gn_apply_fp8<TI, 16>(g, stat, codes, scale, s);
-    case 32: return gn_apply_fp8<TI, 32>(g, stat, codes, scale, s);
-    case 64: return gn_apply_fp8<TI, 64>(g, stat, codes, scale, s);
-    case 128: return gn_apply_fp8<TI, 128>(g, stat, codes, scale, s);
+    case 1: return gn_apply_fp8<TI, 1>(g, coef, codes, scale, s);
+    case 2: return gn_apply_fp8<TI, 2>(g, coef, codes, scale, s);
+    case 4: return gn_apply_fp8<TI, 4>(g, coef, codes, scale, s);
+    case 8: return gn_apply_fp8<TI, 8>(g, coef, codes, scale, s);
+    case 16: return gn_apply_fp8<TI, 16>(g, coef, codes, scale, s);
+    case 32: return gn_apply_fp8<TI, 32>(g, coef, codes, scale, s);
+    case 64: return gn_apply_fp8<TI, 64>(g, coef, codes, scale, s);
+    case 128: return gn_apply_fp8<TI, 128>(g, coef, codes, scale, s);
     default: return hipErrorInvalidValue;
   }
 }
 
 hipError_t launch_group_norm_fp8(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,
                                  hipStream_t s) {
-  float2* stat;
-  const hipError_t e = gn_statistics(g, ws, &stat, s);
-  if (e != hipSuccess) return e;
-  return g.x_f32 ? gn_apply_fp8_hb<float>(g, hb, stat, codes, scale, s)
-                 : gn_apply_fp8_hb<uint16_t>(g, hb, stat, codes, scale, s);
+  return g.x_f32 ? group_norm_fp8_t<float>(g, hb, codes, scale, ws, s)
+                 : group_norm_fp8_t<uint16_t>(g, hb, codes, scale, ws, s);
 }
 
 }  // namespace hdq

@@ -239,7 +239,7 @@ struct GroupNormArgs {
   int act;  // 0 none, 1 SiLU
 };
 constexpr int64_t kGnMaxChannels = 8192;  // a row's (mean, M2) pairs fit 64 KB of LDS
-size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups);
+size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups, bool fp8);
 hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* ws, hipStream_t s);
 // The result rotated in blocks of hb and coded as [n * length, C] FP8 rows; C % 8 == 0.
 hipError_t launch_group_norm_fp8(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,

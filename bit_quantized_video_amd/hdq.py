@@ -142,7 +142,7 @@ def _load():
     L.hdq_fp8_linear.argtypes = [_p, _c.POINTER(Fp8TensorDesc), _c.c_int64, _c.c_int64, _c.POINTER(Fp8TensorDesc), _p,
                                  _c.c_int32, _p, _c.c_size_t, _p]
     L.hdq_group_norm_workspace_bytes.restype = _c.c_size_t
-    L.hdq_group_norm_workspace_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
+    L.hdq_group_norm_workspace_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32]
     norm = [_p, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _p, _p, _c.c_float, _c.c_int32]
     L.hdq_group_norm.restype = _c.c_int
     L.hdq_group_norm.argtypes = norm + [_p, _c.c_int32, _p, _c.c_size_t, _p]
@@ -668,9 +668,9 @@ def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
 
 # ---- group norm, channels last --------------------------------------------------
 
-def group_norm_workspace_bytes(n, length, channels, groups):
-    """hdq_group_norm_workspace_bytes."""
-    return lib.hdq_group_norm_workspace_bytes(n, length, channels, groups)
+def group_norm_workspace_bytes(n, length, channels, groups, fp8=False):
+    """hdq_group_norm_workspace_bytes: the scratch group_norm or (fp8) group_norm_fp8 needs."""
+    return lib.hdq_group_norm_workspace_bytes(n, length, channels, groups, int(fp8))
 
 
 _NORM_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
@@ -702,7 +702,7 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None
 
     def call(s):
         out = torch.empty(x.shape, dtype=dt, device=dev) if y is None else y
-        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), dev)
+        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 0), dev)
         st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, out.data_ptr(), yt,
                                 _ptr(scratch), 0 if scratch is None else scratch.numel(), s)
         _check("hdq_group_norm", st)
@@ -721,7 +721,7 @@ def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, ha
 
     def call(s):
         q = Fp8Tensor(n * length, C, had_block, FP8_ROWS, dev) if out is None else out
-        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups), dev)
+        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 1), dev)
         d = q.desc()
         st = lib.hdq_group_norm_fp8(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, had_block, _c.byref(d),
                                     _ptr(scratch), 0 if scratch is None else scratch.numel(), s)

@@ -590,8 +590,9 @@ int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K
 #define HDQ_ACT_SILU 1
 #define HDQ_GROUP_NORM_MAX_CHANNELS 8192
 
-/* Scratch bytes of both group norms; 0 on bad arguments. */
-size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups);
+/* Scratch bytes of hdq_group_norm (fp8 0; 0 for sizes that run in one launch)
+ * or hdq_group_norm_fp8 (fp8 1); 0 on bad arguments. */
+size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channels, int32_t groups, int32_t fp8);
 
 /*
  * hdq_group_norm
@@ -602,9 +603,9 @@ size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channel
  *   weight, bias: device fp32 [channels], or NULL for 1 and 0.
  *   eps         : >= 0.
  *   ws, ws_bytes: device scratch, 256-byte aligned, >=
- *                 hdq_group_norm_workspace_bytes(n, length, channels, groups).
- *                 Nothing in it needs a value before the call; calls that may
- *                 overlap need their own.
+ *                 hdq_group_norm_workspace_bytes(n, length, channels, groups,
+ *                 0) (NULL where that is 0).  Nothing in it needs a value
+ *                 before the call; calls that may overlap need their own.
  */
 int hdq_group_norm(const void *x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,
                    const float *weight, const float *bias, float eps, int32_t act, void *y, int32_t y_dtype,
@@ -617,6 +618,7 @@ int hdq_group_norm(const void *x, int32_t x_dtype, int64_t n, int64_t length, in
  *   channels    : also a multiple of 8 and of had_block.
  *   out         : codes and scale for HDQ_FP8_ROWS [n * length, channels];
  *                 layout, had_block, rows, cols are written.
+ *   ws, ws_bytes: as hdq_group_norm's, with the size for fp8 1.
  *   the other arguments are hdq_group_norm's.
  */
 int hdq_group_norm_fp8(const void *x, int32_t x_dtype, int64_t n, int64_t length, int64_t channels, int32_t groups,

@@ -20,7 +20,9 @@ def test_workspace(hdq):
     for bad in ((0, 5, 8, 2), (1, 0, 8, 2), (1, 5, 0, 1), (1, 5, 8, 3), (1, 5, 8, 0), (1, 5, 8200, 1),
                 (1 << 20, 1 << 20, 8, 2)):
         assert f(*bad) == 0, bad
-    assert f(1, 1, 1, 1) > 0 and f(13, 1350, 512, 32) > 13 * 32 * 8
+    assert f(1, 1, 1, 1) == 0                            # one launch needs none
+    assert f(1, 1, 8, 1, True) >= 3 * 8 * 4              # coefficients of the two-launch FP8 form
+    assert f(1, 100000, 256, 32) >= 3 * 256 * 4 + 32 * 16
 
 
 def test_refusals(hdq):
@@ -42,11 +44,12 @@ def test_refusals(hdq):
             assert norm(fp8, eps=eps) == hdq.ERR_INVALID
         assert norm(fp8, xt=2) == hdq.ERR_UNSUPPORTED
         for kw in (dict(n=0), dict(length=0), dict(length=-1), dict(C=0), dict(G=0), dict(G=7), dict(C=8256, G=8),
-                   dict(n=1 << 16, length=1 << 15), dict(x=FAKE + 8), dict(y=FAKE + 8), dict(w=FAKE + 2),
-                   dict(ws=FAKE + 8)):
+                   dict(n=1 << 16, length=1 << 15), dict(x=FAKE + 8), dict(y=FAKE + 8), dict(w=FAKE + 2)):
             assert norm(fp8, **kw) == hdq.ERR_SHAPE, (fp8, kw)
-        need = hdq.group_norm_workspace_bytes(2, 50, 64, 8)
-        assert norm(fp8, ws=None) == hdq.ERR_WORKSPACE and norm(fp8, wsb=need - 1) == hdq.ERR_WORKSPACE
+        need = hdq.group_norm_workspace_bytes(1, 100000, 64, 8, fp8)
+        big = dict(n=1, length=100000)
+        assert norm(fp8, ws=None, **big) == hdq.ERR_WORKSPACE and norm(fp8, wsb=need - 1, **big) == hdq.ERR_WORKSPACE
+        assert norm(fp8, ws=FAKE + 8, **big) == hdq.ERR_SHAPE
     assert norm(False, yt=2) == hdq.ERR_UNSUPPORTED
     assert norm(False, xt=0, yt=1, y=FAKE) == hdq.ERR_SHAPE       # in place between types
     assert norm(True, C=60, G=4, had=4) == hdq.ERR_SHAPE          # no multiple of 8
