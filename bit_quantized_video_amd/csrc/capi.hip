@@ -588,6 +588,7 @@ size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y
   if (M <= 0 || N <= 0 || M > 0x7fffffff || N > 0x7fffffff || !fp8_cols_ok(K)) return 0;
   if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return 0;
   const size_t kb = (size_t)fp8_kb(K);
+  if (gemm_fp8_quantizes(M, (int64_t)kb)) return 0;
   return align_up((size_t)M * kb * 128) + align_up((size_t)M * kb * 4);
 }
 
@@ -613,6 +614,9 @@ int hdq_fp8_linear(const void* x, const hdq_fp8_tensor* xq, int64_t M, int64_t K
   if (xq != nullptr) {
     xc = xq->codes;
     xs = xq->scale;
+  } else if (gemm_fp8_quantizes(M, kb)) {
+    return hip_status(launch_gemm_fp8_bf16(static_cast<const uint16_t*>(x), K, w->had_block, w->codes, w->scale, y,
+                                           y_dtype, M, N, kb, s));
   } else {
     const size_t need = hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype);
     if (ws == nullptr || ws_bytes < need) return HDQ_ERR_WORKSPACE;

@@ -5,127 +5,149 @@
 
 namespace hdq {
 
-// Few rows or small layers: no LDS staging, no barrier in the K loop.  A
-// workgroup owns MT x 16 tokens by NT x 16 features; its WAVES waves take the
-// blocks of K in turn (wave w: w, w + WAVES, ...), each reading its fragments
-// from global memory straight into registers one block ahead, and the partial
-// tiles are added over LDS in a fixed order.  Bound by the weights' bytes at
-// few rows.
-template <int OUT, int MT, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_fp8_skinny(const uint8_t* __restrict__ xc,
-                                                           const float* __restrict__ xs,
-                                                           const uint8_t* __restrict__ wc,
-                                                           const float* __restrict__ ws, void* __restrict__ Y,
-                                                           int64_t M, int N, int kb, int tiles_n) {
+// At most 16 tokens (single-token serving): no LDS staging of the weights and no
+// barrier in the K loop.  A workgroup owns 16 features; its WAVES waves take the
+// blocks of K in turn (wave w: w, w + WAVES, ...), each reading its weight
+// fragments from global memory straight into registers one block ahead, and
+// the partial tiles are added over LDS in a fixed order.  Bound by the weights'
+// bytes, and for small layers by the launch.
+//
+// HB > 0: the activations come as bf16 and the workgroup quantizes them itself
+// (rotation block HB), into LDS, while its first weights are on their way: the
+// same codes as k_fp8_quant_rows', without a launch and a workspace.  One pass
+// of its threads has to do, M x kb <= 16 WAVES row blocks.
+template <int OUT, int WAVES, int HB>
+__global__ __launch_bounds__(64 * WAVES) void k_fp8_few(const uint8_t* __restrict__ xc, const float* __restrict__ xs,
+                                                        const uint16_t* __restrict__ xb, int K, float c_b,
+                                                        const uint8_t* __restrict__ wc, const float* __restrict__ ws,
+                                                        void* __restrict__ Y, int M, int N, int kb) {
   constexpr bool FAST = OUT == kOutBf16;
-  __shared__ v4f part[WAVES > 1 ? WAVES / 2 : 1][MT * NT][64];
+  constexpr int XBLOCKS = HB > 0 ? 16 * WAVES : 1;
+  __shared__ v4f part[WAVES / 2][64];
+  __shared__ __attribute__((aligned(16))) uint8_t xcodes[XBLOCKS * kFp8Block];
+  __shared__ float xscale[XBLOCKS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
-  const int tn = (int)(blockIdx.x % (unsigned)tiles_n);
-  const int64_t m0 = (int64_t)(blockIdx.x / (unsigned)tiles_n) * (16 * MT);
-  const int n0 = tn * (16 * NT);
+  const int n0 = blockIdx.x * 16;
   const int64_t ld = (int64_t)kb * kFp8Block;
   // rows past the end repeat the last one; their results are not stored
-  const uint8_t* xp[MT];
-  const float* xsp[MT];
-  const uint8_t* wp[NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = min(m0 + 16 * i + r16, M - 1);
-    xp[i] = xc + m * ld + 16 * q;
-    xsp[i] = xs + m;
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j) wp[j] = wc + (int64_t)min(n0 + 16 * j + r16, N - 1) * ld + 16 * q;
+  const int m = min(r16, M - 1);
+  const uint8_t* xp = HB > 0 ? nullptr : xc + m * ld + 16 * q;
+  const uint8_t* wp = wc + (int64_t)min(n0 + r16, N - 1) * ld + 16 * q;
   // the tile's features lie in one block row of the weights' scales
   const float* wsp = ws + (int64_t)(n0 / kFp8Block) * kb;
 
   struct Block {
-    Fp8Frag x[MT], w[NT];
-    float s[MT];
+    Fp8Frag x, w;
+    float s;
   };
-  auto load = [&](Block& b, int k) {
+  auto load_w = [&](Block& b, int k) {
     const int64_t o = (int64_t)k * kFp8Block;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      b.w[j].lo = *reinterpret_cast<const v4i*>(wp[j] + o);
-      b.w[j].hi = *reinterpret_cast<const v4i*>(wp[j] + o + 64);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      b.x[i].lo = *reinterpret_cast<const v4i*>(xp[i] + o);
-      b.x[i].hi = *reinterpret_cast<const v4i*>(xp[i] + o + 64);
-      b.s[i] = xsp[i][(int64_t)k * M] * wsp[k];
+    b.w.lo = *reinterpret_cast<const v4i*>(wp + o);
+    b.w.hi = *reinterpret_cast<const v4i*>(wp + o + 64);
+    b.s = wsp[k];
+  };
+  auto load_x = [&](Block& b, int k) {
+    if constexpr (HB > 0) {
+      const uint8_t* p = xcodes + (m * kb + k) * kFp8Block + 16 * q;
+      b.x.lo = *reinterpret_cast<const v4i*>(p);
+      b.x.hi = *reinterpret_cast<const v4i*>(p + 64);
+      b.s *= xscale[m * kb + k];
+    } else {
+      const int64_t o = (int64_t)k * kFp8Block;
+      b.x.lo = *reinterpret_cast<const v4i*>(xp + o);
+      b.x.hi = *reinterpret_cast<const v4i*>(xp + o + 64);
+      b.s *= xs[(int64_t)k * M + m];
     }
   };
-  v4f acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   auto compute = [&](const Block& b) {
-    Fp8Operand<FAST> w[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) w[j].set(b.w[j]);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      Fp8Operand<FAST> x;
-      x.set(b.x[i]);
-      v4f p[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) p[j] = block_product(w[j], x);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) add_scaled(acc[i][j], p[j], b.s[i]);
-    }
+    Fp8Operand<FAST> w, x;
+    w.set(b.w);
+    x.set(b.x);
+    add_scaled(acc, block_product(w, x), b.s);
   };
   Block b0, b1;
   int k = wave;
-  if (k < kb) load(b0, k);
+  if (k < kb) load_w(b0, k);
+  if constexpr (HB > 0) {
+    const int rb = threadIdx.x >> 2, part4 = threadIdx.x & 3;  // a quad per row block
+    if (rb < M * kb) {
+      const int row = rb / kb, b = rb - row * kb;
+      float y[32];
+      load_row32(reinterpret_cast<const uint4*>(xb + (int64_t)row * K), b * 16 + part4 * 4, K >> 3, y);
+      rotate32<HB>(y, lane, c_b);
+      float s, inv;
+      fp8_scales(quad_max(absmax32(y)), s, inv);
+      uint4 out[2];
+      fp8_encode32(y, b * kFp8Block + part4 * 32 < K ? inv : 0.0f, out);
+      uint4* dst = reinterpret_cast<uint4*>(xcodes + rb * kFp8Block + part4 * 32);
+      dst[0] = out[0];
+      dst[1] = out[1];
+      if (part4 == 0) xscale[rb] = s;
+    }
+    __syncthreads();
+  }
+  if (k < kb) load_x(b0, k);
   while (k < kb) {
-    if (k + WAVES < kb) load(b1, k + WAVES);
+    if (k + WAVES < kb) {
+      load_w(b1, k + WAVES);
+      load_x(b1, k + WAVES);
+    }
     compute(b0);
     k += WAVES;
     if (k >= kb) break;
-    if (k + WAVES < kb) load(b0, k + WAVES);
+    if (k + WAVES < kb) {
+      load_w(b0, k + WAVES);
+      load_x(b0, k + WAVES);
+    }
     compute(b1);
     k += WAVES;
   }
   // halving sum over the waves: wave w adds wave w + h
 #pragma unroll
   for (int h = WAVES / 2; h >= 1; h >>= 1) {
-    if (wave >= h && wave < 2 * h) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave - h][i * NT + j][lane] = acc[i][j];
-    }
+    if (wave >= h && wave < 2 * h) part[wave - h][lane] = acc;
     __syncthreads();
-    if (wave < h) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] += part[wave][i * NT + j][lane];
-    }
+    if (wave < h) acc += part[wave][lane];
     __syncthreads();
   }
-  if (wave != 0) return;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + 16 * i + r16;
-    if (m >= M) continue;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) store_out4<OUT>(Y, m, n0 + 16 * j + 4 * q, N, acc[i][j]);
+  if (wave == 0 && r16 < M) store_out4<OUT>(Y, r16, n0 + 4 * q, N, acc);
+}
+
+constexpr int kFewWaves = 8;
+
+template <int OUT, int HB>
+static hipError_t launch_few(const uint8_t* xc, const float* xs, const uint16_t* xb, int64_t K, const uint8_t* wc,
+                             const float* ws, void* y, int64_t M, int64_t N, int64_t kb, hipStream_t s) {
+  k_fp8_few<OUT, kFewWaves, HB><<<dim3((unsigned)((N + 15) / 16)), dim3(64 * kFewWaves), 0, s>>>(
+      xc, xs, xb, (int)K, HB > 0 ? hadamard_scale(HB) : 1.0f, wc, ws, y, (int)M, (int)N, (int)kb);
+  return hipGetLastError();
+}
+
+bool gemm_fp8_quantizes(int64_t M, int64_t kb) { return M <= 16 && M * kb <= 16 * kFewWaves; }
+
+template <int OUT>
+static hipError_t launch_few_bf16(const uint16_t* x, int64_t K, int hb, const uint8_t* wc, const float* ws, void* y,
+                                  int64_t M, int64_t N, int64_t kb, hipStream_t s) {
+  switch (hb) {
+    case 1: return launch_few<OUT, 1>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 2: return launch_few<OUT, 2>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 4: return launch_few<OUT, 4>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 8: return launch_few<OUT, 8>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 16: return launch_few<OUT, 16>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 32: return launch_few<OUT, 32>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 64: return launch_few<OUT, 64>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    case 128: return launch_few<OUT, 128>(nullptr, nullptr, x, K, wc, ws, y, M, N, kb, s);
+    default: return hipErrorInvalidValue;
   }
 }
 
-template <int OUT, int MT, int NT, int WAVES>
-static hipError_t launch_skinny(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
-                                int64_t M, int64_t N, int64_t kb, hipStream_t s) {
-  const int64_t tiles_n = (N + 16 * NT - 1) / (16 * NT), tiles_m = (M + 16 * MT - 1) / (16 * MT);
-  if (tiles_n * tiles_m > 0x7fffffff) return hipErrorInvalidValue;
-  k_fp8_skinny<OUT, MT, NT, WAVES><<<dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WAVES), 0, s>>>(
-      xc, xs, wc, ws, y, M, (int)N, (int)kb, (int)tiles_n);
-  return hipGetLastError();
+hipError_t launch_gemm_fp8_bf16(const uint16_t* x, int64_t K, int hb, const uint8_t* wc, const float* ws, void* y,
+                                int out_dtype, int64_t M, int64_t N, int64_t kb, hipStream_t s) {
+  if (!gemm_fp8_quantizes(M, kb)) return hipErrorNotSupported;
+  return out_dtype == kOutBf16 ? launch_few_bf16<kOutBf16>(x, K, hb, wc, ws, y, M, N, kb, s)
+                               : launch_few_bf16<kOutF32>(x, K, hb, wc, ws, y, M, N, kb, s);
 }
 
 // Middle sizes: one tile of 32 WM_T x 32 WN_T per workgroup, KW groups of 2 x 2
@@ -329,7 +351,8 @@ static hipError_t launch_pipe(const uint8_t* xc, const float* xs, const uint8_t*
 
 // Which kernel: by how many tiles of each size there are for the 256 CUs.
 // Measured on both sides of each border (us, bf16 output, N x K in brackets):
-//  * 16 tokens: skinny 6.0, 32 x 64 tiles 5.8 (5760 x 1920); one token 4.9 / 5.8.
+//  * up to 16 tokens: k_fp8_few 6.0, 32 x 64 tiles 5.8 (16, 5760 x 1920); one
+//    token 4.9 / 5.8.
 //  * fewer than 192 tiles of 64 x 64: 32 x 64 tiles with four K groups 6.2, 64 x
 //    64 tiles 7.2 (64 tokens, 5760 x 1920), 8.8 / 12.0 (226, 1920 x 4096); with
 //    256 of them (1024, 1024 x 1024) 8.8 / 5.6.
@@ -341,7 +364,7 @@ template <int OUT>
 static hipError_t launch_fp8_out(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
                                  int64_t M, int64_t N, int64_t kb, hipStream_t s) {
   const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
-  if (M <= 16) return launch_skinny<OUT, 1, 1, 8>(xc, xs, wc, ws, y, M, N, kb, s);
+  if (M <= 16) return launch_few<OUT, 0>(xc, xs, nullptr, 0, wc, ws, y, M, N, kb, s);
   if (tiles(64, 64) < 192) return launch_deep<OUT, 1, 2, 4, 3, false>(xc, xs, wc, ws, y, M, N, kb, s);
   if (tiles(128, 128) < 300) return launch_deep<OUT, 2, 2, 1, 4, true>(xc, xs, wc, ws, y, M, N, kb, s);
   if (tiles(256, 256) < 256) return launch_pipe<OUT, 4, 4, 4>(xc, xs, wc, ws, y, M, N, kb, 512, s);

@@ -228,6 +228,11 @@ hipError_t launch_fp8_quant(const uint16_t* x, int64_t rows, int64_t cols, int h
 // block-scaled weights of kb blocks.
 hipError_t launch_gemm_fp8(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
                            int out_dtype, int64_t M, int64_t N, int64_t kb, hipStream_t s);
+// The same from bf16 activations [M, K], quantized (rotation block hb) by the
+// GEMM's own workgroups; hipErrorNotSupported unless gemm_fp8_quantizes.
+bool gemm_fp8_quantizes(int64_t M, int64_t kb);
+hipError_t launch_gemm_fp8_bf16(const uint16_t* x, int64_t K, int hb, const uint8_t* wc, const float* ws, void* y,
+                                int out_dtype, int64_t M, int64_t N, int64_t kb, hipStream_t s);
 // ---- group norm (group_norm.hip) ----
 struct GroupNormArgs {
   const void* x;  // [n, length, C], bf16 or (x_f32) float

@@ -573,7 +573,7 @@ def _launch(dev, stream, call):
 
 def _operand(t, name, dtype, shape, dev):
     """Checks a tensor the library reads or writes in place."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name}: expected a contiguous {dtype} {shape} tensor on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t
@@ -678,15 +678,15 @@ _NORM_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 def _norm_input(x, weight, bias):
     """(x's dtype code, n, length, channels, weight and bias pointers)."""
-    if x.dtype not in _NORM_DTYPES or not x.is_cuda or not x.is_contiguous() or x.dim() < 2:
+    xt, shape, dev = _NORM_DTYPES.get(x.dtype), x.shape, x.device
+    if xt is None or not x.is_cuda or not x.is_contiguous() or len(shape) < 2:
         raise ValueError("x must be a contiguous bfloat16 or float32 CUDA tensor [n, ..., channels]")
-    n, C = x.shape[0], x.shape[-1]
-    if x.numel() == 0:
+    n, C, numel = shape[0], shape[-1], x.numel()
+    if numel == 0:
         raise ValueError("x is empty")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _operand(t, name, torch.float32, (C,), x.device)
-    return _NORM_DTYPES[x.dtype], n, x.numel() // (n * C), C, _ptr(weight), _ptr(bias)
+    wp = _operand(weight, "weight", torch.float32, (C,), dev).data_ptr() if weight is not None else None
+    bp = _operand(bias, "bias", torch.float32, (C,), dev).data_ptr() if bias is not None else None
+    return xt, n, numel // (n * C), C, wp, bp
 
 
 def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None, y_dtype=None, ws=None, stream=None):
@@ -698,7 +698,7 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None
     dt = torch.float32 if yt == DTYPE_F32 else torch.bfloat16
     dev = x.device
     if y is not None:
-        _operand(y, "y", dt, tuple(x.shape), dev)
+        _operand(y, "y", dt, x.shape, dev)
 
     def call(s):
         out = torch.empty(x.shape, dtype=dt, device=dev) if y is None else y

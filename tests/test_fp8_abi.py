@@ -18,6 +18,8 @@ def test_workspace(hdq):
     f = hdq.fp8_linear_workspace_bytes
     assert f(0, 128, 16) == 0 and f(8, 12, 16) == 0 and f(8, 128, 0) == 0 and f(8, 128, 16, hdq.DTYPE_I32) == 0
     assert f(8, hdq.FP8_MAX_COLS + 8, 16) == 0
+    assert f(1, 16384, 512) == 0 and f(16, 1024, 512) == 0          # quantized within the product's kernel
+    assert f(1, 16512, 512) > 0 and f(17, 128, 512) > 0
     M, K = 1000, 1000
     assert f(M, K, 512) >= M * 1024 + 4 * M * 8       # codes and scales
 

@@ -96,7 +96,9 @@ SHAPES = [(1, 8, 1, 8), (1, 128, 16, 128), (1, 1920, 577, 128), (2, 1000, 130, 8
           (17, 384, 100, 32), (33, 128, 257, 128), (65, 640, 33, 128), (64, 1928, 200, 8), (130, 776, 129, 8),
           (226, 2048, 192, 128), (300, 256, 520, 64), (513, 512, 384, 128), (700, 1160, 301, 8), (1000, 256, 1030, 128),
           (2100, 392, 2050, 8), (4200, 128, 1030, 128), (2304, 640, 4096, 64), (16500, 264, 260, 8),
-          (4100, 264, 4200, 8), (4353, 136, 4104, 8), (33, 4224, 100, 128), (1100, 1032, 1000, 8), (20, 40, 6000, 8)]
+          (4100, 264, 4200, 8), (4353, 136, 4104, 8), (33, 4224, 100, 128), (1100, 1032, 1000, 8), (20, 40, 6000, 8),
+          (1, 12288, 40, 128), (1, 16384, 20, 2), (1, 16512, 20, 128), (4, 4096, 50, 4), (5, 4096, 50, 16), (16, 1024, 33, 32),
+          (16, 1032, 33, 8), (3, 24, 3, 1)]
 
 
 @pytest.mark.parametrize("y_dtype", [hdq.DTYPE_BF16, hdq.DTYPE_F32])
@@ -140,8 +142,8 @@ def test_linear_writes_its_output_only(M, K, N, y_dtype):
     pad = 4096
     buf = torch.full((M * N + 2 * pad,), -7.0, dtype=dt, device=DEV)
     y = buf[pad:pad + M * N].view(M, N)
-    ws = torch.full((hdq.fp8_linear_workspace_bytes(M, K, N, y_dtype) + 512,), 77, dtype=torch.uint8, device=DEV)
-    n = ws.numel() - 512
+    n = hdq.fp8_linear_workspace_bytes(M, K, N, y_dtype)
+    ws = torch.full((n + 512,), 77, dtype=torch.uint8, device=DEV)
     hdq.fp8_linear(x, wq, y=y, y_dtype=y_dtype, ws=ws[:n])
     assert torch.equal(y, hdq.fp8_linear(None, wq, xq=xq, y_dtype=y_dtype))
     assert bool((buf[:pad] == -7).all()) and bool((buf[pad + M * N:] == -7).all()) and bool((ws[n:] == 77).all())
