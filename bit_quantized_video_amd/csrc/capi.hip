@@ -557,6 +557,8 @@ static_assert(HDQ_FP8_ROWS == kFp8Rows && HDQ_FP8_BLOCKS == kFp8Blocks, "the hea
 static int64_t fp8_kb(int64_t cols) { return (cols + 127) / 128; }
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Rows of a tensor: the kernels round them up to whole tiles in 32 bits.
+static bool fp8_rows_ok(int64_t rows) { return rows > 0 && rows <= HDQ_FP8_MAX_ROWS; }
 // cols of a tensor the quantizers and GEMMs take.
 static bool fp8_cols_ok(int64_t cols) { return cols > 0 && cols <= HDQ_FP8_MAX_COLS && cols % 8 == 0; }
 
@@ -571,7 +573,7 @@ static int check_fp8_tensor(const hdq_fp8_tensor& t, int32_t layout, int64_t row
 int hdq_fp8_quantize(const void* x, int64_t rows, int64_t cols, int32_t had_block, int32_t layout,
                      hdq_fp8_tensor* out, void* stream) {
   if (x == nullptr || out == nullptr || (layout != HDQ_FP8_ROWS && layout != HDQ_FP8_BLOCKS)) return HDQ_ERR_INVALID;
-  if (rows <= 0 || rows > 0x7fffffff || !fp8_cols_ok(cols) || !aligned16(x)) return HDQ_ERR_SHAPE;
+  if (!fp8_rows_ok(rows) || !fp8_cols_ok(cols) || !aligned16(x)) return HDQ_ERR_SHAPE;
   hdq_fp8_tensor t = *out;
   t.layout = layout;
   t.had_block = had_block;
@@ -585,7 +587,7 @@ int hdq_fp8_quantize(const void* x, int64_t rows, int64_t cols, int32_t had_bloc
 }
 
 size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y_dtype) {
-  if (M <= 0 || N <= 0 || M > 0x7fffffff || N > 0x7fffffff || !fp8_cols_ok(K)) return 0;
+  if (!fp8_rows_ok(M) || !fp8_rows_ok(N) || !fp8_cols_ok(K)) return 0;
   if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return 0;
   const size_t kb = (size_t)fp8_kb(K);
   if (gemm_fp8_quantizes(M, (int64_t)kb)) return 0;
@@ -597,7 +599,7 @@ int hdq_fp8_linear(const void* x, const hdq_fp8_tensor* xq, int64_t M, int64_t K
   if (w == nullptr || y == nullptr || (x == nullptr && xq == nullptr)) return HDQ_ERR_INVALID;
   if (y_dtype != HDQ_DTYPE_F32 && y_dtype != HDQ_DTYPE_BF16) return HDQ_ERR_UNSUPPORTED;
   const int64_t N = w->rows;
-  if (M <= 0 || M > 0x7fffffff || N <= 0 || N > 0x7fffffff || !fp8_cols_ok(K)) return HDQ_ERR_SHAPE;
+  if (!fp8_rows_ok(M) || !fp8_rows_ok(N) || !fp8_cols_ok(K)) return HDQ_ERR_SHAPE;
   int st;
   if ((st = check_fp8_tensor(*w, HDQ_FP8_BLOCKS, N, K)) != HDQ_OK) return st;
   if (!aligned16(y)) return HDQ_ERR_SHAPE;
@@ -636,7 +638,7 @@ static_assert(HDQ_GROUP_NORM_MAX_CHANNELS == kGnMaxChannels, "the header's limit
 
 static bool gn_shape_ok(int64_t n, int64_t length, int64_t channels, int32_t groups) {
   return n > 0 && length > 0 && channels > 0 && channels <= HDQ_GROUP_NORM_MAX_CHANNELS && groups > 0 &&
-         channels % groups == 0 && n <= 0x7fffffff && length <= 0x7fffffff && n * length <= 0x7fffffff;
+         channels % groups == 0 && n <= HDQ_FP8_MAX_ROWS && length <= HDQ_FP8_MAX_ROWS && n * length <= HDQ_FP8_MAX_ROWS;
 }
 
 // The checks both group norms share; fills `g`.

@@ -43,20 +43,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_fp8_few(const uint8_t* __restric
   };
   auto load_w = [&](Block& b, int k) {
     const int64_t o = (int64_t)k * kFp8Block;
-    b.w.lo = *reinterpret_cast<const v4i*>(wp + o);
-    b.w.hi = *reinterpret_cast<const v4i*>(wp + o + 64);
+    b.w = load_frag(wp + o, wp + o + 64);
     b.s = wsp[k];
   };
   auto load_x = [&](Block& b, int k) {
     if constexpr (HB > 0) {
       const uint8_t* p = xcodes + (m * kb + k) * kFp8Block + 16 * q;
-      b.x.lo = *reinterpret_cast<const v4i*>(p);
-      b.x.hi = *reinterpret_cast<const v4i*>(p + 64);
+      b.x = load_frag(p, p + 64);
       b.s *= xscale[m * kb + k];
     } else {
       const int64_t o = (int64_t)k * kFp8Block;
-      b.x.lo = *reinterpret_cast<const v4i*>(xp + o);
-      b.x.hi = *reinterpret_cast<const v4i*>(xp + o + 64);
+      b.x = load_frag(xp + o, xp + o + 64);
       b.s *= xs[(int64_t)k * M + m];
     }
   };
@@ -215,10 +212,7 @@ __global__ __launch_bounds__(256 * KW * (PROD ? 2 : 1)) void k_fp8_deep(const ui
   const ConstFloats wsp = (ConstFloats)(uintptr_t)ws + (int64_t)nb * kb;
 
   auto frag = [&](const uint8_t* rows, int r) {
-    Fp8Frag f;
-    f.lo = *reinterpret_cast<const v4i*>(rows + r * 128 + 16 * (q ^ (r & 7)));
-    f.hi = *reinterpret_cast<const v4i*>(rows + r * 128 + 16 * ((q + 4) ^ (r & 7)));
-    return f;
+    return load_frag(rows + r * 128 + 16 * (q ^ (r & 7)), rows + r * 128 + 16 * ((q + 4) ^ (r & 7)));
   };
   auto compute = [&](int buf, float sw) {
     const uint8_t* lx = smem + buf * Tile::STAGE + kw * Tile::BLOCK;
@@ -360,6 +354,8 @@ static hipError_t launch_pipe(const uint8_t* xc, const float* xs, const uint8_t*
 //    (226, 5760 x 1920: 90 tiles); with 495 (1350, 5760 x 1920) 33.8 / 21.3.
 //  * from 256 tiles of 256 x 256 on: 128 x 128 tiles 30.3, 256 x 256 tiles 25.5
 //    (17550, 1536 x 512: 414 tiles); with 138 (1350, 5760 x 1920) 21.3 / 29.1.
+//    fp32 output, from 400 on: 155.9 / 152.6 (17776, 1920 x 1920: 560 tiles); with
+//    368 (4050, 5760 x 1920) 98.5 / 103.9.
 template <int OUT>
 static hipError_t launch_fp8_out(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
                                  int64_t M, int64_t N, int64_t kb, hipStream_t s) {
@@ -367,7 +363,7 @@ static hipError_t launch_fp8_out(const uint8_t* xc, const float* xs, const uint8
   if (M <= 16) return launch_few<OUT, 0>(xc, xs, nullptr, 0, wc, ws, y, M, N, kb, s);
   if (tiles(64, 64) < 192) return launch_deep<OUT, 1, 2, 4, 3, false>(xc, xs, wc, ws, y, M, N, kb, s);
   if (tiles(128, 128) < 300) return launch_deep<OUT, 2, 2, 1, 4, true>(xc, xs, wc, ws, y, M, N, kb, s);
-  if (tiles(256, 256) < 256) return launch_pipe<OUT, 4, 4, 4>(xc, xs, wc, ws, y, M, N, kb, 512, s);
+  if (tiles(256, 256) < (OUT == kOutBf16 ? 256 : 400)) return launch_pipe<OUT, 4, 4, 4>(xc, xs, wc, ws, y, M, N, kb, 512, s);
   return launch_pipe<OUT, 8, 8, 4>(xc, xs, wc, ws, y, M, N, kb, 256, s);
 }
 

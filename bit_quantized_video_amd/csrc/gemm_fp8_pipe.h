@@ -35,12 +35,12 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
   constexpr int BM = Tile::BM, BN = Tile::BN, XB = Tile::XB, SB = Tile::STAGE, kOutPitch = Tile::OUT_PITCH;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % 2, wn = wave / 2;
   // The tile's loads are issued by LOADERS waves; a wave is held up while it
   // issues, so with two waves of a workgroup on a SIMD one of them issues none.
   constexpr int LOADERS = WAVES > 4 ? WAVES / 2 : WAVES;
-  const bool loader = __builtin_amdgcn_readfirstlane(wave) < LOADERS;
+  const bool loader = wave < LOADERS;
   const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (N + BN - 1) / BN;
   const TileSeq seq = tile_seq(tiles_m * tiles_n);
   const int G = seq.count * kb;
@@ -98,10 +98,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
   zero_acc();
   const int r16 = lane & 15, q = lane >> 4;
   auto frag = [&](const uint8_t* rows, int r) {
-    Fp8Frag f;
-    f.lo = *reinterpret_cast<const v4i*>(rows + r * 128 + 16 * (q ^ (r & 7)));
-    f.hi = *reinterpret_cast<const v4i*>(rows + r * 128 + 16 * ((q + 4) ^ (r & 7)));
-    return f;
+    return load_frag(rows + r * 128 + 16 * (q ^ (r & 7)), rows + r * 128 + 16 * ((q + 4) ^ (r & 7)));
   };
   auto compute = [&](int buf, float sw) {
     const uint8_t* lx = smem + buf * SB;
@@ -114,7 +111,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
     // the scaling and adding of product t - LAG, so its readers are always LAG
     // matrix instructions behind it, and token fragment i + 2 is read when
     // fragment i's last product has been issued.
-    constexpr int LAG = 3;
+    constexpr int LAG = FAST ? 3 : 1;  // a product is one matrix instruction, or four in a chain
     Fp8Frag x[2];
     v4f p[LAG + 1];
     float sx[3];  // fragment i's activation scales in sx[i % 3]
@@ -211,7 +208,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
   auto open_scales = [&]() {
     int tm, tn;
     grouped_tile(clogical, tiles_m, tiles_n, tm, tn);
-    const int nb = min(__builtin_amdgcn_readfirstlane((tn * BN + wn * 16 * WN_T) / kFp8Block), nblocks - 1);
+    const int nb = min((tn * BN + wn * 16 * WN_T) / kFp8Block, nblocks - 1);
     wsp = (ConstFloats)(uintptr_t)ws + (int64_t)nb * kb;
   };
   open_scales();

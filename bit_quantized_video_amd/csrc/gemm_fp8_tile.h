@@ -29,13 +29,11 @@ namespace hdq {
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-// A fragment's two 16-byte pieces.
-struct Fp8Frag {
-  v4i lo, hi;
-};
-
-__device__ __forceinline__ v8i frag_bits(const Fp8Frag& f) {
-  return v8i{f.lo[0], f.lo[1], f.lo[2], f.lo[3], f.hi[0], f.hi[1], f.hi[2], f.hi[3]};
+// A fragment from its two 16-byte pieces.
+typedef v8i Fp8Frag;
+__device__ __forceinline__ Fp8Frag load_frag(const uint8_t* lo, const uint8_t* hi) {
+  return __builtin_shufflevector(*reinterpret_cast<const v4i*>(lo), *reinterpret_cast<const v4i*>(hi), 0, 1, 2, 3, 4,
+                                 5, 6, 7);
 }
 
 // Eight E4M3 codes (two words) to bf16, exact.
@@ -53,16 +51,14 @@ struct Fp8Operand;
 template <>
 struct Fp8Operand<true> {
   v8i v;
-  __device__ __forceinline__ void set(const Fp8Frag& f) { v = frag_bits(f); }
+  __device__ __forceinline__ void set(const Fp8Frag& f) { v = f; }
 };
 template <>
 struct Fp8Operand<false> {
   v8bf v[4];
   __device__ __forceinline__ void set(const Fp8Frag& f) {
-    v[0] = codes_to_bf16(f.lo[0], f.lo[1]);
-    v[1] = codes_to_bf16(f.lo[2], f.lo[3]);
-    v[2] = codes_to_bf16(f.hi[0], f.hi[1]);
-    v[3] = codes_to_bf16(f.hi[2], f.hi[3]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = codes_to_bf16(f[2 * t], f[2 * t + 1]);
   }
 };
 

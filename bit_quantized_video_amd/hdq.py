@@ -29,7 +29,7 @@ OP_SELECT, OP_QUANTIZE, OP_LINEAR, OP_SELECT_Q8, OP_DQ_QUANTIZE, OP_DQ_LINEAR = 
 # FP8 scale layouts: per 128 elements of a row, per 128 x 128 block
 FP8_ROWS, FP8_BLOCKS = 0, 1
 FP8_BLOCK = 128
-FP8_MAX_COLS = 1 << 22       # HDQ_FP8_MAX_COLS
+FP8_MAX_COLS, FP8_MAX_ROWS = 1 << 22, 0x7ffffc00   # HDQ_FP8_MAX_*
 # activations of the group norms
 ACT_NONE, ACT_SILU = 0, 1
 GROUP_NORM_MAX_CHANNELS = 8192   # HDQ_GROUP_NORM_MAX_CHANNELS
@@ -560,6 +560,8 @@ def _launch(dev, stream, call):
     """call(raw stream) with `dev` the current device and `stream` (None: the
     device's current stream) the current stream, so that what the call
     allocates belongs to the stream its kernels run on."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}, not on a GPU")
     if stream is None:
         if dev.index == torch.cuda.current_device():
             return call(torch._C._cuda_getCurrentRawStream(dev.index))
@@ -577,6 +579,21 @@ def _operand(t, name, dtype, shape, dev):
         raise ValueError(f"{name}: expected a contiguous {dtype} {shape} tensor on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t
+
+
+def _scratch(ws, nbytes, dev):
+    """The caller's workspace if it is large enough, else a new one, or None
+    where none is needed: (tensor, pointer, bytes)."""
+    if nbytes == 0:
+        return None, None, 0
+    if ws is not None:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: expected a contiguous tensor on {dev}")
+        size = ws.numel() * ws.element_size()
+        if size >= nbytes:
+            return ws, ws.data_ptr(), size
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws, ws.data_ptr(), nbytes
 
 
 class Fp8Tensor:
@@ -655,9 +672,8 @@ def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
         out = torch.empty((M, N), dtype=dt, device=dev) if y is None else y
         wd = w.desc()
         if xq is None:
-            scratch = _workspace(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype), dev)
-            st = lib.hdq_fp8_linear(x.data_ptr(), None, M, K, _c.byref(wd), out.data_ptr(), y_dtype, _ptr(scratch),
-                                    0 if scratch is None else scratch.numel(), s)
+            _keep, wp, wn = _scratch(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype), dev)
+            st = lib.hdq_fp8_linear(x.data_ptr(), None, M, K, _c.byref(wd), out.data_ptr(), y_dtype, wp, wn, s)
         else:
             xd = xq.desc()
             st = lib.hdq_fp8_linear(None, _c.byref(xd), M, K, _c.byref(wd), out.data_ptr(), y_dtype, None, 0, s)
@@ -702,9 +718,8 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None
 
     def call(s):
         out = torch.empty(x.shape, dtype=dt, device=dev) if y is None else y
-        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 0), dev)
-        st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, out.data_ptr(), yt,
-                                _ptr(scratch), 0 if scratch is None else scratch.numel(), s)
+        _keep, sp, sn = _scratch(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 0), dev)
+        st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, out.data_ptr(), yt, sp, sn, s)
         _check("hdq_group_norm", st)
         return out
     return _launch(dev, stream, call)
@@ -721,10 +736,10 @@ def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, ha
 
     def call(s):
         q = Fp8Tensor(n * length, C, had_block, FP8_ROWS, dev) if out is None else out
-        scratch = _workspace(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 1), dev)
+        _keep, sp, sn = _scratch(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 1), dev)
         d = q.desc()
         st = lib.hdq_group_norm_fp8(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, had_block, _c.byref(d),
-                                    _ptr(scratch), 0 if scratch is None else scratch.numel(), s)
+                                    sp, sn, s)
         _check("hdq_group_norm_fp8", st)
         q.had_block = had_block
         return q

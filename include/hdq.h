@@ -530,6 +530,7 @@ int hdq_dq_linear(const hdq_dq_grid *g, const uint8_t *core_codes, const void *c
 #define HDQ_FP8_ROWS 0
 #define HDQ_FP8_BLOCKS 1
 #define HDQ_FP8_MAX_COLS (1 << 22)
+#define HDQ_FP8_MAX_ROWS 0x7ffffc00
 typedef struct hdq_fp8_tensor {
   int32_t layout;    /* HDQ_FP8_*                                     */
   int32_t had_block; /* Hadamard block the rows were rotated with     */
@@ -542,7 +543,8 @@ typedef struct hdq_fp8_tensor {
 /*
  * hdq_fp8_quantize -- rotation fused with FP8 quantization.
  *   x        : device bf16 [rows, cols], 16-byte aligned; cols a multiple of
- *              8 and of had_block, at most HDQ_FP8_MAX_COLS.
+ *              8 and of had_block, at most HDQ_FP8_MAX_COLS; rows at most
+ *              HDQ_FP8_MAX_ROWS.
  *   had_block: power of two in [1, 128]; 1 rotates nothing.
  *   out      : host struct with caller-allocated codes and scale; layout,
  *              had_block, rows, cols are written.
@@ -562,14 +564,15 @@ size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y
  *   xq      : NULL, or the activations as HDQ_FP8_ROWS [M, K] with the
  *             weights' had_block.
  *   w       : HDQ_FP8_BLOCKS [N, K].  K as hdq_fp8_quantize's cols; M and N
- *             any size.
+ *             any size up to HDQ_FP8_MAX_ROWS.
  *   y       : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32.
  *   ws      : device scratch, 256-byte aligned, ws_bytes >=
  *             hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype) unless xq is
  *             given.  Nothing in it needs a value before the call; calls that
  *             may overlap need their own.
  * y = sum over 128-blocks b of sx[b, m] sw[n / 128, b] sum_{k in b} cx cw, each
- * scale pair and block sum combined in float32.  With a bf16 output the block
+ * scale pair and block sum combined in float32 (scale pairs whose product is
+ * outside its range are outside the layer's).  With a bf16 output the block
  * sums run on the FP8 matrix instructions, whose products are aligned to the
  * largest one of an instruction (at least 14 fraction bits: about 1.3e-5 of
  * the result in the 2-norm, where rounding to bf16 costs 1.7e-3); with an fp32
@@ -599,7 +602,7 @@ size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channel
  *   x, y        : device [n, length, channels], 16-byte aligned, each
  *                 HDQ_DTYPE_BF16 or HDQ_DTYPE_F32; y may be x (same type).
  *   groups      : divides channels (at most HDQ_GROUP_NORM_MAX_CHANNELS);
- *                 n * length < 2^31.
+ *                 n * length at most HDQ_FP8_MAX_ROWS.
  *   weight, bias: device fp32 [channels], or NULL for 1 and 0.
  *   eps         : >= 0.
  *   ws, ws_bytes: device scratch, 256-byte aligned, >=

@@ -34,7 +34,7 @@ def test_quantize_refusals(hdq):
     assert q(layout=2) == hdq.ERR_INVALID and q(layout=-1) == hdq.ERR_INVALID
     assert q(codes=None) == hdq.ERR_INVALID and q(scale=None) == hdq.ERR_INVALID
     assert hdq.lib.hdq_fp8_quantize(FAKE, 4, 64, 16, 0, None, None) == hdq.ERR_INVALID
-    for kw in (dict(rows=0), dict(rows=-1), dict(rows=1 << 31), dict(cols=0), dict(cols=60), dict(cols=72),
+    for kw in (dict(rows=0), dict(rows=-1), dict(rows=hdq.FP8_MAX_ROWS + 1), dict(cols=0), dict(cols=60), dict(cols=72),
                dict(hb=0), dict(hb=12), dict(hb=256), dict(cols=hdq.FP8_MAX_COLS + 128), dict(x=FAKE + 2),
                dict(codes=FAKE + 8), dict(scale=FAKE + 2)):
         assert q(**kw) == hdq.ERR_SHAPE, kw
@@ -53,10 +53,10 @@ def test_linear_refusals(hdq):
                                 ws, wsb, None)
     assert lin(w=None) == hdq.ERR_INVALID and lin(y=None) == hdq.ERR_INVALID and lin(x=None) == hdq.ERR_INVALID
     assert lin(dt=2) == hdq.ERR_UNSUPPORTED and lin(dt=7) == hdq.ERR_UNSUPPORTED
-    for kw in (dict(M=0), dict(M=1 << 31), dict(K=0), dict(K=504), dict(K=256), dict(x=FAKE + 2), dict(y=FAKE + 4)):
+    for kw in (dict(M=0), dict(M=hdq.FP8_MAX_ROWS + 1), dict(K=0), dict(K=504), dict(K=256), dict(x=FAKE + 2), dict(y=FAKE + 4)):
         assert lin(**kw) == hdq.ERR_SHAPE, kw
     assert lin(w=dict(ok_w, layout=0)) == hdq.ERR_UNSUPPORTED
-    assert lin(w=dict(ok_w, rows=0)) == hdq.ERR_SHAPE
+    assert lin(w=dict(ok_w, rows=0)) == hdq.ERR_SHAPE and lin(w=dict(ok_w, rows=hdq.FP8_MAX_ROWS + 1)) == hdq.ERR_SHAPE
     assert lin(w=dict(ok_w, hb=3)) == hdq.ERR_SHAPE
     assert lin(w=dict(ok_w, codes=None)) == hdq.ERR_INVALID and lin(w=dict(ok_w, scale=None)) == hdq.ERR_INVALID
     assert lin(w=dict(ok_w, codes=FAKE + 4)) == hdq.ERR_SHAPE
@@ -79,9 +79,26 @@ def test_binding_refusals(hdq):
         hdq.Fp8Tensor(4, 300, codes=torch.zeros(4, 384, dtype=torch.uint8), scale=torch.zeros(4, 3))  # [kb, rows]
     with pytest.raises(ValueError):
         hdq.fp8_quantize(torch.zeros(4, 128, dtype=torch.bfloat16), 1)                # not on a GPU
+    with pytest.raises(ValueError):                                                   # codes in host memory
+        hdq.fp8_linear(None, hdq.Fp8Tensor(16, 128, 1, hdq.FP8_BLOCKS, "cpu"), xq=hdq.Fp8Tensor(4, 128, 1, device="cpu"))
     t = hdq.Fp8Tensor(130, 300, 4, hdq.FP8_BLOCKS, "cpu")
     assert t.codes.shape == (130, 384) and t.scale.shape == (2, 3)
     assert hdq.Fp8Tensor(130, 300, 4, hdq.FP8_ROWS, "cpu").scale.shape == (3, 130)
+
+
+def test_binding_scratch(hdq):
+    """A caller's workspace is used when it fits and refused when it is strided."""
+    dev = torch.device("cpu")
+    assert hdq._scratch(None, 0, dev) == (None, None, 0)
+    ws = torch.zeros(100, dtype=torch.int32)
+    t, p, n = hdq._scratch(ws, 400, dev)
+    assert t is ws and p == ws.data_ptr() and n == 400
+    t, p, n = hdq._scratch(ws, 401, dev)
+    assert t is not ws and n == 401 and t.numel() == 401
+    with pytest.raises(ValueError):
+        hdq._scratch(torch.zeros(100, 2, dtype=torch.uint8)[:, 0], 10, dev)
+    with pytest.raises(ValueError):
+        hdq._scratch(ws, 10, torch.device("meta"))
 
 
 def test_struct_matches_header(hdq, tmp_path):
