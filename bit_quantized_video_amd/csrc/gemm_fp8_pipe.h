@@ -160,7 +160,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
       uint8_t* const stage = smem + buf * SB;
       uint16_t* y16 = static_cast<uint16_t*>(Y);
       const int n = n0 + 8 * (tid % PIECES);
-      const bool vec = n + 8 <= N && (N & 7) == 0;
+      const bool vec = n + 8 <= N;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         lds_only_barrier();
@@ -181,7 +181,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
           if (m < M) {
             uint16_t* dst = y16 + m * N + n;
             if (vec) {
-              store16_nt(dst, src);
+              __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(src), reinterpret_cast<i32x4_a2*>(dst));
             } else {
               for (int e = 0; e < 8 && n + e < N; ++e) dst[e] = reinterpret_cast<const uint16_t*>(src)[e];
             }
