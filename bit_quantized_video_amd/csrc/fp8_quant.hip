@@ -3,7 +3,10 @@
 //
 // Per block of 128 (of a row, or 128 x 128): a = max|y|, s = a / 448,
 // code = E4M3(y * (448 / a)).  Bound by HBM: 2 bytes read and 1 + 4/128
-// written per element (rows), 2 and 1 (blocks).
+// written per element (rows), 2 and 1 (blocks); one pass over the data, since
+// a block's maximum is known within a quad of lanes or a workgroup.  Measured:
+// rows 17776 x 12288, rotated by 128, 135 us (4.9 TB/s, what a large copy
+// reaches); 226 x 1000 3.3 us (the launch); blocks 5760 x 1920 7.7 us.
 #include "fp8_device.h"
 #include "hdq_internal.h"
 

@@ -10,7 +10,8 @@ namespace hdq {
 // blocks of K in turn (wave w: w, w + WAVES, ...), each reading its weight
 // fragments from global memory straight into registers one block ahead, and
 // the partial tiles are added over LDS in a fixed order.  Bound by the weights'
-// bytes, and for small layers by the launch.
+// bytes, and for small layers by the launch: one token, 3072 -> 12288 8.4 us (4.5
+// TB/s), 12288 -> 3072 9.4, 1920 -> 5760 4.5 from codes and 5.6 from bf16.
 //
 // HB > 0: the activations come as bf16 and the workgroup quantizes them itself
 // (rotation block HB), into LDS, while its first weights are on their way: the
@@ -152,7 +153,9 @@ hipError_t launch_gemm_fp8_bf16(const uint16_t* x, int64_t K, int hb, const uint
 // filled by LDS-DMA STAGES - 1 stages ahead: with few workgroups a stage's
 // arithmetic is much shorter than its loads' latency.  PROD: waves of their own
 // issue the loads (a wave is held up while it issues; 5-15% faster with one
-// group).  The groups' partial tiles are added over LDS in a fixed order.
+// group).  The groups' partial tiles are added over LDS in a fixed order.  Bound
+// by the latency of a stage (load, barrier, fragment reads): 226 x 4096 -> 1920
+// 8.3 us (direct loads without LDS 25.5), 1350 x 1920 -> 1024 10.0.
 template <int WM_T, int WN_T, int KW, int STAGES, bool PROD>
 struct Fp8Deep {
   static constexpr int BM = 32 * WM_T, BN = 32 * WN_T, THREADS = 256 * KW * (PROD ? 2 : 1);

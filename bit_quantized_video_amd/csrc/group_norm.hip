@@ -8,11 +8,13 @@
 //
 // Bound by HBM: x has to be read for the statistics before the first output,
 // and again unless it is kept.  Three ways, by the size of a sample's slab (the
-// channels of a few groups, see gn_slab): a slab that fits a workgroup's
+// channels of a few groups, see gn_plan): a slab that fits a workgroup's
 // registers is read once, normalized and written in one launch; a slab that one
 // workgroup can still stream takes one launch for the statistics and one for
 // the normalization; else partial statistics per chunk of rows, their join and
-// the normalization.
+// the normalization.  Measured: 691200 x 256 bf16 with SiLU 176 us (4.0 TB/s of
+// bytes read and written once, where a large copy reaches 4.8), 13 x 1350 x 512
+// 17 us (9 + 8), 2 x 77 x 300 fp32 5.5 us (one launch's latency).
 //
 // Statistics: a thread takes up to 16 rows at a time into registers, sums each
 // channel's values (relative to the first) and then the squared deviations from
