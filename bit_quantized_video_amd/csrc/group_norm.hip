@@ -33,6 +33,8 @@ namespace hdq {
 constexpr int kGnThreads = 512, kGnSlabThreads = 512;
 // a slab's pairs (one per thread and channel of its vector) and groups
 constexpr int kGnSlabLds = kGnSlabThreads * 8 * 8 + 8 * 8192;
+// a short sample's pairs, groups and coefficients (at most 512 channels)
+constexpr int kGnShortLds = (kGnThreads * 8 + 512 + 2) * 8 + 3 * 512 * 4;
 
 // NT: 16-byte stores that do not stay in the caches.
 template <typename T, int V, bool NT = false>
@@ -458,6 +460,29 @@ __global__ __launch_bounds__(T) void k_gn_slab(const TI* x, int64_t length, int 
   }
 }
 
+// Rotates and codes one 8-channel chunk (of block b; in: within the channels) of
+// a row held by 16 lanes, and stores it.
+__device__ __forceinline__ void gn_code_chunk(float (&y)[8], bool in, int lane, int hb, float c_b,
+                                              uint8_t* __restrict__ codes, float* __restrict__ scale, int64_t row,
+                                              int b, int chunk, int kb, int64_t total_rows) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = in ? y[e] : 0.0f;
+  if (hb > 1) {
+    const float sc = fwht8(y, lane, hb) * c_b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = y[e] * sc;
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(y[e]));
+  float s, inv;
+  fp8_scales(row16_max(m), s, inv);
+  // lanes past the channels (whole Hadamard blocks) hold rotated zeros of either sign
+  *reinterpret_cast<uint2*>(codes + row * ((int64_t)kb * kFp8Block) + b * kFp8Block + 8 * chunk) =
+      fp8_encode8(y, in ? inv : 0.0f);
+  if ((lane & 15) == 0) scale[(int64_t)b * total_rows + row] = s;
+}
+
 // The normalization to FP8 codes: a wave owns one block of 128 channels of four
 // rows at a time, a lane one 8-channel chunk (the one the rotation's lane
 // numbering gives it), whose coefficients it keeps over the rows of its chunk.
@@ -503,24 +528,82 @@ __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, 
         float y[8];
         q[u].get(y);
         gn_normalize<8>(y, mean, a, bs, act);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = in ? y[e] : 0.0f;
-        if constexpr (HB > 1) {
-          const float sc = fwht8(y, lane, HB) * c_b;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * sc;
-        }
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(y[e]));
-        float s, inv;
-        fp8_scales(row16_max(m), s, inv);
-        const int64_t row = row0 + r + 4 * u;
-        // lanes past the channels (whole Hadamard blocks) hold rotated zeros of either sign
-        *reinterpret_cast<uint2*>(codes + row * ((int64_t)kb * kFp8Block) + b * kFp8Block + 8 * chunk) =
-            fp8_encode8(y, in ? inv : 0.0f);
-        if (l16 == 0) scale[(int64_t)b * total_rows + row] = s;
+        gn_code_chunk(y, in, lane, HB, c_b, codes, scale, row0 + r + 4 * u, b, chunk, kb, total_rows);
       }
+  }
+}
+
+// Short samples to FP8 codes in one launch: a workgroup codes 16 rows, and works
+// out the whole sample's statistics by itself first (so do the sample's other
+// workgroups: a short sample's rows come from L2, and a launch, its workspace
+// and its wait cost more).
+template <typename TI, int V, bool MERGE>
+__global__ __launch_bounds__(kGnThreads) void k_gn_short_fp8(const TI* __restrict__ x, int length, int C, int groups,
+                                                             int chunks, float eps, const float* __restrict__ weight,
+                                                             const float* __restrict__ bias, int act, int hb,
+                                                             float c_b, int kb, int64_t total_rows,
+                                                             uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  extern __shared__ float2 pair_s[];  // [rpar][C or cv], then one (mean, rstd) per group
+  const int64_t sample = blockIdx.x / (unsigned)chunks;
+  const int r0 = (int)(blockIdx.x % (unsigned)chunks) * 16;
+  const int cv = C / V, rpar = kGnThreads / cv, cg = C / groups;
+  const TI* xs = x + sample * length * C;
+  float2* const stat_s = pair_s + ((rpar * (MERGE ? cv : C) + 1) & ~1);
+  auto slot_rows = [&](int r) { return r < length ? (length - r + rpar - 1) / rpar : 0; };
+  {
+    const int pr = (int)threadIdx.x / cv, c = (int)threadIdx.x - pr * cv;
+    GnSums<V> t;
+    t.clear();
+    if (pr < rpar) {
+      gn_stream<TI, V>(xs + (int64_t)pr * C + c * V, (int64_t)rpar * C, slot_rows(pr), t);
+      gn_put<MERGE, V>(pair_s, t, pr, c, cv);
+    }
+  }
+  __syncthreads();
+  const int P = gn_lanes(groups, kGnThreads);
+  for (int g0 = 0; g0 < groups; g0 += kGnThreads / P) {
+    const int g = g0 + (int)threadIdx.x / P;
+    if (g >= groups) continue;  // lane groups of P leave together
+    double n, mean, m2;
+    gn_join_group<MERGE, V>(pair_s, g, cg, cv, min(rpar, length), (int)threadIdx.x % P, P, slot_rows, n, mean, m2);
+    if (threadIdx.x % P == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, eps));
+  }
+  __syncthreads();
+  float* const coef_s = reinterpret_cast<float*>(stat_s + groups + (groups & 1));  // [3][C]
+  for (int ch = threadIdx.x; ch < C; ch += kGnThreads) {
+    const float2 st = stat_s[ch / cg];
+    gn_write_coef(coef_s, C, ch, st.x, st.y, weight, bias);
+  }
+  // a wave codes four rows of a block of 128 channels at a time, as
+  // k_gn_apply_fp8; the next four are loaded meanwhile
+  const int lane = threadIdx.x & 63, l16 = lane & 15, nl = fwht_lanes(hb);
+  const int chunk = (l16 & ~(nl - 1)) + fwht_chunk(lane, hb);
+  constexpr int kWaves = kGnThreads / 64;
+  auto load = [&](int u, GnRaw<TI, 8>& q) {
+    const int row = r0 + 4 * (u & 3) + (lane >> 4), ch = (u >> 2) * kFp8Block + 8 * chunk;
+    if (u < 4 * kb && row < length && ch < C) q.load(xs + (int64_t)row * C + ch);
+  };
+  GnRaw<TI, 8> next;
+  int u = (int)threadIdx.x >> 6;
+  load(u, next);
+  __syncthreads();
+  for (; u < 4 * kb; u += kWaves) {
+    const GnRaw<TI, 8> q = next;
+    load(u + kWaves, next);
+    const int b = u >> 2, row = r0 + 4 * (u & 3) + (lane >> 4);
+    if (row >= length) continue;  // 16 lanes stay together
+    const int ch = b * kFp8Block + 8 * chunk;
+    const bool in = ch < C;
+    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (in) {
+      float mean[8], a[8], bs[8];
+      gn_load_coef<8>(coef_s + ch, mean);
+      gn_load_coef<8>(coef_s + C + ch, a);
+      gn_load_coef<8>(coef_s + 2 * C + ch, bs);
+      q.get(y);
+      gn_normalize<8>(y, mean, a, bs, act);
+    }
+    gn_code_chunk(y, in, lane, hb, c_b, codes, scale, sample * length + row, b, chunk, kb, total_rows);
   }
 }
 
@@ -545,6 +628,8 @@ static int64_t gn_rpar(int64_t C, int64_t vec) {
 
 // How a call runs (a rule on its sizes alone; the workspace follows it).
 constexpr int64_t kGnKeep = 16, kGnStream = 64;  // rows a thread keeps / streams at most
+// k_gn_short_fp8: channels and elements of a sample at most
+constexpr int64_t kGnBriefChannels = 512, kGnBriefSample = 96 << 10;
 struct GnPlan {
   int64_t vec;
   bool merge;            // a vector lies in one group
@@ -552,6 +637,7 @@ struct GnPlan {
   int64_t threads, rows; // of a slab: threads, and rows per thread
   bool keep;             // the slab is kept in registers (not for the FP8 form)
   bool slab;             // the statistics are a slab's
+  bool brief;            // the FP8 form takes one launch
   int64_t chunks, rows_per;
 };
 
@@ -584,6 +670,10 @@ static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool
   // CU: with few of them the chunks' three launches are faster (1 x 16384 x 128:
   // 15.5 us against 47.0).
   p.slab = p.keep || (p.threads == 256 && p.rows <= kGnKeep) || (p.rows <= kGnStream && n * p.slabs >= 256);
+  // As long on the GPU as two launches (225 x 320: 10.4 us and 10.0; 64 x 512: 7.5
+  // and 8.3; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
+  // launch's host time and no workspace.
+  p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample;
   gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
   return p;
 }
@@ -598,7 +688,7 @@ size_t group_norm_ws_bytes(int64_t n, int64_t length, int64_t C, int64_t groups,
   size_t most = 0;
   for (const bool f32 : {false, true}) {
     const GnPlan p = gn_plan(n, length, C, groups, f32);
-    if (p.keep && !fp8) continue;
+    if (fp8 ? p.brief : p.keep) continue;
     const size_t b = gn_coef_bytes(n, C) + (p.slab ? 0 : gn_align((size_t)(n * p.chunks * groups) * sizeof(double2)));
     if (b > most) most = b;
   }
@@ -704,9 +794,35 @@ static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float* coef, uint8_
 }
 
 template <typename TI>
+static hipError_t gn_short_fp8(const GroupNormArgs& g, const GnPlan& p, int hb, uint8_t* codes, float* scale,
+                               hipStream_t s) {
+  const int64_t chunks = (g.length + 15) / 16;
+  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
+  return gn_dispatch<TI>(p, [&](auto v, auto merge) {
+    constexpr int V = decltype(v)::value;
+    constexpr bool MERGE = decltype(merge)::value;
+    if constexpr (V == 1 || (V == 4 && sizeof(TI) == 2)) {
+      return hipErrorInvalidValue;  // channels are a multiple of 8
+    } else {
+      // pairs, (mean, rstd) of the groups, coefficients; 16-byte aligned
+      const size_t pairs = (size_t)(kGnThreads / (g.C / V)) * (size_t)(MERGE ? g.C / V : g.C);
+      const size_t lds = (pairs + (pairs & 1) + (size_t)(g.groups + (g.groups & 1))) * sizeof(float2) + (size_t)g.C * 3 * sizeof(float);
+      const hipError_t e = set_dynamic_lds_once<&k_gn_short_fp8<TI, V, MERGE>>(kGnShortLds);
+      if (e != hipSuccess) return e;
+      k_gn_short_fp8<TI, V, MERGE><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(
+          static_cast<const TI*>(g.x), (int)g.length, (int)g.C, (int)g.groups, (int)chunks, g.eps, g.weight, g.bias,
+          g.act, hb, hadamard_scale(hb), (int)fp8_blocks(g.C), g.n * g.length, codes, scale);
+      return hipGetLastError();
+    }
+  });
+}
+
+template <typename TI>
 static hipError_t group_norm_fp8_t(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,
                                    hipStream_t s) {
-  const hipError_t e = gn_statistics<TI>(g, gn_plan(g.n, g.length, g.C, g.groups, g.x_f32), ws, s);
+  const GnPlan p = gn_plan(g.n, g.length, g.C, g.groups, g.x_f32);
+  if (p.brief) return gn_short_fp8<TI>(g, p, hb, codes, scale, s);
+  const hipError_t e = gn_statistics<TI>(g, p, ws, s);
   if (e != hipSuccess) return e;
   const float* coef = static_cast<const float*>(ws);
   switch (hb) {

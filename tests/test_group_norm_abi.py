@@ -21,7 +21,8 @@ def test_workspace(hdq):
                 (1 << 20, 1 << 20, 8, 2)):
         assert f(*bad) == 0, bad
     assert f(1, 1, 1, 1) == 0                            # one launch needs none
-    assert f(1, 1, 8, 1, True) >= 3 * 8 * 4              # coefficients of the two-launch FP8 form
+    assert f(1, 1, 8, 1, True) == 0 and f(1, 225, 320, 32, True) == 0
+    assert f(13, 1350, 512, 32, True) >= 13 * 3 * 512 * 4   # coefficients of the two-launch FP8 form
     assert f(1, 100000, 256, 32) >= 3 * 256 * 4 + 32 * 16
 
 
