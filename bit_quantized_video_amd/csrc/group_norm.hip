@@ -628,8 +628,8 @@ static int64_t gn_rpar(int64_t C, int64_t vec) {
 
 // How a call runs (a rule on its sizes alone; the workspace follows it).
 constexpr int64_t kGnKeep = 16, kGnStream = 64;  // rows a thread keeps / streams at most
-// k_gn_short_fp8: channels and elements of a sample at most
-constexpr int64_t kGnBriefChannels = 512, kGnBriefSample = 96 << 10;
+// k_gn_short_fp8: channels and elements of a sample at most, rows of a workgroup
+constexpr int64_t kGnBriefChannels = 512, kGnBriefSample = 96 << 10, kGnBriefRows = 16;
 struct GnPlan {
   int64_t vec;
   bool merge;            // a vector lies in one group
@@ -670,10 +670,13 @@ static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool
   // CU: with few of them the chunks' three launches are faster (1 x 16384 x 128:
   // 15.5 us against 47.0).
   p.slab = p.keep || (p.threads == 256 && p.rows <= kGnKeep) || (p.rows <= kGnStream && n * p.slabs >= 256);
-  // As long on the GPU as two launches (225 x 320: 10.4 us and 10.0; 64 x 512: 7.5
-  // and 8.3; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
-  // launch's host time and no workspace.
-  p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample;
+  // As long on the GPU as two launches (225 x 320: 10.4 us and 9.8; 64 x 512: 7.5
+  // and 8.2; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
+  // launch's host time and no workspace.  A sample's workgroups read it again
+  // each, so either it has one (1000 x 16 x 512: 26.2 and 49.8) or all run at a
+  // time (13 x 225 x 320: 12.0 and 10.6; 64 x 225 x 320, 960 of them: 42.6 and 15.9).
+  p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample &&
+            (length <= kGnBriefRows || n * ((length + kGnBriefRows - 1) / kGnBriefRows) <= 256);
   gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
   return p;
 }
@@ -796,7 +799,7 @@ static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float* coef, uint8_
 template <typename TI>
 static hipError_t gn_short_fp8(const GroupNormArgs& g, const GnPlan& p, int hb, uint8_t* codes, float* scale,
                                hipStream_t s) {
-  const int64_t chunks = (g.length + 15) / 16;
+  const int64_t chunks = (g.length + kGnBriefRows - 1) / kGnBriefRows;
   if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
   return gn_dispatch<TI>(p, [&](auto v, auto merge) {
     constexpr int V = decltype(v)::value;

@@ -141,7 +141,8 @@ def test_in_place_and_guard_bytes(n, L, C, G):
 FP8_SHAPES = [(1, 1, 8, 1, 8), (2, 5, 64, 8, 64), (1, 225, 320, 32, 64), (3, 37, 136, 17, 8), (1, 700, 1280, 32, 128),
               (13, 50, 512, 32, 128), (1, 3000, 64, 4, 1), (9, 2500, 512, 32, 16), (2, 18, 4104, 27, 2), (1, 5, 200, 5, 4),
               (1, 6, 160, 5, 32), (3, 170, 512, 32, 128), (2, 33, 504, 21, 8), (1, 1000, 40, 5, 4),
-              (7, 16, 256, 256, 64), (5, 17, 264, 8, 1)]
+              (7, 16, 256, 256, 64), (5, 17, 264, 8, 1),
+              (20, 225, 320, 32, 64), (300, 16, 128, 8, 128), (300, 17, 128, 8, 8), (1, 4097, 16, 4, 16)]
 
 
 @pytest.mark.parametrize("silu", [False, True])

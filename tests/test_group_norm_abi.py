@@ -22,6 +22,9 @@ def test_workspace(hdq):
         assert f(*bad) == 0, bad
     assert f(1, 1, 1, 1) == 0                            # one launch needs none
     assert f(1, 1, 8, 1, True) == 0 and f(1, 225, 320, 32, True) == 0
+    # with many samples of several workgroups each one launch would read them too often
+    assert f(64, 225, 320, 32, True) >= 64 * 3 * 320 * 4 and f(1, 12288, 8, 2, True) > 0
+    assert f(20000, 16, 512, 32, True) == 0
     assert f(13, 1350, 512, 32, True) >= 13 * 3 * 512 * 4   # coefficients of the two-launch FP8 form
     assert f(1, 100000, 256, 32) >= 3 * 256 * 4 + 32 * 16
 
