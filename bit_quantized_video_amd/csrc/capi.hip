@@ -655,7 +655,7 @@ static int check_group_norm(const void* x, int32_t x_dtype, int64_t n, int64_t l
   const size_t need = group_norm_ws_bytes(n, length, channels, groups, fp8);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return HDQ_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return HDQ_ERR_SHAPE;
-  g = GroupNormArgs{x, x_dtype == HDQ_DTYPE_F32, n, length, channels, groups, weight, bias, eps, act == HDQ_ACT_SILU};
+  g = GroupNormArgs{x, x_dtype == HDQ_DTYPE_F32, n, length, channels, groups, n * length, weight, bias, eps, act == HDQ_ACT_SILU};
   return HDQ_OK;
 }
 

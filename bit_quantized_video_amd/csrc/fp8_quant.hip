@@ -23,8 +23,9 @@ __global__ __launch_bounds__(256) void k_fp8_quant_rows(const uint16_t* __restri
                                                         float* __restrict__ scale) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int kgroups = (kb + 3) >> 2;
-  const int b = (int)(blockIdx.x % (unsigned)kgroups) * 4 + wave;
-  const int64_t row = (int64_t)(blockIdx.x / (unsigned)kgroups) * 16 + (lane >> 2);
+  const unsigned blk = wide_block();
+  const int b = (int)(blk % (unsigned)kgroups) * 4 + wave;
+  const int64_t row = (int64_t)(blk / (unsigned)kgroups) * 16 + (lane >> 2);
   if (b >= kb || row >= rows) return;  // whole quads leave together
   float y[32];
   const int part = lane & 3;
@@ -49,8 +50,10 @@ __global__ __launch_bounds__(512) void k_fp8_quant_blocks(const uint16_t* __rest
                                                           float* __restrict__ scale) {
   __shared__ float red[8];
   const int tid = threadIdx.x, lane = tid & 63, part = tid & 3;
-  const int b = (int)(blockIdx.x % (unsigned)kb);
-  const int64_t rb = blockIdx.x / (unsigned)kb, row = rb * kFp8Block + (tid >> 2);
+  const unsigned blk = wide_block();
+  const int b = (int)(blk % (unsigned)kb);
+  const int64_t rb = blk / (unsigned)kb, row = rb * kFp8Block + (tid >> 2);
+  if (rb * kFp8Block >= rows) return;
   float y[32];
   // rows past the end hold zeros (their quads take part in the maximum)
   const bool in = row < rows;
@@ -83,11 +86,11 @@ static hipError_t launch_fp8_quant_hb(const uint16_t* x, int64_t rows, int64_t c
   if (layout == kFp8Rows) {
     const int64_t grid = (rows + 15) / 16 * ((kb + 3) / 4);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    k_fp8_quant_rows<HB><<<dim3((unsigned)grid), dim3(256), 0, s>>>(x, rows, (int)cols, (int)kb, c_b, codes, scale);
+    k_fp8_quant_rows<HB><<<wide_grid(grid), dim3(256), 0, s>>>(x, rows, (int)cols, (int)kb, c_b, codes, scale);
   } else {
     const int64_t grid = fp8_blocks(rows) * kb;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    k_fp8_quant_blocks<HB><<<dim3((unsigned)grid), dim3(512), 0, s>>>(x, rows, (int)cols, (int)kb, c_b, codes, scale);
+    k_fp8_quant_blocks<HB><<<wide_grid(grid), dim3(512), 0, s>>>(x, rows, (int)cols, (int)kb, c_b, codes, scale);
   }
   return hipGetLastError();
 }

@@ -29,7 +29,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_fp8_few(const uint8_t* __restric
   __shared__ float xscale[XBLOCKS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = (int)wide_block() * 16;
+  if (n0 >= N) return;
   const int64_t ld = (int64_t)kb * kFp8Block;
   // rows past the end repeat the last one; their results are not stored
   const int m = min(r16, M - 1);
@@ -118,7 +119,7 @@ constexpr int kFewWaves = 8;
 template <int OUT, int HB>
 static hipError_t launch_few(const uint8_t* xc, const float* xs, const uint16_t* xb, int64_t K, const uint8_t* wc,
                              const float* ws, void* y, int64_t M, int64_t N, int64_t kb, hipStream_t s) {
-  k_fp8_few<OUT, kFewWaves, HB><<<dim3((unsigned)((N + 15) / 16)), dim3(64 * kFewWaves), 0, s>>>(
+  k_fp8_few<OUT, kFewWaves, HB><<<wide_grid((N + 15) / 16), dim3(64 * kFewWaves), 0, s>>>(
       xc, xs, xb, (int)K, HB > 0 ? hadamard_scale(HB) : 1.0f, wc, ws, y, (int)M, (int)N, (int)kb);
   return hipGetLastError();
 }

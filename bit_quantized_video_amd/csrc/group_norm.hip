@@ -26,6 +26,7 @@
 #include "fp8_device.h"
 #include "hdq_internal.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace hdq {
@@ -655,6 +656,7 @@ static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool
   p.slabs = (C + p.width - 1) / p.width;
   const int64_t cv = p.width / p.vec;
   // the fewest threads whose registers hold the slab: fewer pairs to join
+  p.threads = 0;
   p.rows = kGnStream + 1;
   for (const int64_t t : {(int64_t)256, (int64_t)kGnSlabThreads}) {
     if (cv > t) continue;
@@ -713,7 +715,6 @@ static hipError_t gn_dispatch(const GnPlan& p, F f) {
 
 template <typename TI, typename TO, int T, int ROWS>
 static hipError_t gn_launch_slab(const GroupNormArgs& g, const GnPlan& p, void* y, float* coef, hipStream_t s) {
-  if (g.n * p.slabs > 0x7fffffff) return hipErrorInvalidValue;
   return gn_dispatch<TI>(p, [&](auto v, auto merge) {
     constexpr int V = decltype(v)::value;
     constexpr bool MERGE = decltype(merge)::value;
@@ -737,7 +738,6 @@ static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* w
     return p.threads == 256 ? gn_launch_slab<TI, TI, 256, 0>(g, p, nullptr, coef, s)
                             : gn_launch_slab<TI, TI, kGnSlabThreads, 0>(g, p, nullptr, coef, s);
   double2* part = reinterpret_cast<double2*>(static_cast<uint8_t*>(ws) + gn_coef_bytes(g.n, g.C));
-  if (g.n * p.chunks > 0x7fffffff) return hipErrorInvalidValue;
   const hipError_t e = gn_dispatch<TI>(p, [&](auto v, auto merge) {
     constexpr int V = decltype(v)::value;
     constexpr bool MERGE = decltype(merge)::value;
@@ -748,7 +748,6 @@ static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* w
   });
   if (e != hipSuccess) return e;
   const int64_t total = g.n * g.groups;
-  if ((total + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
   k_gn_final<<<dim3((unsigned)((total + 3) / 4)), dim3(256), 0, s>>>(part, total, g.length, (int)(g.C / g.groups),
                                                                      (int)g.groups, (int)p.chunks, p.rows_per, g.eps,
                                                                      g.weight, g.bias, coef);
@@ -767,7 +766,6 @@ static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStr
   if (e != hipSuccess) return e;
   int64_t chunks, rows_per;
   gn_chunks(8192, g.n, g.length, 4 * gn_rpar(g.C, p.vec), chunks, rows_per);
-  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
   return gn_dispatch<TI>(p, [&](auto v, auto) {
     constexpr int V = decltype(v)::value;
     k_gn_apply<TI, TO, V><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), 0, s>>>(
@@ -777,9 +775,29 @@ static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStr
   });
 }
 
+// HIP takes fewer than 2^32 threads a launch: f(arguments, first sample) for
+// runs of samples of about equal number, whose grids stay near kWideRow
+// workgroups (a sample has at most ceil(C / 64) slabs then).  From 512 samples on
+// the plan does not depend on their number, so neither does the workspace's use.
+template <typename F>
+static hipError_t gn_runs(const GroupNormArgs& g, F f) {
+  const int64_t most = kWideRow / ((g.C + 63) / 64), runs = (g.n + most - 1) / most, step = (g.n + runs - 1) / runs;
+  for (int64_t n0 = 0; n0 < g.n; n0 += step) {
+    GroupNormArgs r = g;
+    r.x = static_cast<const uint8_t*>(g.x) + n0 * g.length * g.C * (g.x_f32 ? 4 : 2);
+    r.n = std::min(step, g.n - n0);
+    const hipError_t e = f(r, n0);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* ws, hipStream_t s) {
-  if (g.x_f32) return y_f32 ? group_norm_t<float, float>(g, y, ws, s) : group_norm_t<float, uint16_t>(g, y, ws, s);
-  return y_f32 ? group_norm_t<uint16_t, float>(g, y, ws, s) : group_norm_t<uint16_t, uint16_t>(g, y, ws, s);
+  return gn_runs(g, [&](const GroupNormArgs& r, int64_t n0) {
+    void* yr = static_cast<uint8_t*>(y) + n0 * g.length * g.C * (y_f32 ? 4 : 2);
+    if (r.x_f32) return y_f32 ? group_norm_t<float, float>(r, yr, ws, s) : group_norm_t<float, uint16_t>(r, yr, ws, s);
+    return y_f32 ? group_norm_t<uint16_t, float>(r, yr, ws, s) : group_norm_t<uint16_t, uint16_t>(r, yr, ws, s);
+  });
 }
 
 template <typename TI, int HB>
@@ -788,11 +806,12 @@ static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float* coef, uint8_
   const int64_t kb = fp8_blocks(g.C), kgroups = (kb + 3) / 4;
   // one pass of a wave's loop: more rows a workgroup were slower (13 x 1350 x
   // 512 with its statistics: 21.3 us, 32 rows 23.2; 17776 x 1280: 46.0 and 51.9)
-  const int64_t rows_per = 4 * kGnRows, chunks = (g.length + rows_per - 1) / rows_per;
-  if (g.n * chunks * kgroups > 0x7fffffff) return hipErrorInvalidValue;
+  // (but for a grid past kWideRow workgroups)
+  const int64_t passes = (g.length + 4 * kGnRows - 1) / (4 * kGnRows), most = std::max<int64_t>(1, kWideRow / (g.n * kgroups));
+  const int64_t rows_per = 4 * kGnRows * ((passes + most - 1) / most), chunks = (g.length + rows_per - 1) / rows_per;
   k_gn_apply_fp8<TI, HB><<<dim3((unsigned)(g.n * chunks * kgroups)), dim3(256), 0, s>>>(
       static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, coef, g.act, hadamard_scale(HB), (int)kb,
-      g.n * g.length, codes, scale);
+      g.total_rows, codes, scale);
   return hipGetLastError();
 }
 
@@ -800,7 +819,6 @@ template <typename TI>
 static hipError_t gn_short_fp8(const GroupNormArgs& g, const GnPlan& p, int hb, uint8_t* codes, float* scale,
                                hipStream_t s) {
   const int64_t chunks = (g.length + kGnBriefRows - 1) / kGnBriefRows;
-  if (g.n * chunks > 0x7fffffff) return hipErrorInvalidValue;
   return gn_dispatch<TI>(p, [&](auto v, auto merge) {
     constexpr int V = decltype(v)::value;
     constexpr bool MERGE = decltype(merge)::value;
@@ -814,7 +832,7 @@ static hipError_t gn_short_fp8(const GroupNormArgs& g, const GnPlan& p, int hb, 
       if (e != hipSuccess) return e;
       k_gn_short_fp8<TI, V, MERGE><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(
           static_cast<const TI*>(g.x), (int)g.length, (int)g.C, (int)g.groups, (int)chunks, g.eps, g.weight, g.bias,
-          g.act, hb, hadamard_scale(hb), (int)fp8_blocks(g.C), g.n * g.length, codes, scale);
+          g.act, hb, hadamard_scale(hb), (int)fp8_blocks(g.C), g.total_rows, codes, scale);
       return hipGetLastError();
     }
   });
@@ -843,8 +861,12 @@ static hipError_t group_norm_fp8_t(const GroupNormArgs& g, int hb, uint8_t* code
 
 hipError_t launch_group_norm_fp8(const GroupNormArgs& g, int hb, uint8_t* codes, float* scale, void* ws,
                                  hipStream_t s) {
-  return g.x_f32 ? group_norm_fp8_t<float>(g, hb, codes, scale, ws, s)
-                 : group_norm_fp8_t<uint16_t>(g, hb, codes, scale, ws, s);
+  return gn_runs(g, [&](const GroupNormArgs& r, int64_t n0) {
+    const int64_t row0 = n0 * g.length;
+    uint8_t* cr = codes + row0 * fp8_blocks(g.C) * kFp8Block;
+    return r.x_f32 ? group_norm_fp8_t<float>(r, hb, cr, scale + row0, ws, s)
+                   : group_norm_fp8_t<uint16_t>(r, hb, cr, scale + row0, ws, s);
+  });
 }
 
 }  // namespace hdq

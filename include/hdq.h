@@ -526,7 +526,8 @@ int hdq_dq_linear(const hdq_dq_grid *g, const uint8_t *core_codes, const void *c
  *   s = fl32(a / 448), code = E4M3 nearest to fl32(y * fl32(448 / a)), ties
  *   to even, so value = code * s.  A block with a < 2^-100 gets s = 0 and
  *   zero codes; a block holding a NaN or an infinity gets s = NaN and zero
- *   codes, so that the outputs that read it are NaN. */
+ *   codes, so that the outputs that read it are NaN.
+ * No output may overlap an input or the scratch. */
 #define HDQ_FP8_ROWS 0
 #define HDQ_FP8_BLOCKS 1
 #define HDQ_FP8_MAX_COLS (1 << 22)
@@ -588,7 +589,8 @@ int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K
  *   t = (x - mean) / sqrt(var + eps) * weight + bias,
  * mean and (biased) variance over the group's length x channels / groups
  * elements, joined in float64; y = t (HDQ_ACT_NONE) or t / (1 + e^-t)
- * (HDQ_ACT_SILU).  A NaN or an infinity makes its group's outputs NaN. */
+ * (HDQ_ACT_SILU).  A NaN or an infinity makes its group's outputs NaN.  Apart
+ * from y = x, no output may overlap an input or the scratch. */
 #define HDQ_ACT_NONE 0
 #define HDQ_ACT_SILU 1
 #define HDQ_GROUP_NORM_MAX_CHANNELS 8192

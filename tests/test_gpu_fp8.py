@@ -197,3 +197,29 @@ def test_offsets_past_32_bits():
         y = hdq.fp8_linear(None, wq, xq=xq, y_dtype=dt)
         assert bool((y[:-200] == 0).all())
         check_linear(y[-200:], tq, wq)
+
+
+def test_quantize_more_rows_than_one_grid_row():
+    """16 threads a row pass 2^32: repeated rows give repeated codes."""
+    S, reps, K = 4096, 65537, 8
+    x = activations(S, K, 3).to(DEV)
+    q, small = hdq.fp8_quantize(x.repeat(reps, 1), 8), hdq.fp8_quantize(x, 8)
+    codes = q.codes.view(reps, S, 128)
+    for i in range(0, reps, 4096):
+        assert bool((codes[i:i + 4096] == small.codes).all())
+    assert bool((codes[-1] == small.codes).all()) and bool((q.scale.view(reps, S) == small.scale).all())
+
+
+def test_linear_more_features_than_one_grid_row():
+    """One token, 32 threads a feature past 2^32: the last features are a small layer's."""
+    N, tail = 1 << 27, 40
+    x = activations(1, 8, 4).to(DEV)
+    small = hdq.fp8_quantize((0.02 * torch.randn(tail, 8, generator=torch.Generator().manual_seed(1))).to(torch.bfloat16).to(DEV),
+                             8, hdq.FP8_BLOCKS)
+    codes = torch.zeros(N + tail, 128, dtype=torch.uint8, device=DEV)
+    scale = torch.ones(N // 128 + 1, 1, device=DEV)
+    codes[N:], scale[-1] = small.codes, small.scale[0]
+    w = hdq.Fp8Tensor(N + tail, 8, 8, hdq.FP8_BLOCKS, codes=codes, scale=scale)
+    xq = hdq.fp8_quantize(x, 8)
+    for y in (hdq.fp8_linear(x, w), hdq.fp8_linear(None, w, xq=xq)):
+        assert torch.equal(y[:, N:], hdq.fp8_linear(x, small)) and bool((y[:, :N] == 0).all())

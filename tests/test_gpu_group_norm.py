@@ -234,3 +234,33 @@ def test_group_norm_past_32_bit_offsets():
     d = (y[-1:].float() - want.float()).abs()
     assert bool((d <= 2.0 ** -7 * want.float().abs() + 2.0 ** -20).all())
     assert bool((y[:-1] == 0).all())
+
+
+def test_more_samples_than_one_launch_takes():
+    """256 threads a sample pass 2^32: repeated samples give repeated outputs."""
+    S, reps, C, G = 4096, 4097, 8, 2
+    x, w, b = (t.to(DEV) for t in inputs(S, 1, C, torch.bfloat16, 12))
+    big = x.repeat(reps, 1, 1)
+    y = hdq.group_norm(big, G, w, b)
+    assert bool((y.view(reps, S, 1, C) == hdq.group_norm(x, G, w, b)).all())
+    del y
+    q, small = hdq.group_norm_fp8(big, G, w, b, had_block=8), hdq.group_norm_fp8(x, G, w, b, had_block=8)
+    assert bool((q.codes.view(reps, S, 128) == small.codes).all()) and bool((q.scale.view(reps, S) == small.scale).all())
+
+
+def test_fp8_rows_past_one_launch():
+    """16 threads a row pass 2^32: rows of period 4096 give codes of that period,
+    and those of a sample with the same statistics within one E4M3 step."""
+    S, reps, C, G = 4096, 65537, 8, 2
+    x, w, b = (t.to(DEV) for t in inputs(1, S, C, torch.bfloat16, 13, offset=0.0))
+    q = hdq.group_norm_fp8(x.repeat(1, reps, 1), G, w, b)
+    codes, scale = q.codes.view(reps, S, 128), q.scale.view(reps, S)
+    for i in range(0, reps, 4096):
+        assert bool((codes[i:i + 4096] == codes[0]).all())
+    assert bool((codes[-1] == codes[0]).all()) and bool((scale == scale[0]).all())
+    small = hdq.group_norm_fp8(x, G, w, b)
+    value = lambda c, s: c.view(torch.float8_e4m3fn).float()[:, :C] * s.view(-1, 1)
+    v, t = value(codes[0].contiguous(), scale[0]), value(small.codes, small.scale)
+    # nearly equal inputs can fall to either side of a rounding border: one step
+    step = torch.maximum(2.0 ** -3 * t.abs(), 2.0 ** -9 * small.scale.view(-1, 1))
+    assert bool(((v - t).abs() <= step * (1 + 2.0 ** -10)).all())
