@@ -563,7 +563,7 @@ def _launch(dev, stream, call):
     if dev.type != "cuda":
         raise ValueError(f"the tensors are on {dev}, not on a GPU")
     if stream is None:
-        if dev.index == torch.cuda.current_device():
+        if dev.index == torch._C._cuda_getDevice():
             return call(torch._C._cuda_getCurrentRawStream(dev.index))
         with torch.cuda.device(dev):
             return call(torch._C._cuda_getCurrentRawStream(dev.index))
@@ -613,12 +613,12 @@ class Fp8Tensor:
         sshape = (kb, rows) if layout == FP8_ROWS else (-(-rows // FP8_BLOCK), kb)
         dev = codes.device if codes is not None else scale.device if scale is not None else device
         if codes is None:
-            codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+            codes = torch.empty(*cshape, dtype=torch.uint8, device=dev)
         else:
             codes = codes.view(torch.uint8) if codes.dtype == torch.float8_e4m3fn else codes
             _operand(codes, "codes", torch.uint8, cshape, dev)
         if scale is None:
-            scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+            scale = torch.empty(*sshape, dtype=torch.float32, device=dev)
         else:
             _operand(scale, "scale", torch.float32, sshape, dev)
         self.codes, self.scale = codes, scale
@@ -669,7 +669,7 @@ def fp8_linear(x, w, xq=None, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
         _operand(y, "y", dt, (M, N), dev)
 
     def call(s):
-        out = torch.empty((M, N), dtype=dt, device=dev) if y is None else y
+        out = torch.empty(M, N, dtype=dt, device=dev) if y is None else y
         wd = w.desc()
         if xq is None:
             _keep, wp, wn = _scratch(ws, lib.hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype), dev)
@@ -717,7 +717,7 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, y=None
         _operand(y, "y", dt, x.shape, dev)
 
     def call(s):
-        out = torch.empty(x.shape, dtype=dt, device=dev) if y is None else y
+        out = torch.empty_like(x, dtype=dt) if y is None else y
         _keep, sp, sn = _scratch(ws, lib.hdq_group_norm_workspace_bytes(n, length, C, groups, 0), dev)
         st = lib.hdq_group_norm(x.data_ptr(), xt, n, length, C, groups, wp, bp, eps, act, out.data_ptr(), yt, sp, sn, s)
         _check("hdq_group_norm", st)
