@@ -12,9 +12,13 @@
 // registers is read once, normalized and written in one launch; a slab that one
 // workgroup can still stream takes one launch for the statistics and one for
 // the normalization; else partial statistics per chunk of rows, their join and
-// the normalization.  Measured: 691200 x 256 bf16 with SiLU 176 us (4.0 TB/s of
-// bytes read and written once, where a large copy reaches 4.8), 13 x 1350 x 512
-// 17 us (9 + 8), 2 x 77 x 300 fp32 5.5 us (one launch's latency).
+// the normalization.  The FP8 form codes whole rows, so it has no slab form: its
+// short samples take one launch whose workgroups each read the whole sample for
+// the statistics (k_gn_short_fp8), the others the statistics of the plain form.
+// Measured: 691200 x 256 bf16 with SiLU 176 us (4.0 TB/s of bytes read and
+// written once, where a large copy reaches 4.8), 13 x 1350 x 512 17 us (9 + 8),
+// to FP8 21 (9 + 12), 2 x 77 x 300 fp32 5.5 us (one launch's latency), 225 x 320
+// to FP8 10.4 (one launch).
 //
 // Statistics: a thread takes up to 16 rows at a time into registers, sums each
 // channel's values (relative to the first) and then the squared deviations from
