@@ -322,28 +322,28 @@ static hipError_t launch_deep(const uint8_t* xc, const float* xs, const uint8_t*
   return hipGetLastError();
 }
 
-template <int OUT, int WAVES, int WM_T, int WN_T>
-__global__ __launch_bounds__(64 * WAVES, 2) void k_fp8_pipe(const uint8_t* __restrict__ xc, const float* __restrict__ xs,
-                                                            const uint8_t* __restrict__ wc,
-                                                            const float* __restrict__ ws, void* __restrict__ Y,
-                                                            int64_t M, int N, int kb) {
-  gemm_fp8_pipe_body<OUT, WAVES, WM_T, WN_T>(xc, xs, wc, ws, Y, M, N, kb);
+template <int OUT, int WM_T, int WN_T>
+__global__ __launch_bounds__(kPipeThreads, 2) void k_fp8_pipe(const uint8_t* __restrict__ xc, const float* __restrict__ xs,
+                                                              const uint8_t* __restrict__ wc,
+                                                              const float* __restrict__ ws, void* __restrict__ Y,
+                                                              int64_t M, int N, int kb) {
+  gemm_fp8_pipe_body<OUT, WM_T, WN_T>(xc, xs, wc, ws, Y, M, N, kb);
 }
 
-// `slots` workgroups run at a time.
-template <int OUT, int WAVES, int WM_T, int WN_T>
+constexpr int64_t kPipeSlots = 256;  // workgroups that run at a time, one per CU
+template <int OUT, int WM_T, int WN_T>
 static hipError_t launch_pipe(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
-                              int64_t M, int64_t N, int64_t kb, int64_t slots, hipStream_t s) {
-  using Tile = Fp8Tile<WAVES, WM_T, WN_T>;
+                              int64_t M, int64_t N, int64_t kb, hipStream_t s) {
+  using Tile = Fp8Tile<WM_T, WN_T>;
   const int64_t tiles = ((M + Tile::BM - 1) / Tile::BM) * ((N + Tile::BN - 1) / Tile::BN);
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;
-  const hipError_t e = set_dynamic_lds_once<&k_fp8_pipe<OUT, WAVES, WM_T, WN_T>>(Tile::LDS);
+  const hipError_t e = set_dynamic_lds_once<&k_fp8_pipe<OUT, WM_T, WN_T>>(Tile::LDS);
   if (e != hipSuccess) return e;
   // as few workgroups as keep the number of rounds, a multiple of 8 (XCDs)
-  const int64_t rounds = (tiles + slots - 1) / slots;
-  const int64_t grid = tiles <= slots ? tiles : ((tiles + rounds - 1) / rounds + 7) / 8 * 8;
-  k_fp8_pipe<OUT, WAVES, WM_T, WN_T>
-      <<<dim3((unsigned)grid), dim3(Tile::THREADS), Tile::LDS, s>>>(xc, xs, wc, ws, y, M, (int)N, (int)kb);
+  const int64_t rounds = (tiles + kPipeSlots - 1) / kPipeSlots;
+  const int64_t grid = tiles <= kPipeSlots ? tiles : ((tiles + rounds - 1) / rounds + 7) / 8 * 8;
+  k_fp8_pipe<OUT, WM_T, WN_T>
+      <<<dim3((unsigned)grid), dim3(kPipeThreads), Tile::LDS, s>>>(xc, xs, wc, ws, y, M, (int)N, (int)kb);
   return hipGetLastError();
 }
 
@@ -354,21 +354,23 @@ static hipError_t launch_pipe(const uint8_t* xc, const float* xs, const uint8_t*
 //  * fewer than 192 tiles of 64 x 64: 32 x 64 tiles with four K groups 6.2, 64 x
 //    64 tiles 7.2 (64 tokens, 5760 x 1920), 8.8 / 12.0 (226, 1920 x 4096); with
 //    256 of them (1024, 1024 x 1024) 8.8 / 5.6.
-//  * fewer than 300 tiles of 128 x 128: 64 x 64 tiles 10.1, 128 x 128 tiles 14.9
-//    (226, 5760 x 1920: 90 tiles); with 495 (1350, 5760 x 1920) 33.8 / 21.3.
-//  * from 256 tiles of 256 x 256 on: 128 x 128 tiles 30.3, 256 x 256 tiles 25.5
-//    (17550, 1536 x 512: 414 tiles); with 138 (1350, 5760 x 1920) 21.3 / 29.1.
-//    fp32 output, from 400 on: 155.9 / 152.6 (17776, 1920 x 1920: 560 tiles); with
-//    368 (4050, 5760 x 1920) 98.5 / 103.9.
+//  * fewer than 800 tiles of 64 x 64 (fp32 output: 1300): 64 x 64 tiles 15.3, 128
+//    x 256 tiles 17.9 (450, 5760 x 1920: 720 tiles), fp32 21.1 / 31.4; with 832 (800,
+//    4096 x 512) 10.2 / 8.8, fp32 with 1320 (1350, 3840 x 1024) 23.3 / 21.6.
+//  * 128 x 256 tiles or 256 x 256 ones: by rounds of 256 tiles, a 128 x 256 round
+//    priced at 5 / 8 of the other.  1 round and 1 (1350, 5760 x 1920) 19.9 / 27.1,
+//    3 and 2 (4050, 5760 x 1920) 53.7 / 53.3, fp32 94 / 102; 2 and 1 (3000, 4096 x 1024)
+//    21.8 / 19.9, fp32 37.9 / 34.4; 13 and 7 (17776, 5760 x 1920) 231 / 208.
 template <int OUT>
 static hipError_t launch_fp8_out(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,
                                  int64_t M, int64_t N, int64_t kb, hipStream_t s) {
   const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
+  const auto rounds = [&](int64_t m, int64_t n) { return (tiles(m, n) + kPipeSlots - 1) / kPipeSlots; };
   if (M <= 16) return launch_few<OUT, 0>(xc, xs, nullptr, 0, wc, ws, y, M, N, kb, s);
   if (tiles(64, 64) < 192) return launch_deep<OUT, 1, 2, 4, 3, false>(xc, xs, wc, ws, y, M, N, kb, s);
-  if (tiles(128, 128) < 300) return launch_deep<OUT, 2, 2, 1, 4, true>(xc, xs, wc, ws, y, M, N, kb, s);
-  if (tiles(256, 256) < (OUT == kOutBf16 ? 256 : 400)) return launch_pipe<OUT, 4, 4, 4>(xc, xs, wc, ws, y, M, N, kb, 512, s);
-  return launch_pipe<OUT, 8, 8, 4>(xc, xs, wc, ws, y, M, N, kb, 256, s);
+  if (tiles(64, 64) < (OUT == kOutBf16 ? 800 : 1300)) return launch_deep<OUT, 2, 2, 1, 4, true>(xc, xs, wc, ws, y, M, N, kb, s);
+  if (5 * rounds(128, 256) < 8 * rounds(256, 256)) return launch_pipe<OUT, 4, 4>(xc, xs, wc, ws, y, M, N, kb, s);
+  return launch_pipe<OUT, 8, 4>(xc, xs, wc, ws, y, M, N, kb, s);
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws, void* y,

@@ -5,8 +5,8 @@
 
 namespace hdq {
 
-// Tiles of BM x BN = 32 WM_T x (16 WN_T waves / 2): the waves are 2 (tokens) x
-// WAVES / 2 (features), each of 16 WM_T x 16 WN_T.  A persistent tile loop with
+// Tiles of BM x BN = 32 WM_T x 64 WN_T: the eight waves are 2 (tokens) x 4
+// (features), each of 16 WM_T x 16 WN_T.  A persistent tile loop with
 // the tile order of the other GEMMs.  A stage is one block of 128 k: the tile's
 // X and W codes and its activation scales, brought into one of two LDS buffers
 // by LDS-DMA while the other is computed.  Code rows are 128 bytes with 16-byte
@@ -16,36 +16,41 @@ namespace hdq {
 // The weights' scale of the wave's features is a scalar.
 //
 // Bound by operand delivery and power, not by the scaling: 256 x 256 tiles,
-// 17776 x 3072 -> 12288, bf16 output: 627 us, 2.1 PFLOP/s, matrix units busy 0.49
-// of 1.4M cycles at 2.1 GHz (without the loads 570 us; a loop of products and
-// scalings alone runs at 3.7 PFLOP/s, at 1.8 GHz).  fp32 output, 17776 x 1920 ->
-// 5760: 390 us, 1.0 PFLOP/s of twice the matrix work.
-template <int WAVES, int WM_T, int WN_T>
+// 17776 x 3072 -> 12288, bf16 output: 613-640 us, 2.1 PFLOP/s, matrix units busy
+// 0.49 of 1.4M cycles at 2.1 GHz (without the loads 570 us; a loop of products
+// and scalings alone runs at 3.7 PFLOP/s, at 1.8 GHz).  fp32 output, 17776 x 1920
+// -> 5760: 386 us, 1.0 PFLOP/s of twice the matrix work.  A 128 x 256 tile
+// takes 0.62 (fp32) to 0.74 of the time of a 256 x 256 one (1350 x 1920 -> 5760, one
+// round of each: 19.9 and 27.1 us); a third stage buffer, which it leaves room
+// for, changed nothing (20.8), and 128 x 128 tiles of four waves, two of them on a
+// CU, were slower (21.2).
+constexpr int kPipeWaves = 8, kPipeThreads = 64 * kPipeWaves;
+template <int WM_T, int WN_T>
 struct Fp8Tile {
-  static constexpr int BM = 32 * WM_T, BN = 8 * WN_T * WAVES, THREADS = 64 * WAVES;
+  static constexpr int BM = 32 * WM_T, BN = 64 * WN_T;
   static constexpr int XB = BM * kFp8Block, WB = BN * kFp8Block;
-  static constexpr int OUT_PITCH = BN * 2 + 16;            // bf16 output row staged in LDS
-  static constexpr int kNeed = XB + WB + 4 * THREADS;      // scales: one 4-byte slot per thread
-  static constexpr int kOut = BM / 2 * OUT_PITCH;          // half an output tile
+  static constexpr int OUT_PITCH = BN * 2 + 16;                // bf16 output row staged in LDS
+  static constexpr int kNeed = XB + WB + 4 * kPipeThreads;     // scales: one 4-byte slot per thread
+  static constexpr int kOut = BM / 2 * OUT_PITCH;              // half an output tile
   static constexpr int STAGE = ((kNeed > kOut ? kNeed : kOut) + 1023) / 1024 * 1024;
   static constexpr int LDS = 2 * STAGE;
-  static_assert(BM <= THREADS && kFp8Block % (16 * WN_T) == 0, "tile shape");
+  static_assert(BM <= kPipeThreads / 2 && kFp8Block % (16 * WN_T) == 0 && LDS <= 160 * 1024, "tile shape");
 };
 
-template <int OUT, int WAVES, int WM_T, int WN_T>
+template <int OUT, int WM_T, int WN_T>
 __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ xc, const float* __restrict__ xs,
                                                    const uint8_t* __restrict__ wc, const float* __restrict__ ws,
                                                    void* __restrict__ Y, int64_t M, int N, int kb) {
   constexpr bool FAST = OUT == kOutBf16;
-  using Tile = Fp8Tile<WAVES, WM_T, WN_T>;
+  using Tile = Fp8Tile<WM_T, WN_T>;
   constexpr int BM = Tile::BM, BN = Tile::BN, XB = Tile::XB, SB = Tile::STAGE, kOutPitch = Tile::OUT_PITCH;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % 2, wn = wave / 2;
   // The tile's loads are issued by LOADERS waves; a wave is held up while it
-  // issues, so with two waves of a workgroup on a SIMD one of them issues none.
-  constexpr int LOADERS = WAVES > 4 ? WAVES / 2 : WAVES;
+  // issues, so of the two waves on a SIMD one issues none.
+  constexpr int LOADERS = kPipeWaves / 2;
   const bool loader = wave < LOADERS;
   const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (N + BN - 1) / BN;
   const TileSeq seq = tile_seq(tiles_m * tiles_n);
@@ -181,7 +186,7 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
           }
         lds_only_barrier();
 #pragma unroll 4
-        for (int r = tid / PIECES; r < 2 * HM; r += Tile::THREADS / PIECES) {
+        for (int r = tid / PIECES; r < 2 * HM; r += kPipeThreads / PIECES) {
           const uint8_t* src = stage + r * kOutPitch + 16 * (tid % PIECES);
           const int64_t m = m0 + r / HM * (2 * HM) + hh * HM + r % HM;
           if (m < M) {
@@ -233,18 +238,23 @@ __device__ __forceinline__ void gemm_fp8_pipe_body(const uint8_t* __restrict__ x
 
   // Stage g lives in buffer g % 2; stage g + 1 is issued when stage g's compute
   // starts, into the buffer every wave finished reading before the last barrier.
+  // Only the loaders wait for vector memory; the others' stores stay in flight.
+  auto end_stage = [&]() {
+    if (loader) wait_vmem<0>();
+    lds_only_barrier();
+  };
   issue(0);
-  stage_barrier();
-  for (int g = 0; g < G; g += 2) {
-    if (g + 1 < G) issue(1);
-    compute(0, sw);
-    finish_stage(0);
-    if (g + 1 == G) break;
-    stage_barrier();
-    if (g + 2 < G) issue(0);
-    compute(1, sw);
-    finish_stage(1);
-    stage_barrier();
+  end_stage();
+  for (int g0 = 0; g0 < G; g0 += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (g0 + u < G) {
+        if (g0 + u + 1 < G) issue(u ^ 1);
+        compute(u, sw);
+        finish_stage(u);
+        end_stage();
+      }
+    }
   }
 }
 

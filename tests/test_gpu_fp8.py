@@ -98,7 +98,8 @@ SHAPES = [(1, 8, 1, 8), (1, 128, 16, 128), (1, 1920, 577, 128), (2, 1000, 130, 8
           (2100, 392, 2050, 8), (4200, 128, 1030, 128), (2304, 640, 4096, 64), (16500, 264, 260, 8),
           (4100, 264, 4200, 8), (4353, 136, 4104, 8), (33, 4224, 100, 128), (1100, 1032, 1000, 8), (20, 40, 6000, 8),
           (1, 12288, 40, 128), (1, 16384, 20, 2), (1, 16512, 20, 128), (4, 4096, 50, 4), (5, 4096, 50, 16), (16, 1024, 33, 32),
-          (16, 1032, 33, 8), (3, 24, 3, 1)]
+          (16, 1032, 33, 8), (3, 24, 3, 1), (1351, 520, 3900, 8), (1700, 264, 2001, 8),
+          (3000, 264, 4101, 8), (1290, 128, 1290, 64)]
 
 
 @pytest.mark.parametrize("y_dtype", [hdq.DTYPE_BF16, hdq.DTYPE_F32])
