@@ -11,10 +11,11 @@
 // channels of a few groups, see gn_plan): a slab that fits a workgroup's
 // registers is read once, normalized and written in one launch; a slab that one
 // workgroup can still stream takes one launch for the statistics and one for
-// the normalization; else partial statistics per chunk of rows, their join and
-// the normalization.  The FP8 form codes whole rows, so it has no slab form: its
+// the normalization; else partial statistics per chunk of rows, their join (of
+// few chunks in small inputs: by the normalization itself) and the
+// normalization.  The FP8 form codes whole rows, so it has no slab form: its
 // short samples take one launch whose workgroups each read the whole sample for
-// the statistics (k_gn_short_fp8), the others the statistics of the plain form.
+// the statistics (k_gn_short_fp8), the others the plain form's statistics.
 // Measured: 691200 x 256 bf16 with SiLU 176 us (4.0 TB/s of bytes read and
 // written once, where a large copy reaches 4.8), 13 x 1350 x 512 17 us (9 + 8),
 // to FP8 21 (9 + 12), 2 x 77 x 300 fp32 5.5 us (one launch's latency), 225 x 320
@@ -198,6 +199,18 @@ __device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, int pr
     for (int e = 0; e < V; ++e) pairs[(pr * cv + c) * V + e] = make_float2(t.mean[e], t.m2[e]);
   }
 }
+// The end of a join over P lanes, from the lanes' sums of n, n d and M2 + n d^2.
+__device__ __forceinline__ void gn_join_lanes(int P, double ref, double sn, double sd, double s2, double& n,
+                                              double& mean, double& m2) {
+  for (int o = 1; o < P; o <<= 1) {
+    sn += __shfl_xor(sn, o);
+    sd += __shfl_xor(sd, o);
+    s2 += __shfl_xor(s2, o);
+  }
+  n = sn;
+  mean = ref + sd / sn;
+  m2 = fmax(s2 - sd * (sd / sn), 0.0) + 0.0 * s2;  // NaN stays NaN
+}
 // Joins group g's pairs of row slots 0 .. slots - 1 (slot r: rows(r) rows) over
 // the P lanes of an aligned lane group, in one pass: sums of n, n d and
 // M2 + n d^2 in float64, d the distance of a pair's mean from the first one's.
@@ -224,14 +237,7 @@ __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg
       ++r;
     }
   }
-  for (int o = 1; o < P; o <<= 1) {
-    sn += __shfl_xor(sn, o);
-    sd += __shfl_xor(sd, o);
-    s2 += __shfl_xor(s2, o);
-  }
-  n = sn;
-  mean = ref + sd / sn;
-  m2 = fmax(s2 - sd * (sd / sn), 0.0) + 0.0 * s2;  // NaN stays NaN
+  gn_join_lanes(P, ref, sn, sd, s2, n, mean, m2);
 }
 
 __device__ __forceinline__ float gn_rstd(double m2, double n, float eps) {
@@ -351,13 +357,71 @@ __device__ __forceinline__ void gn_normalize(float (&v)[V], const float (&mean)[
   }
 }
 
+// Where a normalization takes its groups' statistics from: coefficients that a
+// launch before it has written (part null), or the statistics' chunks, which
+// each workgroup joins itself.
+struct GnFrom {
+  const float* coef;
+  const double2* part;
+  int chunks;
+  int64_t rows_per;
+  int groups;
+  float eps;
+  const float* weight;
+  const float* bias;
+};
+
+// (mean, rstd) of a sample's groups into stat_s, from its chunks' pairs.
+template <int T>
+__device__ __forceinline__ void gn_join_chunks(const GnFrom& f, int64_t sample, int64_t length, int cg, float2* stat_s) {
+  const double2* part = f.part + sample * f.chunks * f.groups;
+  const int P = gn_lanes(f.groups, T), p = (int)threadIdx.x % P;
+  for (int g0 = 0; g0 < f.groups; g0 += T / P) {
+    const int g = g0 + (int)threadIdx.x / P;
+    if (g >= f.groups) continue;  // lane groups of P leave together
+    const double ref = part[g].x;
+    double sn = 0.0, sd = 0.0, s2 = 0.0;
+    for (int i = p; i < f.chunks; i += P) {
+      const double2 q = part[i * f.groups + g];
+      const double w = (double)min(f.rows_per, length - i * f.rows_per) * cg, d = q.x - ref;
+      sn += w;
+      sd += w * d;
+      s2 += q.y + w * d * d;
+    }
+    double n, mean, m2;
+    gn_join_lanes(P, ref, sn, sd, s2, n, mean, m2);
+    if (p == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, f.eps));
+  }
+  __syncthreads();
+}
+
+// A vector's coefficients.
+template <int V, bool JOIN>
+__device__ __forceinline__ void gn_coefs(const GnFrom& f, int64_t sample, int C, int cg, int ch, const float2* stat_s,
+                                         float (&mean)[V], float (&a)[V], float (&b)[V]) {
+  if constexpr (JOIN) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 st = stat_s[(ch + e) / cg];
+      mean[e] = st.x;
+      a[e] = f.weight != nullptr ? st.y * f.weight[ch + e] : st.y;
+      b[e] = f.bias != nullptr ? f.bias[ch + e] : 0.0f;
+    }
+  } else {
+    const float* cf = f.coef + sample * 3 * C + ch;
+    gn_load_coef<V>(cf, mean);
+    gn_load_coef<V>(cf + C, a);
+    gn_load_coef<V>(cf + 2 * C, b);
+  }
+}
+
 // Rows [r0, r0 + rows_per) of a sample, one channel vector per thread as in
 // k_gn_partial; the workgroups run through the rows from the end, so that
 // what the statistics read last is still in the memory-side cache.
-template <typename TI, typename TO, int V>
+template <typename TI, typename TO, int V, bool JOIN>
 __global__ __launch_bounds__(kGnThreads) void k_gn_apply(const TI* x, int64_t length, int C, int chunks,
-                                                         int64_t rows_per, const float* __restrict__ coef, int act,
-                                                         TO* y) {
+                                                         int64_t rows_per, GnFrom from, int act, TO* y) {
+  extern __shared__ float2 pair_s[];  // JOIN: one (mean, rstd) per group
   const unsigned blk = gridDim.x - 1 - blockIdx.x;
   const int64_t sample = blk / (unsigned)chunks;
   const int64_t r0 = (blk % (unsigned)chunks) * rows_per;
@@ -365,13 +429,12 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply(const TI* x, int64_t le
   const int64_t base = (sample * length + r0) * C;
   const int cv = C / V, rpar = cv >= kGnThreads ? 1 : kGnThreads / cv;
   const int pr = rpar > 1 ? (int)threadIdx.x / cv : 0;
+  const int cg = JOIN ? C / from.groups : 1;
+  if constexpr (JOIN) gn_join_chunks<kGnThreads>(from, sample, length, cg, pair_s);
   if (pr >= rpar) return;
-  const float* cf = coef + sample * 3 * C;
   for (int c = (int)threadIdx.x - pr * cv; c < cv; c += kGnThreads) {
     float mean[V], a[V], b[V];
-    gn_load_coef<V>(cf + c * V, mean);
-    gn_load_coef<V>(cf + C + c * V, a);
-    gn_load_coef<V>(cf + 2 * C + c * V, b);
+    gn_coefs<V, JOIN>(from, sample, C, cg, c * V, pair_s, mean, a, b);
     const int64_t o = base + (int64_t)pr * C + c * V, step = (int64_t)rpar * C;
     const int cnt = pr < rows ? (rows - pr + rpar - 1) / rpar : 0;
     // four rows are loaded before the first is stored (y may be x)
@@ -495,11 +558,12 @@ __device__ __forceinline__ void gn_code_chunk(float (&y)[8], bool in, int lane, 
 // as in the quantizer, take 96 registers of coefficients: 20.1 us for 13 x 1350
 // x 512, this form 8.)
 constexpr int kGnRows = 4;
-template <typename TI, int HB>
+template <typename TI, int HB, bool JOIN>
 __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int chunks,
-                                                      int64_t rows_per, const float* __restrict__ coef, int act,
-                                                      float c_b, int kb, int64_t total_rows,
-                                                      uint8_t* __restrict__ codes, float* __restrict__ scale) {
+                                                      int64_t rows_per, GnFrom from, int act, float c_b, int kb,
+                                                      int64_t total_rows, uint8_t* __restrict__ codes,
+                                                      float* __restrict__ scale) {
+  extern __shared__ float2 pair_s[];  // JOIN: one (mean, rstd) per group
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
   const int kgroups = (kb + 3) >> 2;
   const unsigned blk = gridDim.x - 1 - blockIdx.x;
@@ -508,6 +572,8 @@ __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, 
   const int64_t sample = rest / (unsigned)chunks;
   const int64_t r0 = (rest % (unsigned)chunks) * rows_per;
   const int rows = (int)min(rows_per, length - r0);
+  const int cg = JOIN ? C / from.groups : 1;
+  if constexpr (JOIN) gn_join_chunks<256>(from, sample, length, cg, pair_s);
   if (b >= kb) return;
   constexpr int NL = HB >= 16 ? HB / 8 : 1;
   const int chunk = (l16 & ~(NL - 1)) + fwht_chunk(lane, HB);
@@ -516,12 +582,7 @@ __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, 
   const int64_t row0 = sample * length + r0;
   const TI* p = x + row0 * C + (in ? ch : 0);
   float mean[8], a[8], bs[8];
-  {
-    const float* cf = coef + sample * 3 * C + (in ? ch : 0);
-    gn_load_coef<8>(cf, mean);
-    gn_load_coef<8>(cf + C, a);
-    gn_load_coef<8>(cf + 2 * C, bs);
-  }
+  gn_coefs<8, JOIN>(from, sample, C, cg, in ? ch : 0, pair_s, mean, a, bs);
   for (int r = lane >> 4; r < rows; r += 4 * kGnRows) {  // 16 lanes stay together
     GnRaw<TI, 8> q[kGnRows];
 #pragma unroll
@@ -635,6 +696,8 @@ static int64_t gn_rpar(int64_t C, int64_t vec) {
 constexpr int64_t kGnKeep = 16, kGnStream = 64;  // rows a thread keeps / streams at most
 // k_gn_short_fp8: channels and elements of a sample at most, rows of a workgroup
 constexpr int64_t kGnBriefChannels = 512, kGnBriefSample = 96 << 10, kGnBriefRows = 16;
+// elements of x and pairs of a sample up to which the normalization joins the chunks
+constexpr int64_t kGnJoinElements = 3 << 19, kGnJoinPairs = 1024;
 struct GnPlan {
   int64_t vec;
   bool merge;            // a vector lies in one group
@@ -643,6 +706,7 @@ struct GnPlan {
   bool keep;             // the slab is kept in registers (not for the FP8 form)
   bool slab;             // the statistics are a slab's
   bool brief;            // the FP8 form takes one launch
+  bool join;             // the normalization joins the chunks
   int64_t chunks, rows_per;
 };
 
@@ -684,6 +748,11 @@ static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool
   p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample &&
             (length <= kGnBriefRows || n * ((length + kGnBriefRows - 1) / kGnBriefRows) <= 256);
   gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
+  // A launch less, and no longer on the GPU: 984 x 537, one group 12.7 us, joined
+  // here 9.5; 6469 x 64 fp32 (832 pairs) 12.2 and 11.3; 2 x 3000 x 256 to FP8 16.2
+  // and 15.4.  With more rows or pairs it is longer (16384 x 128, 256 pairs 12.6
+  // and 13.9; 5000 x 256, 1280 pairs 14.4 and 16.0).
+  p.join = !p.slab && n * length * C <= kGnJoinElements && p.chunks * groups <= kGnJoinPairs;
   return p;
 }
 
@@ -734,14 +803,16 @@ static hipError_t gn_launch_slab(const GroupNormArgs& g, const GnPlan& p, void* 
   });
 }
 
-// The coefficients of every sample and channel into ws.
+// The statistics into ws: the coefficients of every sample and channel, or
+// (p.join) the chunks' pairs.
 template <typename TI>
-static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* ws, hipStream_t s) {
+static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* ws, GnFrom& from, hipStream_t s) {
   float* coef = static_cast<float*>(ws);
+  double2* part = reinterpret_cast<double2*>(static_cast<uint8_t*>(ws) + gn_coef_bytes(g.n, g.C));
+  from = GnFrom{coef, part, (int)p.chunks, p.rows_per, (int)g.groups, g.eps, g.weight, g.bias};
   if (p.slab)
     return p.threads == 256 ? gn_launch_slab<TI, TI, 256, 0>(g, p, nullptr, coef, s)
                             : gn_launch_slab<TI, TI, kGnSlabThreads, 0>(g, p, nullptr, coef, s);
-  double2* part = reinterpret_cast<double2*>(static_cast<uint8_t*>(ws) + gn_coef_bytes(g.n, g.C));
   const hipError_t e = gn_dispatch<TI>(p, [&](auto v, auto merge) {
     constexpr int V = decltype(v)::value;
     constexpr bool MERGE = decltype(merge)::value;
@@ -750,7 +821,7 @@ static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* w
         static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)p.chunks, p.rows_per, part);
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || p.join) return e;
   const int64_t total = g.n * g.groups;
   k_gn_final<<<dim3((unsigned)((total + 3) / 4)), dim3(256), 0, s>>>(part, total, g.length, (int)(g.C / g.groups),
                                                                      (int)g.groups, (int)p.chunks, p.rows_per, g.eps,
@@ -766,16 +837,21 @@ static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStr
     if (p.rows <= 8) return gn_launch_slab<TI, TO, 256, 8>(g, p, y, nullptr, s);
     return gn_launch_slab<TI, TO, 256, 16>(g, p, y, nullptr, s);
   }
-  const hipError_t e = gn_statistics<TI>(g, p, ws, s);
+  GnFrom from;
+  const hipError_t e = gn_statistics<TI>(g, p, ws, from, s);
   if (e != hipSuccess) return e;
   int64_t chunks, rows_per;
   gn_chunks(8192, g.n, g.length, 4 * gn_rpar(g.C, p.vec), chunks, rows_per);
   return gn_dispatch<TI>(p, [&](auto v, auto) {
     constexpr int V = decltype(v)::value;
-    k_gn_apply<TI, TO, V><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), 0, s>>>(
-        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, static_cast<const float*>(ws), g.act,
-        static_cast<TO*>(y));
-    return hipGetLastError();
+    const auto launch = [&](auto kernel, size_t lds) {
+      kernel<<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(static_cast<const TI*>(g.x), g.length,
+                                                                           (int)g.C, (int)chunks, rows_per, from,
+                                                                           g.act, static_cast<TO*>(y));
+      return hipGetLastError();
+    };
+    return p.join ? launch(&k_gn_apply<TI, TO, V, true>, (size_t)g.groups * sizeof(float2))
+                  : launch(&k_gn_apply<TI, TO, V, false>, 0);
   });
 }
 
@@ -805,18 +881,22 @@ hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* 
 }
 
 template <typename TI, int HB>
-static hipError_t gn_apply_fp8(const GroupNormArgs& g, const float* coef, uint8_t* codes, float* scale,
-                               hipStream_t s) {
+static hipError_t gn_apply_fp8(const GroupNormArgs& g, const GnPlan& p, const GnFrom& from, uint8_t* codes,
+                               float* scale, hipStream_t s) {
   const int64_t kb = fp8_blocks(g.C), kgroups = (kb + 3) / 4;
   // one pass of a wave's loop: more rows a workgroup were slower (13 x 1350 x
   // 512 with its statistics: 21.3 us, 32 rows 23.2; 17776 x 1280: 46.0 and 51.9)
   // (but for a grid past kWideRow workgroups)
   const int64_t passes = (g.length + 4 * kGnRows - 1) / (4 * kGnRows), most = std::max<int64_t>(1, kWideRow / (g.n * kgroups));
   const int64_t rows_per = 4 * kGnRows * ((passes + most - 1) / most), chunks = (g.length + rows_per - 1) / rows_per;
-  k_gn_apply_fp8<TI, HB><<<dim3((unsigned)(g.n * chunks * kgroups)), dim3(256), 0, s>>>(
-      static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, coef, g.act, hadamard_scale(HB), (int)kb,
-      g.total_rows, codes, scale);
-  return hipGetLastError();
+  const auto launch = [&](auto kernel, size_t lds) {
+    kernel<<<dim3((unsigned)(g.n * chunks * kgroups)), dim3(256), lds, s>>>(
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, from, g.act, hadamard_scale(HB),
+        (int)kb, g.total_rows, codes, scale);
+    return hipGetLastError();
+  };
+  return p.join ? launch(&k_gn_apply_fp8<TI, HB, true>, (size_t)g.groups * sizeof(float2))
+                : launch(&k_gn_apply_fp8<TI, HB, false>, 0);
 }
 
 template <typename TI>
@@ -847,18 +927,18 @@ static hipError_t group_norm_fp8_t(const GroupNormArgs& g, int hb, uint8_t* code
                                    hipStream_t s) {
   const GnPlan p = gn_plan(g.n, g.length, g.C, g.groups, g.x_f32);
   if (p.brief) return gn_short_fp8<TI>(g, p, hb, codes, scale, s);
-  const hipError_t e = gn_statistics<TI>(g, p, ws, s);
+  GnFrom from;
+  const hipError_t e = gn_statistics<TI>(g, p, ws, from, s);
   if (e != hipSuccess) return e;
-  const float* coef = static_cast<const float*>(ws);
   switch (hb) {
-    case 1: return gn_apply_fp8<TI, 1>(g, coef, codes, scale, s);
-    case 2: return gn_apply_fp8<TI, 2>(g, coef, codes, scale, s);
-    case 4: return gn_apply_fp8<TI, 4>(g, coef, codes, scale, s);
-    case 8: return gn_apply_fp8<TI, 8>(g, coef, codes, scale, s);
-    case 16: return gn_apply_fp8<TI, 16>(g, coef, codes, scale, s);
-    case 32: return gn_apply_fp8<TI, 32>(g, coef, codes, scale, s);
-    case 64: return gn_apply_fp8<TI, 64>(g, coef, codes, scale, s);
-    case 128: return gn_apply_fp8<TI, 128>(g, coef, codes, scale, s);
+    case 1: return gn_apply_fp8<TI, 1>(g, p, from, codes, scale, s);
+    case 2: return gn_apply_fp8<TI, 2>(g, p, from, codes, scale, s);
+    case 4: return gn_apply_fp8<TI, 4>(g, p, from, codes, scale, s);
+    case 8: return gn_apply_fp8<TI, 8>(g, p, from, codes, scale, s);
+    case 16: return gn_apply_fp8<TI, 16>(g, p, from, codes, scale, s);
+    case 32: return gn_apply_fp8<TI, 32>(g, p, from, codes, scale, s);
+    case 64: return gn_apply_fp8<TI, 64>(g, p, from, codes, scale, s);
+    case 128: return gn_apply_fp8<TI, 128>(g, p, from, codes, scale, s);
     default: return hipErrorInvalidValue;
   }
 }

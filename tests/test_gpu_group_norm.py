@@ -59,7 +59,8 @@ def check(y, x, groups, w, b, eps=1e-5, silu=False, norm=True):
 SHAPES = [(1, 1, 1, 1), (2, 1, 8, 4), (1, 2, 32, 32), (3, 7, 58, 1), (2, 77, 300, 30), (1, 1000, 64, 8),
           (2, 225, 320, 32), (1, 513, 1280, 32), (5, 130, 8, 2), (1, 9, 4104, 27), (1, 40, 8192, 32), (2, 33, 8191, 1),
           (13, 90, 512, 32), (40, 3, 96, 32), (1, 20011, 136, 17),
-          (2, 700, 256, 32), (1, 1300, 64, 4), (9, 2500, 512, 32), (300, 150, 44, 11), (1, 1021, 24, 8)]
+          (2, 700, 256, 32), (1, 1300, 64, 4), (9, 2500, 512, 32), (300, 150, 44, 11), (1, 1021, 24, 8),
+          (1, 984, 537, 1), (1, 5400, 64, 64), (2, 2001, 100, 25), (1, 800, 1537, 1)]
 
 
 @pytest.mark.parametrize("silu", [False, True])
@@ -142,7 +143,8 @@ FP8_SHAPES = [(1, 1, 8, 1, 8), (2, 5, 64, 8, 64), (1, 225, 320, 32, 64), (3, 37,
               (13, 50, 512, 32, 128), (1, 3000, 64, 4, 1), (9, 2500, 512, 32, 16), (2, 18, 4104, 27, 2), (1, 5, 200, 5, 4),
               (1, 6, 160, 5, 32), (3, 170, 512, 32, 128), (2, 33, 504, 21, 8), (1, 1000, 40, 5, 4),
               (7, 16, 256, 256, 64), (5, 17, 264, 8, 1),
-              (20, 225, 320, 32, 64), (300, 16, 128, 8, 128), (300, 17, 128, 8, 8), (1, 4097, 16, 4, 16)]
+              (20, 225, 320, 32, 64), (300, 16, 128, 8, 128), (300, 17, 128, 8, 8), (1, 4097, 16, 4, 16),
+              (1, 9000, 320, 32, 64), (2, 3000, 256, 16, 128)]
 
 
 @pytest.mark.parametrize("silu", [False, True])
