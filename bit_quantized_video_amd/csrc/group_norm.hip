@@ -358,8 +358,8 @@ __device__ __forceinline__ void gn_normalize(float (&v)[V], const float (&mean)[
 }
 
 // Where a normalization takes its groups' statistics from: coefficients that a
-// launch before it has written (part null), or the statistics' chunks, which
-// each workgroup joins itself.
+// launch before it has written, or (JOIN) the statistics' chunks, which each
+// workgroup joins itself.
 struct GnFrom {
   const float* coef;
   const double2* part;
