@@ -26,8 +26,8 @@
 // their mean, in float32, so neither a large mean nor an outlier cancels
 // digits; (mean, sum of squared deviations) pairs are joined by
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2,
-// a thread's own in float32, those of threads and workgroups in float64, in a
-// fixed order.
+// in a fixed order: means in float64 throughout (rounded to float32 once, in a
+// thread's pair), a thread's own M2 in float32 and the joined ones in float64.
 #include "fp8_device.h"
 #include "hdq_internal.h"
 
@@ -110,14 +110,21 @@ __device__ __forceinline__ int gn_lanes(int groups, int threads) {
   return p;
 }
 
-// A thread's (mean, M2) of each channel of one vector over n rows.
+// A thread's (mean, M2) of each channel of one vector over n rows.  The mean is
+// kept in float64: one workgroup may have a sample's every row, and a float32
+// mean rounded again every eight rows drifts by 2e-3 deviations over 20000 of
+// them when it is 2000 times the deviation.
 template <int V>
 struct GnSums {
-  float n, mean[V], m2[V];
+  float n, m2[V];
+  double mean[V];
   __device__ __forceinline__ void clear() {
     n = 0.0f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) mean[e] = m2[e] = 0.0f;
+    for (int e = 0; e < V; ++e) {
+      mean[e] = 0.0;
+      m2[e] = 0.0f;
+    }
   }
   // Joins the first cnt (1 .. K) of K rows held in q.
   template <typename T, int K>
@@ -148,24 +155,27 @@ struct GnSums {
     const float f = k / (n + k), g = n * f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float d = m[e] - mean[e];
-      m2[e] += __builtin_fmaf(d * d, g, d2[e]);
-      mean[e] = __builtin_fmaf(d, f, mean[e]);
+      const double d = (double)m[e] - mean[e];
+      const float df = (float)d;
+      m2[e] += __builtin_fmaf(df * df, g, d2[e]);
+      mean[e] = __builtin_fma(d, (double)f, mean[e]);
     }
     n += k;
   }
   // (mean, M2) of all V channels together (one group's).
   __device__ __forceinline__ float2 all() const {
-    float m = 0.0f, s = 0.0f, d2 = 0.0f;
+    double m = 0.0;
+    float s = 0.0f, d2 = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) m += mean[e] - mean[0];
-    m = __builtin_fmaf(m, 1.0f / V, mean[0]);
+    m = __builtin_fma(m, 1.0 / V, mean[0]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
+      const float d = (float)(mean[e] - m);
       s += m2[e];
-      d2 = __builtin_fmaf(mean[e] - m, mean[e] - m, d2);
+      d2 = __builtin_fmaf(d, d, d2);
     }
-    return make_float2(m, __builtin_fmaf(n, d2, s));
+    return make_float2((float)m, __builtin_fmaf(n, d2, s));
   }
 };
 
@@ -196,7 +206,7 @@ __device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, int pr
     pairs[pr * cv + c] = t.all();
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) pairs[(pr * cv + c) * V + e] = make_float2(t.mean[e], t.m2[e]);
+    for (int e = 0; e < V; ++e) pairs[(pr * cv + c) * V + e] = make_float2((float)t.mean[e], t.m2[e]);
   }
 }
 // The end of a join over P lanes, from the lanes' sums of n, n d and M2 + n d^2.
