@@ -3,7 +3,7 @@
 //
 // x [n, length, channels]; a group is channels / groups adjacent channels of
 // one sample:
-//   t = (x - mean) rsqrt(var + eps) weight + bias,  y = t or t / (1 + e^-t),
+//   t = (x - mean) / sqrt(var + eps) weight + bias,  y = t or t / (1 + e^-t),
 // mean and var over the group's length x channels / groups elements.
 //
 // Bound by HBM: x has to be read for the statistics before the first output,
@@ -28,6 +28,8 @@
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2,
 // in a fixed order: means in float64 throughout (rounded to float32 once, in a
 // thread's pair), a thread's own M2 in float32 and the joined ones in float64.
+// Where a thread's M2 leaves the float32 range, it sums its rows anew in float64,
+// so every finite input has finite statistics.
 #include "fp8_device.h"
 #include "hdq_internal.h"
 
@@ -162,7 +164,17 @@ struct GnSums {
     }
     n += k;
   }
-  // (mean, M2) of all V channels together (one group's).
+  // Whether M2 holds: not past the float32 range (then it is infinite, or NaN),
+  // nor so small that squares may have underflowed.
+  __device__ __forceinline__ bool holds(float least) const {
+    bool ok = true;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ok = ok && m2[e] >= least && m2[e] < __builtin_inff();
+    return ok;
+  }
+  // The pair of channel e, and of all V together (one group's): the mean and
+  // the root of M2 per element.
+  __device__ __forceinline__ float2 one(int e) const { return make_float2((float)mean[e], __builtin_sqrtf(m2[e] / n)); }
   __device__ __forceinline__ float2 all() const {
     double m = 0.0;
     float s = 0.0f, d2 = 0.0f;
@@ -172,12 +184,35 @@ struct GnSums {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float d = (float)(mean[e] - m);
-      s += m2[e];
-      d2 = __builtin_fmaf(d, d, d2);
+      s += m2[e] * (1.0f / V);
+      d2 = __builtin_fmaf(d * (1.0f / V), d, d2);
     }
-    return make_float2((float)m, __builtin_fmaf(n, d2, s));
+    return make_float2((float)m, __builtin_sqrtf(d2 + s / n));
   }
 };
+
+// Sums of squared deviations below this may have lost float32 squares to
+// underflow; an eps above 2^-100 hides them.
+__host__ __device__ inline float gn_least(float eps) { return eps < 0x1p-100f ? 0x1p-60f : 0.0f; }
+
+__device__ __forceinline__ double gn_value(float v) { return v; }
+__device__ __forceinline__ double gn_value(uint16_t v) { return bf16_lo(v); }
+
+// A channel's mean and M2 over cnt rows, in float64, a value at a time: for the
+// threads whose M2 float32 does not hold.
+template <typename T>
+__device__ __forceinline__ void gn_wide_sums(const T* p, int64_t step, int cnt, double& mean, double& m2) {
+  const double first = gn_value(p[0]);
+  mean = m2 = 0.0;
+#pragma nounroll
+  for (int i = 0; i < cnt; ++i) mean += gn_value(p[i * step]) - first;
+  mean = first + mean / cnt;
+#pragma nounroll
+  for (int i = 0; i < cnt; ++i) {
+    const double d = gn_value(p[i * step]) - mean;
+    m2 = __builtin_fma(d, d, m2);
+  }
+}
 
 // Sums cnt vectors at p, p + step, ...; eight loads are in flight at a time.
 template <typename T, int V>
@@ -197,17 +232,40 @@ __device__ __forceinline__ void gn_stream(const T* p, int64_t step, int cnt, GnS
   }
 }
 
-// Puts a thread's sums (row slot pr, channel vector c of cv) among a
-// workgroup's pairs: one pair per thread when a vector lies in one group
-// (MERGE), else one per channel.
-template <bool MERGE, int V>
-__device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, int pr, int c, int cv) {
-  if constexpr (MERGE) {
-    pairs[pr * cv + c] = t.all();
-  } else {
+// Puts the pairs of a thread's sums (cnt rows at p, p + step, ...; row slot pr,
+// channel vector c of cv) among a workgroup's: one pair per thread when a vector
+// lies in one group (MERGE), else one per channel.  A pair is the mean and the
+// root of M2 per element: both are within the float32 range for any finite rows.
+template <bool MERGE, typename T, int V>
+__device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, const T* p, int64_t step, int cnt,
+                                       float least, int pr, int c, int cv) {
+  if (cnt == 0) return;
+  float2* const to = pairs + (pr * cv + c) * (MERGE ? 1 : V);
+  if (t.holds(least)) {
+    if constexpr (MERGE) {
+      to[0] = t.all();
+    } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) pairs[(pr * cv + c) * V + e] = make_float2((float)t.mean[e], t.m2[e]);
+      for (int e = 0; e < V; ++e) to[e] = t.one(e);
+    }
+    return;
   }
+  double sd = 0.0, s2 = 0.0, ref = 0.0;  // MERGE: sums of d and M2 / cnt + d^2, d a channel's distance from ref
+#pragma nounroll
+  for (int e = 0; e < V; ++e) {
+    double mean, m2;
+    gn_wide_sums(p + e, step, cnt, mean, m2);
+    if constexpr (MERGE) {
+      if (e == 0) ref = mean;
+      const double d = mean - ref;
+      sd += d;
+      s2 += m2 / cnt + d * d;
+    } else {
+      to[e] = make_float2((float)mean, (float)sqrt(m2 / cnt));
+    }
+  }
+  if constexpr (MERGE)
+    to[0] = make_float2((float)(ref + sd / V), (float)sqrt(fmax(s2 / V - (sd / V) * (sd / V), 0.0) + 0.0 * s2));
 }
 // The end of a join over P lanes, from the lanes' sums of n, n d and M2 + n d^2.
 __device__ __forceinline__ void gn_join_lanes(int P, double ref, double sn, double sd, double s2, double& n,
@@ -223,7 +281,8 @@ __device__ __forceinline__ void gn_join_lanes(int P, double ref, double sn, doub
 }
 // Joins group g's pairs of row slots 0 .. slots - 1 (slot r: rows(r) rows) over
 // the P lanes of an aligned lane group, in one pass: sums of n, n d and
-// M2 + n d^2 in float64, d the distance of a pair's mean from the first one's.
+// n r^2 + n d^2 in float64, r a pair's root and d the distance of its mean from
+// the first one's.
 template <bool MERGE, int V, typename Rows>
 __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg, int cv, int slots, int p, int P,
                                               Rows rows, double& n, double& mean, double& m2) {
@@ -239,7 +298,7 @@ __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg
     const double w = (double)(rows(r) * (MERGE ? V : 1)), d = (double)q.x - ref;
     sn += w;
     sd += w * d;
-    s2 += (double)q.y + w * d * d;
+    s2 += w * ((double)q.y * (double)q.y + d * d);
     r += dr;
     c += dc;
     if (c >= per) {
@@ -250,8 +309,11 @@ __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg
   gn_join_lanes(P, ref, sn, sd, s2, n, mean, m2);
 }
 
-__device__ __forceinline__ float gn_rstd(double m2, double n, float eps) {
-  return (float)(1.0 / sqrt(m2 / n + (double)eps));
+// A group's (mean / 4, 4 rstd): t = (x / 4 - mean / 4) (4 rstd weight) + bias has
+// the roundings of the formula without the fours, and neither the difference of
+// two finite values overflows nor rstd underflows.
+__device__ __forceinline__ float2 gn_stat(double mean, double m2, double n, float eps) {
+  return make_float2((float)(0.25 * mean), (float)(4.0 / sqrt(m2 / n + (double)eps)));
 }
 
 // Chunk `c` of sample `s` (blockIdx = s * chunks + c): partial (mean, M2) of
@@ -260,7 +322,8 @@ __device__ __forceinline__ float gn_rstd(double m2, double n, float eps) {
 // a row, rpar rows at a time; rows of more than 512 vectors in several turns).
 template <typename T, int V, bool MERGE>
 __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__ x, int64_t length, int C, int groups,
-                                                           int chunks, int64_t rows_per, double2* __restrict__ part) {
+                                                           int chunks, int64_t rows_per, float least,
+                                                           double2* __restrict__ part) {
   extern __shared__ float2 pair_s[];  // [rpar][C], or with MERGE [rpar][cv]
   const int64_t sample = blockIdx.x / (unsigned)chunks;
   const int chunk = (int)(blockIdx.x % (unsigned)chunks);
@@ -279,7 +342,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__
       GnSums<V> t;
       t.clear();
       gn_stream<T, V>(p, step, cnt, t);
-      gn_put<MERGE, V>(pair_s, t, pr, c, cv);
+      gn_put<MERGE>(pair_s, t, p, step, cnt, least, pr, c, cv);
     }
   }
   __syncthreads();
@@ -294,11 +357,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__
 }
 
 // What the normalization reads per sample and channel, three rows of C floats:
-// mean, a = rstd * weight, b = bias, so t = (x - mean) a + b.
-__device__ __forceinline__ void gn_write_coef(float* __restrict__ coef, int C, int ch, float mean, float rstd,
+// mean / 4, a = 4 rstd * weight, b = bias, so t = (x / 4 - mean / 4) a + b.
+__device__ __forceinline__ void gn_write_coef(float* __restrict__ coef, int C, int ch, float2 st,
                                               const float* __restrict__ weight, const float* __restrict__ bias) {
-  coef[ch] = mean;
-  coef[C + ch] = weight != nullptr ? rstd * weight[ch] : rstd;
+  coef[ch] = st.x;
+  coef[C + ch] = weight != nullptr ? st.y * weight[ch] : st.y;
   coef[2 * C + ch] = bias != nullptr ? bias[ch] : 0.0f;
 }
 
@@ -343,10 +406,10 @@ __global__ __launch_bounds__(256) void k_gn_final(const double2* __restrict__ pa
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m2 += __shfl_xor(m2, o);
-  const float rstd = gn_rstd(m2, sn, eps);
+  const float2 st = gn_stat(mean, m2, sn, eps);
   const int C = cg * groups;
   for (int c = lane; c < cg; c += 64)
-    gn_write_coef(coef + sample * 3 * C, C, g * cg + c, (float)mean, rstd, weight, bias);
+    gn_write_coef(coef + sample * 3 * C, C, g * cg + c, st, weight, bias);
 }
 
 // V consecutive coefficients (16-byte aligned when V is 4 or 8: C is then a multiple of 4).
@@ -362,7 +425,7 @@ __device__ __forceinline__ void gn_normalize(float (&v)[V], const float (&mean)[
                                              const float (&b)[V], int act) {
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float t = __builtin_fmaf(v[e] - mean[e], a[e], b[e]);
+    const float t = __builtin_fmaf(__builtin_fmaf(v[e], 0.25f, -mean[e]), a[e], b[e]);
     v[e] = act ? gn_silu(t) : t;
   }
 }
@@ -400,7 +463,7 @@ __device__ __forceinline__ void gn_join_chunks(const GnFrom& f, int64_t sample, 
     }
     double n, mean, m2;
     gn_join_lanes(P, ref, sn, sd, s2, n, mean, m2);
-    if (p == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, f.eps));
+    if (p == 0) stat_s[g] = gn_stat(mean, m2, n, f.eps);
   }
   __syncthreads();
 }
@@ -500,7 +563,7 @@ __global__ __launch_bounds__(T) void k_gn_slab(const TI* x, int64_t length, int 
   } else {
     gn_stream<TI, V>(x + o, step, cnt, t);
   }
-  if (pr < rpar) gn_put<MERGE, V>(pair_s, t, pr, c, cv);
+  gn_put<MERGE>(pair_s, t, x + o, step, cnt, gn_least(eps), pr, c, cv);
   __syncthreads();
   const int P = gn_lanes(groups, T);
   for (int g0 = 0; g0 < groups; g0 += T / P) {
@@ -508,13 +571,13 @@ __global__ __launch_bounds__(T) void k_gn_slab(const TI* x, int64_t length, int 
     if (g >= groups) continue;  // lane groups of P leave together
     double n, mean, m2;
     gn_join_group<MERGE, V>(pair_s, g, cg, cv, min(rpar, rows), (int)threadIdx.x % P, P, slot_rows, n, mean, m2);
-    if (threadIdx.x % P == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, eps));
+    if (threadIdx.x % P == 0) stat_s[g] = gn_stat(mean, m2, n, eps);
   }
   __syncthreads();
   if constexpr (ROWS == 0) {
     for (int ch = threadIdx.x; ch < w; ch += T) {
       const float2 st = stat_s[ch / cg];
-      gn_write_coef(coef + sample * 3 * C, C, c0 + ch, st.x, st.y, weight, bias);
+      gn_write_coef(coef + sample * 3 * C, C, c0 + ch, st, weight, bias);
     }
   } else {
     if (cnt == 0) return;
@@ -631,8 +694,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_short_fp8(const TI* __restric
     GnSums<V> t;
     t.clear();
     if (pr < rpar) {
-      gn_stream<TI, V>(xs + (int64_t)pr * C + c * V, (int64_t)rpar * C, slot_rows(pr), t);
-      gn_put<MERGE, V>(pair_s, t, pr, c, cv);
+      const TI* p = xs + (int64_t)pr * C + c * V;
+      const int64_t step = (int64_t)rpar * C;
+      const int cnt = slot_rows(pr);
+      gn_stream<TI, V>(p, step, cnt, t);
+      gn_put<MERGE>(pair_s, t, p, step, cnt, gn_least(eps), pr, c, cv);
     }
   }
   __syncthreads();
@@ -642,13 +708,13 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_short_fp8(const TI* __restric
     if (g >= groups) continue;  // lane groups of P leave together
     double n, mean, m2;
     gn_join_group<MERGE, V>(pair_s, g, cg, cv, min(rpar, length), (int)threadIdx.x % P, P, slot_rows, n, mean, m2);
-    if (threadIdx.x % P == 0) stat_s[g] = make_float2((float)mean, gn_rstd(m2, n, eps));
+    if (threadIdx.x % P == 0) stat_s[g] = gn_stat(mean, m2, n, eps);
   }
   __syncthreads();
   float* const coef_s = reinterpret_cast<float*>(stat_s + groups + (groups & 1));  // [3][C]
   for (int ch = threadIdx.x; ch < C; ch += kGnThreads) {
     const float2 st = stat_s[ch / cg];
-    gn_write_coef(coef_s, C, ch, st.x, st.y, weight, bias);
+    gn_write_coef(coef_s, C, ch, st, weight, bias);
   }
   // a wave codes four rows of a block of 128 channels at a time, as
   // k_gn_apply_fp8; the next four are loaded meanwhile
@@ -828,7 +894,8 @@ static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* w
     constexpr bool MERGE = decltype(merge)::value;
     const size_t lds = (size_t)(gn_rpar(g.C, V) * g.C) * sizeof(float2) / (MERGE ? V : 1);
     k_gn_partial<TI, V, MERGE><<<dim3((unsigned)(g.n * p.chunks)), dim3(kGnThreads), lds, s>>>(
-        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)p.chunks, p.rows_per, part);
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)p.chunks, p.rows_per,
+        gn_least(g.eps), part);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.join) return e;

@@ -588,9 +588,13 @@ int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K
  * whose projections are the linear layers above):
  *   t = (x - mean) / sqrt(var + eps) * weight + bias,
  * mean and (biased) variance over the group's length x channels / groups
- * elements, joined in float64; y = t (HDQ_ACT_NONE) or t / (1 + e^-t)
- * (HDQ_ACT_SILU).  A NaN or an infinity makes its group's outputs NaN.  Apart
- * from y = x, no output may overlap an input or the scratch. */
+ * elements; y = t (HDQ_ACT_NONE) or t / (1 + e^-t) (HDQ_ACT_SILU).  A thread
+ * sums at most 16 rows of a channel at a time in float32, about their first
+ * one; these means and squared deviations are joined in float64.  Finite x of
+ * any size are normalized, where weight / sqrt(var + eps) is in float32's normal
+ * range and, without an eps to hide them, deviations are at least 2^-100; a NaN
+ * or an infinity makes its group's outputs NaN.  Apart from y = x, no output may
+ * overlap an input or the scratch. */
 #define HDQ_ACT_NONE 0
 #define HDQ_ACT_SILU 1
 #define HDQ_GROUP_NORM_MAX_CHANNELS 8192

@@ -1,6 +1,11 @@
-"""The group norm at the ends of its input range: long runs of rows on a large mean."""
+"""The group norm at the ends of its input range: long runs of rows on a large
+mean, magnitudes up to the types' largest and, without eps, small ones."""
+import math
+
 import pytest
 import torch
+
+import fp8_ref as R
 
 pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
@@ -47,3 +52,53 @@ def test_long_runs_keep_a_large_mean():
         ref, amp = exact(x[i:i + 1], C, 1e-5)
         err = (y[i:i + 1].double() - ref).abs()
         assert bool((err <= bound(ref, amp, torch.float32)).all()), float(err.max())
+
+
+# every way of the group norm: kept slabs (4, 8, 16 rows a thread), streamed
+# ones, joined chunks, three launches; vectors of 8, 4 and 1 channels, in one
+# group or several
+SHAPES = [(2, 77, 300, 30), (1, 225, 64, 8), (1, 500, 32, 4), (3, 7, 58, 1), (13, 600, 512, 32), (300, 300, 44, 11),
+          (1, 984, 537, 1), (2, 2001, 100, 25), (1, 30000, 64, 8), (2, 9000, 520, 65)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,L,C,G", SHAPES)
+def test_large_finite_values_are_normalized(n, L, C, G, dtype):
+    g = torch.Generator().manual_seed(n + L + C)
+    base = torch.randn(n, L, C, generator=g)
+    one = base.clone()
+    one[0, L // 2, C // 2] = 2e19                      # one value whose square is past float32
+    first = base.clone()
+    first[0, 0, 0] = -1e30                             # it is its thread's first row
+    ends = 3.3e38 * torch.sign(base)                   # differences are past float32
+    for x in (one, first, 2e19 * base, 3e37 * base, ends):
+        x = x.to(dtype)
+        assert bool(torch.isfinite(x).all())
+        ref, amp = exact(x, G, 1e-5)
+        y = hdq.group_norm(x.to(DEV), G).cpu().double()
+        err = (y - ref).abs()
+        assert bool((err <= bound(ref, amp, dtype)).all()), float(err.nan_to_num(nan=math.inf).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,L,C,G", SHAPES)
+def test_small_values_without_eps(n, L, C, G, dtype):
+    x = (1e-27 * torch.randn(n, L, C, generator=torch.Generator().manual_seed(n + L + C))).to(dtype)
+    ref, amp = exact(x, G, 0.0)
+    err = (hdq.group_norm(x.to(DEV), G, eps=0.0).cpu().double() - ref).abs()
+    assert bool((err <= bound(ref, amp, dtype)).all()), float(err.nan_to_num(nan=math.inf).max())
+
+
+@pytest.mark.parametrize("n,L,C,G", [(1, 225, 320, 32), (13, 600, 512, 32), (1, 9000, 64, 4), (2, 3000, 256, 16),
+                                     (5, 17, 264, 11)])
+def test_fp8_form_of_large_finite_values(n, L, C, G):
+    """Codes of the normalized values: half an E4M3 step (2^-4 of the value,
+    2^-10 of the scale for small ones) beside the norm's own bound."""
+    x = (1e20 * torch.randn(n, L, C, generator=torch.Generator().manual_seed(L))).to(torch.bfloat16)
+    ref, amp = exact(x, G, 1e-5)
+    q = hdq.group_norm_fp8(x.to(DEV), G)
+    ref, slack = ref.view(n * L, C), bound(ref, amp, torch.float32).view(n * L, C)
+    s = R.scale_per_element(q.scale.cpu(), "rows", n * L)
+    v = (q.codes.view(torch.float8_e4m3fn).float().cpu().double() * s)[:, :C]
+    tol = torch.maximum(2.0 ** -4 * (ref.abs() + slack), 2.0 ** -10 * s[:, :C]) * (1 + 2.0 ** -20) + slack
+    assert bool(((v - ref).abs() <= tol).all())
