@@ -164,8 +164,9 @@ struct GnSums {
     }
     n += k;
   }
-  // Whether M2 holds: not past the float32 range (then it is infinite, or NaN),
-  // nor so small that squares may have underflowed.
+  // Whether M2 holds: not past the float32 range (then it is infinite, or NaN;
+  // NaN too for a first mean whose square is past it, times the n of 0), nor so
+  // small that squares may have underflowed.
   __device__ __forceinline__ bool holds(float least) const {
     bool ok = true;
 #pragma unroll
@@ -176,18 +177,17 @@ struct GnSums {
   // the root of M2 per element.
   __device__ __forceinline__ float2 one(int e) const { return make_float2((float)mean[e], __builtin_sqrtf(m2[e] / n)); }
   __device__ __forceinline__ float2 all() const {
-    double m = 0.0;
-    float s = 0.0f, d2 = 0.0f;
+    double m = 0.0, d2 = 0.0;
+    float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) m += mean[e] - mean[0];
     m = __builtin_fma(m, 1.0 / V, mean[0]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float d = (float)(mean[e] - m);
       s += m2[e] * (1.0f / V);
-      d2 = __builtin_fmaf(d * (1.0f / V), d, d2);
+      d2 = __builtin_fma(mean[e] - m, mean[e] - m, d2);  // past float32 where all of m2 holds
     }
-    return make_float2((float)m, __builtin_sqrtf(d2 + s / n));
+    return make_float2((float)m, (float)sqrt(__builtin_fma(d2, 1.0 / V, (double)(s / n))));
   }
 };
 

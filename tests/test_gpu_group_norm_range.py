@@ -89,6 +89,32 @@ def test_small_values_without_eps(n, L, C, G, dtype):
     assert bool((err <= bound(ref, amp, dtype)).all()), float(err.nan_to_num(nan=math.inf).max())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,L,C,G", SHAPES + [(1, 1, 64, 8), (3, 1, 320, 32), (2, 16, 520, 65)])
+def test_channels_that_differ_but_do_not_vary(n, L, C, G, dtype):
+    """Every row the same: a thread's deviations are zero, its channels' means
+    differ by more, or without eps by less, than float32's squares hold."""
+    row = torch.randn(n, 1, C, generator=torch.Generator().manual_seed(C)).expand(n, L, C)
+    for scale, eps in ((1e20, 1e-5), (3e37, 0.0), (1e-27, 0.0)):
+        x = (scale * row).to(dtype)
+        ref, amp = exact(x, G, eps)
+        err = (hdq.group_norm(x.to(DEV), G, eps=eps).cpu().double() - ref).abs()
+        assert bool((err <= bound(ref, amp, dtype)).all()), (scale, float(err.nan_to_num(nan=math.inf).max()))
+
+
+@pytest.mark.parametrize("L", [4096, 40000])
+def test_means_that_grow_past_a_float32_square(L):
+    """Every row's deviations from its thread's mean have finite squares, the
+    distance of neighbouring channels' means has not."""
+    x = torch.full((1, L, 64), 2.6e19)
+    x[:, :L // 2] = 1.8e19
+    x[:, :, 1::2] *= -1
+    x = x.to(torch.bfloat16)
+    ref, amp = exact(x, 8, 1e-5)
+    err = (hdq.group_norm(x.to(DEV), 8).cpu().double() - ref).abs()
+    assert bool((err <= bound(ref, amp, torch.bfloat16)).all()), float(err.nan_to_num(nan=math.inf).max())
+
+
 @pytest.mark.parametrize("n,L,C,G", [(1, 225, 320, 32), (13, 600, 512, 32), (1, 9000, 64, 4), (2, 3000, 256, 16),
                                      (5, 17, 264, 11)])
 def test_fp8_form_of_large_finite_values(n, L, C, G):
