@@ -31,6 +31,7 @@
 // Where a thread's M2 leaves the float32 range, it sums its rows anew in float64,
 // so every finite input has finite statistics.
 #include "fp8_device.h"
+#include "group_norm_plan.h"
 #include "hdq_internal.h"
 
 #include <algorithm>
@@ -38,7 +39,6 @@
 
 namespace hdq {
 
-constexpr int kGnThreads = 512, kGnSlabThreads = 512;
 // a slab's pairs (one per thread and channel of its vector) and groups
 constexpr int kGnSlabLds = kGnSlabThreads * 8 * 8 + 8 * 8192;
 // a short sample's pairs, groups and coefficients (at most 512 channels)
@@ -367,12 +367,11 @@ __device__ __forceinline__ void gn_write_coef(float* __restrict__ coef, int C, i
 
 // Group g of sample s (one wave each): the join of at most 512 chunks' pairs,
 // and its channels' coefficients.
-constexpr int kGnMaxChunks = 512;
-__global__ __launch_bounds__(256) void k_gn_final(const double2* __restrict__ part, int64_t total, int64_t length,
+__global__ __launch_bounds__(kGnFinalThreads) void k_gn_final(const double2* __restrict__ part, int64_t total, int64_t length,
                                                   int cg, int groups, int chunks, int64_t rows_per, float eps,
                                                   const float* __restrict__ weight, const float* __restrict__ bias,
                                                   float* __restrict__ coef) {
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t id = (int64_t)wide_block() * kGnFinalGroups + (threadIdx.x >> 6);
   if (id >= total) return;
   const int64_t sample = id / groups;
   const int g = (int)(id - sample * groups), lane = threadIdx.x & 63;
@@ -630,9 +629,8 @@ __device__ __forceinline__ void gn_code_chunk(float (&y)[8], bool in, int lane, 
 // The loads of kGnRows row groups are in flight together.  (32 channels a lane,
 // as in the quantizer, take 96 registers of coefficients: 20.1 us for 13 x 1350
 // x 512, this form 8.)
-constexpr int kGnRows = 4;
 template <typename TI, int HB, bool JOIN>
-__global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int chunks,
+__global__ __launch_bounds__(kGnCodeThreads) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int chunks,
                                                       int64_t rows_per, GnFrom from, int act, float c_b, int kb,
                                                       int64_t total_rows, uint8_t* __restrict__ codes,
                                                       float* __restrict__ scale) {
@@ -646,7 +644,7 @@ __global__ __launch_bounds__(256) void k_gn_apply_fp8(const TI* __restrict__ x, 
   const int64_t r0 = (rest % (unsigned)chunks) * rows_per;
   const int rows = (int)min(rows_per, length - r0);
   const int cg = JOIN ? C / from.groups : 1;
-  if constexpr (JOIN) gn_join_chunks<256>(from, sample, length, cg, pair_s);
+  if constexpr (JOIN) gn_join_chunks<kGnCodeThreads>(from, sample, length, cg, pair_s);
   if (b >= kb) return;
   constexpr int NL = HB >= 16 ? HB / 8 : 1;
   const int chunk = (l16 & ~(NL - 1)) + fwht_chunk(lane, HB);
@@ -749,92 +747,6 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_short_fp8(const TI* __restric
   }
 }
 
-// Chunks of a sample's rows for a pass of about `total` workgroups that take
-// `per` rows at least.  The statistics take 512, the two per CU that run at a
-// time (1 x 691200 x 256: 88 us, 1024 of them 94); the normalization 8192 (172
-// us with the statistics, 1024 of them 182).
-static void gn_chunks(int64_t total, int64_t n, int64_t length, int64_t per, int64_t& chunks, int64_t& rows_per) {
-  int64_t want = (total + n - 1) / n;
-  if (want > (length + per - 1) / per) want = (length + per - 1) / per;
-  if (want < 1) want = 1;
-  rows_per = (length + want - 1) / want;
-  chunks = (length + rows_per - 1) / rows_per;
-}
-
-// 16-byte vectors where the channels allow, else 8 bytes of bf16, else one channel
-static int64_t gn_vec(int64_t C, bool f32) { return C % 8 == 0 && !f32 ? 8 : C % 4 == 0 ? 4 : 1; }
-static int64_t gn_rpar(int64_t C, int64_t vec) {
-  const int64_t cv = C / vec;
-  return cv >= kGnThreads ? 1 : kGnThreads / cv;
-}
-
-// How a call runs (a rule on its sizes alone; the workspace follows it).
-constexpr int64_t kGnKeep = 16, kGnStream = 64;  // rows a thread keeps / streams at most
-// k_gn_short_fp8: channels and elements of a sample at most, rows of a workgroup
-constexpr int64_t kGnBriefChannels = 512, kGnBriefSample = 96 << 10, kGnBriefRows = 16;
-// elements of x and pairs of a sample up to which the normalization joins the chunks
-constexpr int64_t kGnJoinElements = 3 << 19, kGnJoinPairs = 1024;
-struct GnPlan {
-  int64_t vec;
-  bool merge;            // a vector lies in one group
-  int64_t width, slabs;  // channels of a slab, slabs per sample
-  int64_t threads, rows; // of a slab: threads, and rows per thread
-  bool keep;             // the slab is kept in registers (not for the FP8 form)
-  bool slab;             // the statistics are a slab's
-  bool brief;            // the FP8 form takes one launch
-  bool join;             // the normalization joins the chunks
-  int64_t chunks, rows_per;
-};
-
-static GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool f32) {
-  GnPlan p;
-  p.vec = gn_vec(C, f32);
-  const int64_t cg = C / groups;
-  p.merge = cg % p.vec == 0;
-  int64_t unit = cg;  // channels of the fewest whole groups that are whole vectors
-  while (unit % p.vec != 0) unit += cg;
-  // slabs of at least 64 channels, fewer where that leaves CUs without work
-  int64_t k = 1;
-  while (k * unit < 64 && n * (C / ((k + 1) * unit)) >= 256) ++k;
-  p.width = k * unit < C ? k * unit : C;
-  p.slabs = (C + p.width - 1) / p.width;
-  const int64_t cv = p.width / p.vec;
-  // the fewest threads whose registers hold the slab: fewer pairs to join
-  p.threads = 0;
-  p.rows = kGnStream + 1;
-  for (const int64_t t : {(int64_t)256, (int64_t)kGnSlabThreads}) {
-    if (cv > t) continue;
-    p.threads = t;
-    p.rows = (length + t / cv - 1) / (t / cv);
-    if (p.rows <= kGnKeep) break;
-  }
-  // Kept in registers: up to 16 rows of 128 bytes or more; 8 of narrower ones,
-  // whose lines several workgroups share (13 x 675 x 512, 6 rows of 32 bytes:
-  // 11.9 us, with two launches 13.6; 13 x 4000 x 512, 16 rows: 53.9 and 40.1).
-  p.keep = p.threads == 256 && p.rows <= (p.width * (f32 ? 4 : 2) >= 128 ? kGnKeep : kGnKeep / 2);
-  // A larger slab is streamed by one workgroup only where there is one for every
-  // CU: with few of them the chunks' three launches are faster (1 x 16384 x 128:
-  // 15.5 us against 47.0).
-  p.slab = p.keep || (p.threads == 256 && p.rows <= kGnKeep) || (p.rows <= kGnStream && n * p.slabs >= 256);
-  // As long on the GPU as two launches (225 x 320: 10.4 us and 9.8; 64 x 512: 7.5
-  // and 8.2; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
-  // launch's host time and no workspace.  A sample's workgroups read it again
-  // each, so either it has one (1000 x 16 x 512: 26.2 and 49.8) or all run at a
-  // time (13 x 225 x 320: 12.0 and 10.6; 64 x 225 x 320, 960 of them: 42.6 and 15.9).
-  p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample &&
-            (length <= kGnBriefRows || n * ((length + kGnBriefRows - 1) / kGnBriefRows) <= 256);
-  gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
-  // A launch less, and no longer on the GPU: 984 x 537, one group 12.7 us, joined
-  // here 9.5; 6469 x 64 fp32 (832 pairs) 12.2 and 11.3; 2 x 3000 x 256 to FP8 16.2
-  // and 15.4.  With more rows or pairs it is longer (16384 x 128, 256 pairs 12.6
-  // and 13.9; 5000 x 256, 1280 pairs 14.4 and 16.0).
-  p.join = !p.slab && n * length * C <= kGnJoinElements && p.chunks * groups <= kGnJoinPairs;
-  return p;
-}
-
-static size_t gn_align(size_t v) { return (v + 255) / 256 * 256; }
-static size_t gn_coef_bytes(int64_t n, int64_t C) { return gn_align((size_t)(n * C) * 3 * sizeof(float)); }
-
 // Enough for either input type: nothing when the slabs are kept (not the FP8
 // form), else the coefficients, and the chunks' pairs unless the statistics are
 // a slab's.
@@ -872,7 +784,7 @@ static hipError_t gn_launch_slab(const GroupNormArgs& g, const GnPlan& p, void* 
     const size_t lds = ((size_t)T * (MERGE ? 1 : V) + (size_t)(p.width / cg)) * sizeof(float2);
     const hipError_t e = set_dynamic_lds_once<&k_gn_slab<TI, TO, V, MERGE, T, ROWS>>(kGnSlabLds);
     if (e != hipSuccess) return e;
-    k_gn_slab<TI, TO, V, MERGE, T, ROWS><<<dim3((unsigned)(g.n * p.slabs)), dim3(T), lds, s>>>(
+    k_gn_slab<TI, TO, V, MERGE, T, ROWS><<<to_dim3(p.slab_grid), dim3(T), lds, s>>>(
         static_cast<const TI*>(g.x), g.length, (int)g.C, (int)cg, (int)p.width, (int)p.slabs, g.eps, g.weight, g.bias,
         g.act, static_cast<TO*>(y), coef);
     return hipGetLastError();
@@ -893,16 +805,15 @@ static hipError_t gn_statistics(const GroupNormArgs& g, const GnPlan& p, void* w
     constexpr int V = decltype(v)::value;
     constexpr bool MERGE = decltype(merge)::value;
     const size_t lds = (size_t)(gn_rpar(g.C, V) * g.C) * sizeof(float2) / (MERGE ? V : 1);
-    k_gn_partial<TI, V, MERGE><<<dim3((unsigned)(g.n * p.chunks)), dim3(kGnThreads), lds, s>>>(
+    k_gn_partial<TI, V, MERGE><<<to_dim3(p.partial_grid), dim3(kGnThreads), lds, s>>>(
         static_cast<const TI*>(g.x), g.length, (int)g.C, (int)g.groups, (int)p.chunks, p.rows_per,
         gn_least(g.eps), part);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.join) return e;
-  const int64_t total = g.n * g.groups;
-  k_gn_final<<<dim3((unsigned)((total + 3) / 4)), dim3(256), 0, s>>>(part, total, g.length, (int)(g.C / g.groups),
-                                                                     (int)g.groups, (int)p.chunks, p.rows_per, g.eps,
-                                                                     g.weight, g.bias, coef);
+  k_gn_final<<<to_dim3(p.final_grid), dim3(kGnFinalThreads), 0, s>>>(
+      part, g.n * g.groups, g.length, (int)(g.C / g.groups), (int)g.groups, (int)p.chunks, p.rows_per, g.eps, g.weight,
+      g.bias, coef);
   return hipGetLastError();
 }
 
@@ -917,14 +828,12 @@ static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStr
   GnFrom from;
   const hipError_t e = gn_statistics<TI>(g, p, ws, from, s);
   if (e != hipSuccess) return e;
-  int64_t chunks, rows_per;
-  gn_chunks(8192, g.n, g.length, 4 * gn_rpar(g.C, p.vec), chunks, rows_per);
   return gn_dispatch<TI>(p, [&](auto v, auto) {
     constexpr int V = decltype(v)::value;
     const auto launch = [&](auto kernel, size_t lds) {
-      kernel<<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(static_cast<const TI*>(g.x), g.length,
-                                                                           (int)g.C, (int)chunks, rows_per, from,
-                                                                           g.act, static_cast<TO*>(y));
+      kernel<<<to_dim3(p.apply_grid), dim3(kGnThreads), lds, s>>>(static_cast<const TI*>(g.x), g.length, (int)g.C,
+                                                                  (int)p.apply_chunks, p.apply_rows, from, g.act,
+                                                                  static_cast<TO*>(y));
       return hipGetLastError();
     };
     return p.join ? launch(&k_gn_apply<TI, TO, V, true>, (size_t)g.groups * sizeof(float2))
@@ -932,13 +841,10 @@ static hipError_t group_norm_t(const GroupNormArgs& g, void* y, void* ws, hipStr
   });
 }
 
-// HIP takes fewer than 2^32 threads a launch: f(arguments, first sample) for
-// runs of samples of about equal number, whose grids stay near kWideRow
-// workgroups (a sample has at most ceil(C / 64) slabs then).  From 512 samples on
-// the plan does not depend on their number, so neither does the workspace's use.
+// f(arguments, first sample) for every run of samples.
 template <typename F>
 static hipError_t gn_runs(const GroupNormArgs& g, F f) {
-  const int64_t most = kWideRow / ((g.C + 63) / 64), runs = (g.n + most - 1) / most, step = (g.n + runs - 1) / runs;
+  const int64_t step = gn_run_samples(g.n, g.C);
   for (int64_t n0 = 0; n0 < g.n; n0 += step) {
     GroupNormArgs r = g;
     r.x = static_cast<const uint8_t*>(g.x) + n0 * g.length * g.C * (g.x_f32 ? 4 : 2);
@@ -960,16 +866,10 @@ hipError_t launch_group_norm(const GroupNormArgs& g, void* y, bool y_f32, void* 
 template <typename TI, int HB>
 static hipError_t gn_apply_fp8(const GroupNormArgs& g, const GnPlan& p, const GnFrom& from, uint8_t* codes,
                                float* scale, hipStream_t s) {
-  const int64_t kb = fp8_blocks(g.C), kgroups = (kb + 3) / 4;
-  // one pass of a wave's loop: more rows a workgroup were slower (13 x 1350 x
-  // 512 with its statistics: 21.3 us, 32 rows 23.2; 17776 x 1280: 46.0 and 51.9)
-  // (but for a grid past kWideRow workgroups)
-  const int64_t passes = (g.length + 4 * kGnRows - 1) / (4 * kGnRows), most = std::max<int64_t>(1, kWideRow / (g.n * kgroups));
-  const int64_t rows_per = 4 * kGnRows * ((passes + most - 1) / most), chunks = (g.length + rows_per - 1) / rows_per;
   const auto launch = [&](auto kernel, size_t lds) {
-    kernel<<<dim3((unsigned)(g.n * chunks * kgroups)), dim3(256), lds, s>>>(
-        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)chunks, rows_per, from, g.act, hadamard_scale(HB),
-        (int)kb, g.total_rows, codes, scale);
+    kernel<<<to_dim3(p.code_grid), dim3(kGnCodeThreads), lds, s>>>(
+        static_cast<const TI*>(g.x), g.length, (int)g.C, (int)p.code_chunks, p.code_rows, from, g.act,
+        hadamard_scale(HB), (int)fp8_blocks(g.C), g.total_rows, codes, scale);
     return hipGetLastError();
   };
   return p.join ? launch(&k_gn_apply_fp8<TI, HB, true>, (size_t)g.groups * sizeof(float2))
@@ -991,7 +891,7 @@ static hipError_t gn_short_fp8(const GroupNormArgs& g, const GnPlan& p, int hb, 
       const size_t lds = (pairs + (pairs & 1) + (size_t)(g.groups + (g.groups & 1))) * sizeof(float2) + (size_t)g.C * 3 * sizeof(float);
       const hipError_t e = set_dynamic_lds_once<&k_gn_short_fp8<TI, V, MERGE>>(kGnShortLds);
       if (e != hipSuccess) return e;
-      k_gn_short_fp8<TI, V, MERGE><<<dim3((unsigned)(g.n * chunks)), dim3(kGnThreads), lds, s>>>(
+      k_gn_short_fp8<TI, V, MERGE><<<to_dim3(p.brief_grid), dim3(kGnThreads), lds, s>>>(
           static_cast<const TI*>(g.x), (int)g.length, (int)g.C, (int)g.groups, (int)chunks, g.eps, g.weight, g.bias,
           g.act, hb, hadamard_scale(hb), (int)fp8_blocks(g.C), g.total_rows, codes, scale);
       return hipGetLastError();

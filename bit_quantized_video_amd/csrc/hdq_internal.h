@@ -11,6 +11,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "launch_grid.h"
+
 namespace hdq {
 
 // Raises a kernel's dynamic LDS limit to `bytes` once per device (the
@@ -219,13 +221,9 @@ hipError_t launch_gemm_fp4_core_add(const uint8_t* xc, const uint8_t* xs, const 
 hipError_t launch_dq_combine(const float* yd, const float* yc, const float* cscale, const float* wts,
                              const DqGrid& g, int64_t N, void* y, int out_dtype, hipStream_t s);
 // ---- FP8 block-128 (fp8_quant.hip, gemm_fp8.hip) ----
-// A grid of `blocks` workgroups (at most 2^31) of up to 512 threads: HIP takes fewer
-// than 2^32 threads along x, so past 2^22 workgroups they are laid out in
-// rows.  wide_block() is the workgroup's number; the last row may pass `blocks`.
-constexpr int64_t kWideRow = 1 << 22;
-inline dim3 wide_grid(int64_t blocks) {
-  return blocks <= kWideRow ? dim3((unsigned)blocks) : dim3((unsigned)kWideRow, (unsigned)((blocks + kWideRow - 1) / kWideRow));
-}
+inline dim3 to_dim3(const Grid& g) { return dim3((unsigned)g.x, (unsigned)g.y); }
+inline dim3 wide_grid(int64_t blocks) { return to_dim3(wide(blocks)); }
+// The workgroup's number in a wide grid.
 __device__ __forceinline__ unsigned wide_block() { return blockIdx.y * (unsigned)kWideRow + blockIdx.x; }
 constexpr int kFp8Rows = 0, kFp8Blocks = 1;  // scale layouts
 // Rotation + quantization: codes uint8 [rows, 128 kb], scale fp32 [kb, rows]

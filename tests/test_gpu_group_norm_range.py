@@ -54,6 +54,23 @@ def test_long_runs_keep_a_large_mean():
         assert bool((err <= bound(ref, amp, torch.float32)).all()), float(err.max())
 
 
+def test_a_group_per_channel_in_many_samples():
+    """More than 2^26 groups, whose chunks are joined by a wave each (2^32 threads):
+    repeated samples give repeated outputs, in place."""
+    S, reps, L, C = 1024, 418, 513, 157
+    assert S * reps * C > 1 << 26
+    x = torch.randn(S, L, C, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
+    big = x.repeat(reps, 1, 1)
+    hdq.group_norm(big, C, y=big)
+    y = hdq.group_norm(x, C)
+    ref, amp = exact(x[-1:], C, 1e-5)
+    assert bool(((y[-1:].double() - ref).abs() <= bound(ref, amp, torch.bfloat16)).all())
+    for part in big.view(reps, S, L, C).split(32):
+        assert bool((part == y).all())
+    del big, part
+    torch.cuda.empty_cache()
+
+
 # every way of the group norm: kept slabs (4, 8, 16 rows a thread), streamed
 # ones, joined chunks, three launches; vectors of 8, 4 and 1 channels, in one
 # group or several
