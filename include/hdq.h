@@ -566,7 +566,8 @@ size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y
  *             weights' had_block.
  *   w       : HDQ_FP8_BLOCKS [N, K].  K as hdq_fp8_quantize's cols; M and N
  *             any size up to HDQ_FP8_MAX_ROWS.
- *   y       : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32.
+ *   y       : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32, 16-byte aligned
+ *             (as x is).
  *   ws      : device scratch, 256-byte aligned, ws_bytes >=
  *             hdq_fp8_linear_workspace_bytes(M, K, N, y_dtype) unless xq is
  *             given.  Nothing in it needs a value before the call; calls that
@@ -593,7 +594,9 @@ int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K
  * one; these means and squared deviations are joined in float64.  Finite x of
  * any size are normalized, where weight / sqrt(var + eps) is in float32's normal
  * range and, without an eps to hide them, deviations are at least 2^-100; a NaN
- * or an infinity makes its group's outputs NaN.  Apart from y = x, no output may
+ * or an infinity makes its group's outputs NaN.  The SiLU takes the hardware's
+ * exponential and reciprocal: off by at most (2 |t| / (1 + e^t) + 6) 2^-24 of
+ * itself, and 0 where it is below 2^-119.  Apart from y = x, no output may
  * overlap an input or the scratch. */
 #define HDQ_ACT_NONE 0
 #define HDQ_ACT_SILU 1
@@ -610,7 +613,7 @@ size_t hdq_group_norm_workspace_bytes(int64_t n, int64_t length, int64_t channel
  *   groups      : divides channels (at most HDQ_GROUP_NORM_MAX_CHANNELS);
  *                 n * length at most HDQ_FP8_MAX_ROWS.
  *   weight, bias: device fp32 [channels], or NULL for 1 and 0.
- *   eps         : >= 0.
+ *   eps         : 0 to 1e30.
  *   ws, ws_bytes: device scratch, 256-byte aligned, >=
  *                 hdq_group_norm_workspace_bytes(n, length, channels, groups,
  *                 0) (NULL where that is 0).  Nothing in it needs a value

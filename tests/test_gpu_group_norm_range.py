@@ -145,3 +145,20 @@ def test_fp8_form_of_large_finite_values(n, L, C, G):
     v = (q.codes.view(torch.float8_e4m3fn).float().cpu().double() * s)[:, :C]
     tol = torch.maximum(2.0 ** -4 * (ref.abs() + slack), 2.0 ** -10 * s[:, :C]) * (1 + 2.0 ** -20) + slack
     assert bool(((v - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("n,L,C,G", [(1, 8, 4096, 64), (1, 4000, 4096, 64), (300, 200, 4096, 4096)])
+def test_silu_of_float32_outputs(n, L, C, G):
+    """A zero weight leaves the bias: y = t / (1 + e^-t) of chosen t.  e^-t =
+    2^(-t log2 e) of a float32 product (2 |t| u of itself: the product and the
+    constant rounded) and an exponential and a reciprocal of one step each (2 u),
+    a sum and a product (u): 2 |t| u e^-t / (1 + e^-t) + 6 u.  From e^-t past
+    float32 on, and where the reciprocal would be subnormal, y is 0: up to 2^-119."""
+    t = torch.cat((torch.linspace(-110, 110, C // 2), torch.linspace(-4, 4, C // 2)))
+    x = torch.randn(n, L, C, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    y = hdq.group_norm(x.to(DEV), G, torch.zeros(C, device=DEV), t.to(DEV), act=hdq.ACT_SILU, y_dtype=hdq.DTYPE_F32)
+    assert bool((y == y[0, 0]).all())
+    t = t.double()
+    ref = t * torch.sigmoid(t)
+    tol = (2 * t.abs() * torch.sigmoid(-t) + 6) * U * ref.abs() + 2.0 ** -119
+    assert bool(((y[0, 0].cpu().double() - ref).abs() <= tol).all())
