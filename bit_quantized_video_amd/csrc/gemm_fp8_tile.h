@@ -62,7 +62,10 @@ struct Fp8Operand<false> {
   }
 };
 
-// One block's 16 x 16 product.
+// One block's 16 x 16 product.  A caller reads the scaled instruction's result in
+// the basic block it is issued in (no branch between, unrolled loops only): where
+// the reader began the joining block, the compiler left too few wait states and
+// wrong values were read.
 __device__ __forceinline__ v4f block_product(const Fp8Operand<true>& w, const Fp8Operand<true>& x) {
   constexpr int kUnitScale = 0x7f7f7f7f;  // E8M0 2^0 in every byte
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, kUnitScale,
