@@ -556,6 +556,16 @@ def linear(precision, x, w, decision=None, xq=None, x_amax=None, y=None, y_dtype
 
 # ---- FP8 block-128 linear layers ----------------------------------------------
 
+def _torch_call(name, public):
+    """torch's own binding `name`, which builds no Python object on the way, or
+    `public` in a torch that lacks it."""
+    return getattr(torch._C, name, public)
+
+
+_current_device = _torch_call("_cuda_getDevice", torch.cuda.current_device)
+_current_stream = _torch_call("_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(dev, stream, call):
     """call(raw stream) with `dev` the current device and `stream` (None: the
     device's current stream) the current stream, so that what the call
@@ -563,10 +573,10 @@ def _launch(dev, stream, call):
     if dev.type != "cuda":
         raise ValueError(f"the tensors are on {dev}, not on a GPU")
     if stream is None:
-        if dev.index == torch._C._cuda_getDevice():
-            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+        if dev.index == _current_device():
+            return call(_current_stream(dev.index))
         with torch.cuda.device(dev):
-            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+            return call(_current_stream(dev.index))
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.stream(stream):

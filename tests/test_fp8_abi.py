@@ -101,6 +101,12 @@ def test_binding_scratch(hdq):
         hdq._scratch(ws, 10, torch.device("meta"))
 
 
+def test_binding_falls_back_to_public_torch_calls(hdq):
+    public = lambda: 7
+    assert hdq._torch_call("_no_such_binding", public) is public
+    assert hdq._torch_call("_cuda_getDevice", public) is getattr(torch._C, "_cuda_getDevice", public)
+
+
 def test_struct_matches_header(hdq, tmp_path):
     import os
     import shutil

@@ -57,3 +57,18 @@ def test_fp32_output(M, K, N):
     xq, wq = codes(M, K, hdq.FP8_ROWS, M + K), codes(N, K, hdq.FP8_BLOCKS, N)
     err = relative_error(hdq.fp8_linear(None, wq, xq=xq, y_dtype=hdq.DTYPE_F32), xq, wq)
     assert err <= 32 * R.blocks(K) ** 0.5 * 2.0 ** -24
+
+
+def test_public_stream_calls_give_the_same(monkeypatch):
+    """What the binding falls back to, on the current stream and within another's context."""
+    xq, wq = codes(64, 256, hdq.FP8_ROWS, 1), codes(96, 256, hdq.FP8_BLOCKS, 2)
+    want = hdq.fp8_linear(None, wq, xq=xq)
+    monkeypatch.setattr(hdq, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(hdq, "_current_stream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+    assert torch.equal(hdq.fp8_linear(None, wq, xq=xq), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y = hdq.fp8_linear(None, wq, xq=xq)
+    s.synchronize()
+    assert torch.equal(y, want)
