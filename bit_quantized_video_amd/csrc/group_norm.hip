@@ -115,6 +115,15 @@ __device__ __forceinline__ int gn_lanes(int groups, int threads) {
   return p;
 }
 
+// A pair among a workgroup's: mean and variance in float32, or with the sign set
+// the root of a variance that is not in the float32 range (or of NaN).
+__device__ __forceinline__ float2 gn_wide_pair(double mean, double var) {
+  return make_float2((float)mean, -(float)sqrt(var));
+}
+__device__ __forceinline__ double gn_pair_var(const float2& q) {
+  return q.y >= 0.0f ? (double)q.y : (double)q.y * (double)q.y;
+}
+
 // A thread's (mean, M2) of each channel of one vector over n rows.  The mean is
 // kept in float64: one workgroup may have a sample's every row, and a float32
 // mean rounded again every eight rows drifts by 2e-3 deviations over 20000 of
@@ -123,18 +132,10 @@ template <int V>
 struct GnSums {
   float n, m2[V];
   double mean[V];
-  __device__ __forceinline__ void clear() {
-    n = 0.0f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      mean[e] = 0.0;
-      m2[e] = 0.0f;
-    }
-  }
-  // Joins the first cnt (1 .. K) of K rows held in q.
+  // The mean and M2 of the first cnt (1 .. K) of K rows held in q.
   template <typename T, int K>
-  __device__ __forceinline__ void add(const GnRaw<T, V> (&q)[K], int cnt) {
-    float x0[V], m[V], d2[V];
+  static __device__ __forceinline__ void rows(const GnRaw<T, V> (&q)[K], int cnt, float (&m)[V], float (&d2)[V]) {
+    float x0[V];
     q[0].get(x0);
 #pragma unroll
     for (int e = 0; e < V; ++e) m[e] = d2[e] = 0.0f;
@@ -146,7 +147,7 @@ struct GnSums {
 #pragma unroll
         for (int e = 0; e < V; ++e) m[e] += v[e] - x0[e];
       }
-    const float k = (float)cnt, inv = 1.0f / k;
+    const float inv = 1.0f / (float)cnt;
 #pragma unroll
     for (int e = 0; e < V; ++e) m[e] = __builtin_fmaf(m[e], inv, x0[e]);
 #pragma unroll
@@ -157,7 +158,22 @@ struct GnSums {
 #pragma unroll
         for (int e = 0; e < V; ++e) d2[e] = __builtin_fmaf(v[e] - m[e], v[e] - m[e], d2[e]);
       }
-    const float f = k / (n + k), g = n * f;
+  }
+  // Begins with the first cnt rows in q.
+  template <typename T, int K>
+  __device__ __forceinline__ void start(const GnRaw<T, V> (&q)[K], int cnt) {
+    float m[V];
+    rows(q, cnt, m, m2);
+    n = (float)cnt;
+#pragma unroll
+    for (int e = 0; e < V; ++e) mean[e] = (double)m[e];
+  }
+  // Joins all K rows in q.
+  template <typename T, int K>
+  __device__ __forceinline__ void add(const GnRaw<T, V> (&q)[K]) {
+    float m[V], d2[V];
+    rows(q, K, m, d2);
+    const float k = (float)K, f = k / (n + k), g = n * f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const double d = (double)m[e] - mean[e];
@@ -167,30 +183,26 @@ struct GnSums {
     }
     n += k;
   }
-  // Whether M2 holds: not past the float32 range (then it is infinite, or NaN;
-  // NaN too for a first mean whose square is past it, times the n of 0), nor so
-  // small that squares may have underflowed.
+  // Whether M2 holds: not past the float32 range (then it is infinite, or NaN),
+  // nor so small that squares may have underflowed.
   __device__ __forceinline__ bool holds(float least) const {
     bool ok = true;
 #pragma unroll
-    for (int e = 0; e < V; ++e) ok = ok && m2[e] >= least && m2[e] < __builtin_inff();
+    for (int e = 0; e < V; ++e) ok = ok & (m2[e] >= least) & (m2[e] < __builtin_inff());
     return ok;
   }
-  // The pair of channel e, and of all V together (one group's): the mean and
-  // the root of M2 per element.
-  __device__ __forceinline__ float2 one(int e) const { return make_float2((float)mean[e], __builtin_sqrtf(m2[e] / n)); }
-  __device__ __forceinline__ float2 all() const {
-    double m = 0.0, d2 = 0.0;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) m += mean[e] - mean[0];
-    m = __builtin_fma(m, 1.0 / V, mean[0]);
+  // The pair of channel e, and of all V together (one group's), inv = 1 / n.
+  __device__ __forceinline__ float2 one(int e, float inv) const { return make_float2((float)mean[e], m2[e] * inv); }
+  __device__ __forceinline__ float2 all(float inv) const {
+    float d[V], m = 0.0f, v = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      s += m2[e] * (1.0f / V);
-      d2 = __builtin_fma(mean[e] - m, mean[e] - m, d2);  // past float32 where all of m2 holds
+      d[e] = (float)(mean[e] - mean[0]);
+      m += d[e] * (1.0f / V);
     }
-    return make_float2((float)m, (float)sqrt(__builtin_fma(d2, 1.0 / V, (double)(s / n))));
+#pragma unroll
+    for (int e = 0; e < V; ++e) v += __builtin_fmaf(d[e] - m, d[e] - m, m2[e] * inv) * (1.0f / V);
+    return make_float2((float)(mean[0] + (double)m), v);
   }
 };
 
@@ -217,42 +229,28 @@ __device__ __forceinline__ void gn_wide_sums(const T* p, int64_t step, int cnt, 
   }
 }
 
-// Sums cnt vectors at p, p + step, ...; eight loads are in flight at a time.
+// Sums cnt vectors at p, p + step, ...; eight loads are in flight at a time.  The
+// odd ones come first, where there is nothing to join them with.
 template <typename T, int V>
 __device__ __forceinline__ void gn_stream(const T* p, int64_t step, int cnt, GnSums<V>& t) {
-  int i = 0;
+  if (cnt == 0) return;
   GnRaw<T, V> q[8];
-  for (; i + 8 <= cnt; i += 8) {
+  const int head = ((cnt - 1) & 7) + 1;
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (u < head) q[u].load(p + u * step);
+  t.start(q, head);
+  for (int i = head; i < cnt; i += 8) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) q[u].load(p + (i + u) * step);
-    t.add(q, 8);
-  }
-  if (i < cnt) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (i + u < cnt) q[u].load(p + (i + u) * step);
-    t.add(q, cnt - i);
+    t.add(q);
   }
 }
 
-// Puts the pairs of a thread's sums (cnt rows at p, p + step, ...; row slot pr,
-// channel vector c of cv) among a workgroup's: one pair per thread when a vector
-// lies in one group (MERGE), else one per channel.  A pair is the mean and the
-// root of M2 per element: both are within the float32 range for any finite rows.
-template <bool MERGE, typename T, int V>
-__device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, const T* p, int64_t step, int cnt,
-                                       float least, int pr, int c, int cv) {
-  if (cnt == 0) return;
-  float2* const to = pairs + (pr * cv + c) * (MERGE ? 1 : V);
-  if (t.holds(least)) {
-    if constexpr (MERGE) {
-      to[0] = t.all();
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) to[e] = t.one(e);
-    }
-    return;
-  }
+// A thread's pairs from sums made anew in float64 (gn_put).  Out of the ordinary
+// path's way: between it and the join, these instructions cost it 0.5 us.
+template <bool MERGE, int V, typename T>
+__device__ __forceinline__ void gn_put_wide(float2* to, const T* p, int64_t step, int cnt) {
   double sd = 0.0, s2 = 0.0, ref = 0.0;  // MERGE: sums of d and M2 / cnt + d^2, d a channel's distance from ref
 #pragma nounroll
   for (int e = 0; e < V; ++e) {
@@ -264,11 +262,32 @@ __device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, const 
       sd += d;
       s2 += m2 / cnt + d * d;
     } else {
-      to[e] = make_float2((float)mean, (float)sqrt(m2 / cnt));
+      to[e] = gn_wide_pair(mean, m2 / cnt);
     }
   }
   if constexpr (MERGE)
-    to[0] = make_float2((float)(ref + sd / V), (float)sqrt(fmax(s2 / V - (sd / V) * (sd / V), 0.0) + 0.0 * s2));
+    to[0] = gn_wide_pair(ref + sd / V, fmax(s2 / V - (sd / V) * (sd / V), 0.0) + 0.0 * s2);
+}
+
+// Puts the pairs of a thread's sums (cnt rows at p, p + step, ...; row slot pr,
+// channel vector c of cv) among a workgroup's: one pair per thread when a vector
+// lies in one group (MERGE), else one per channel.
+template <bool MERGE, typename T, int V>
+__device__ __forceinline__ void gn_put(float2* pairs, const GnSums<V>& t, const T* p, int64_t step, int cnt,
+                                       float least, int pr, int c, int cv) {
+  if (cnt == 0) return;
+  float2* const to = pairs + (pr * cv + c) * (MERGE ? 1 : V);
+  const float inv = 1.0f / (float)cnt;
+  bool ok = t.holds(least);
+  if constexpr (MERGE) {
+    const float2 q = t.all(inv);
+    ok = ok & (q.y < __builtin_inff());
+    to[0] = q;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) to[e] = t.one(e, inv);
+  }
+  if (__builtin_expect(!ok, 0)) gn_put_wide<MERGE, V>(to, p, step, cnt);
 }
 // The end of a join over P lanes, from the lanes' sums of n, n d and M2 + n d^2.
 __device__ __forceinline__ void gn_join_lanes(int P, double ref, double sn, double sd, double s2, double& n,
@@ -284,8 +303,8 @@ __device__ __forceinline__ void gn_join_lanes(int P, double ref, double sn, doub
 }
 // Joins group g's pairs of row slots 0 .. slots - 1 (slot r: rows(r) rows) over
 // the P lanes of an aligned lane group, in one pass: sums of n, n d and
-// n r^2 + n d^2 in float64, r a pair's root and d the distance of its mean from
-// the first one's.
+// n (variance + d^2) in float64, d the distance of a pair's mean from the first
+// one's.
 template <bool MERGE, int V, typename Rows>
 __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg, int cv, int slots, int p, int P,
                                               Rows rows, double& n, double& mean, double& m2) {
@@ -301,7 +320,7 @@ __device__ __forceinline__ void gn_join_group(const float2* pairs, int g, int cg
     const double w = (double)(rows(r) * (MERGE ? V : 1)), d = (double)q.x - ref;
     sn += w;
     sd += w * d;
-    s2 += w * ((double)q.y * (double)q.y + d * d);
+    s2 += w * (gn_pair_var(q) + d * d);
     r += dr;
     c += dc;
     if (c >= per) {
@@ -343,7 +362,6 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_partial(const T* __restrict__
       const int64_t step = (int64_t)rpar * C;
       const int cnt = slot_rows(pr);
       GnSums<V> t;
-      t.clear();
       gn_stream<T, V>(p, step, cnt, t);
       gn_put<MERGE>(pair_s, t, p, step, cnt, least, pr, c, cv);
     }
@@ -556,12 +574,11 @@ __global__ __launch_bounds__(T) void k_gn_slab(const TI* x, int64_t length, int 
   constexpr int KEEP = ROWS > 0 ? ROWS : 1;
   GnRaw<TI, V> keep[KEEP];
   GnSums<V> t;
-  t.clear();
   if constexpr (ROWS > 0) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
       if (i < cnt) keep[i].load(x + o + i * step);
-    if (cnt > 0) t.add(keep, cnt);
+    if (cnt > 0) t.start(keep, cnt);
   } else {
     gn_stream<TI, V>(x + o, step, cnt, t);
   }
@@ -693,7 +710,6 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_short_fp8(const TI* __restric
   {
     const int pr = (int)threadIdx.x / cv, c = (int)threadIdx.x - pr * cv;
     GnSums<V> t;
-    t.clear();
     if (pr < rpar) {
       const TI* p = xs + (int64_t)pr * C + c * V;
       const int64_t step = (int64_t)rpar * C;
