@@ -6,7 +6,7 @@
 // written per element (rows), 2 and 1 (blocks); one pass over the data, since
 // a block's maximum is known within a quad of lanes or a workgroup.  Measured:
 // rows 17776 x 12288, rotated by 128, 135 us (4.9 TB/s, what a large copy
-// reaches); 226 x 1000 3.3 us (the launch); blocks 5760 x 1920 7.7 us.
+// reaches); 226 x 1000 3.3 to 3.8 us (the launch); blocks 5760 x 1920 7.7 us.
 #include "fp8_device.h"
 #include "hdq_internal.h"
 

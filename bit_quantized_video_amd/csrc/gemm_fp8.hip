@@ -11,7 +11,7 @@ namespace hdq {
 // fragments from global memory straight into registers one block ahead, and
 // the partial tiles are added over LDS in a fixed order.  Bound by the weights'
 // bytes, and for small layers by the launch: one token, 3072 -> 12288 8.4 us (4.5
-// TB/s), 12288 -> 3072 9.4, 1920 -> 5760 4.5 from codes and 5.6 from bf16.
+// TB/s), 12288 -> 3072 9.4, 1920 -> 5760 4.5 from codes and 5.5 from bf16.
 //
 // HB > 0: the activations come as bf16 and the workgroup quantizes them itself
 // (rotation block HB), into LDS, while its first weights are on their way: the
@@ -155,8 +155,10 @@ hipError_t launch_gemm_fp8_bf16(const uint16_t* x, int64_t K, int hb, const uint
 // arithmetic is much shorter than its loads' latency.  PROD: waves of their own
 // issue the loads (a wave is held up while it issues; 5-15% faster with one
 // group).  The groups' partial tiles are added over LDS in a fixed order.  Bound
-// by the latency of a stage (load, barrier, fragment reads): 226 x 4096 -> 1920
-// 8.3 us (direct loads without LDS 25.5), 1350 x 1920 -> 1024 10.0.
+// by the operands' way into LDS: 226 x 4096 -> 1920 takes 8.2 to 9.3 us (direct
+// loads without LDS 25.5), in which each of its 240 workgroups brings 478 KB, 24 to
+// 28 bytes per clock and CU, more than the large tiles reach; a fifth of that
+// are the loads past its last stage.  1350 x 1920 -> 1024: 10.0.
 template <int WM_T, int WN_T, int KW, int STAGES, bool PROD>
 struct Fp8Deep {
   static constexpr int BM = 32 * WM_T, BN = 32 * WN_T, THREADS = 256 * KW * (PROD ? 2 : 1);
@@ -348,7 +350,8 @@ static hipError_t launch_pipe(const uint8_t* xc, const float* xs, const uint8_t*
 }
 
 // Which kernel: by how many tiles of each size there are for the 256 CUs.
-// Measured on both sides of each border (us, bf16 output, N x K in brackets):
+// Measured on both sides of each border, each pair on one card, cards differing by
+// up to 10% (us, bf16 output, N x K in brackets):
 //  * up to 16 tokens: k_fp8_few 6.0, 32 x 64 tiles 5.8 (16, 5760 x 1920); one
 //    token 4.9 / 5.8.
 //  * fewer than 192 tiles of 64 x 64: 32 x 64 tiles with four K groups 6.2, 64 x

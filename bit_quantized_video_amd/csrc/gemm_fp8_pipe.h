@@ -15,11 +15,17 @@ namespace hdq {
 // in-bounds probe; 8 with the swizzle of the 32-row fragments, 16 without one).
 // The weights' scale of the wave's features is a scalar.
 //
-// Bound by operand delivery and power, not by the scaling: 256 x 256 tiles,
-// 17776 x 3072 -> 12288, bf16 output: 613-640 us, 2.1 PFLOP/s, matrix units busy
-// 0.49 of 1.4M cycles at 2.1 GHz (without the loads 570 us; a loop of products
-// and scalings alone runs at 3.7 PFLOP/s, at 1.8 GHz).  fp32 output, 17776 x 1920
-// -> 5760: 386 us, 1.0 PFLOP/s of twice the matrix work.  A 128 x 256 tile
+// At no single limit: 256 x 256 tiles, 17776 x 3072 -> 12288, bf16 output, take
+// 603 to 640 us (2.1 PFLOP/s), 1.24M cycles in which the matrix units are busy
+// for 0.52 and 18 bytes per clock and CU come in, where k_fp8_deep takes in 24 and
+// more.  A loop of products and scalings alone runs at 3.7 PFLOP/s (at 1.8 GHz),
+// the kernel without its loads in 570 us.  What is lost: the stage barrier waits
+// for every load in flight, and 3360 tiles are 14 rounds of 240 workgroups, with 16
+// CUs idle.  The clock gives way, too: an order with 10% fewer cycles took as
+// long (2.14 -> 1.98 GHz).  fp32 output, 17776 x 1920 -> 5760: 386 us, 1.0 PFLOP/s
+// of twice the matrix work; 4050 x 1920 -> 5760: matrix units busy for 0.38, 9
+// bytes per clock and CU: the conversions to bf16 and the LDS reads are not
+// hidden behind the products.  A 128 x 256 tile
 // takes 0.62 (fp32) to 0.74 of the time of a 256 x 256 one (1350 x 1920 -> 5760, one
 // round of each: 19.9 and 27.1 us); a third stage buffer, which it leaves room
 // for, changed nothing (20.8), and 128 x 128 tiles of four waves, two of them on a

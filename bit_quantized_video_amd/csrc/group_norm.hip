@@ -16,10 +16,12 @@
 // normalization.  The FP8 form codes whole rows, so it has no slab form: its
 // short samples take one launch whose workgroups each read the whole sample for
 // the statistics (k_gn_short_fp8), the others the plain form's statistics.
-// Measured: 691200 x 256 bf16 with SiLU 176 us (4.0 TB/s of bytes read and
-// written once, where a large copy reaches 4.8), 13 x 1350 x 512 17 us (9 + 8),
-// to FP8 21 (9 + 12), 2 x 77 x 300 fp32 5.5 us (one launch's latency), 225 x 320
-// to FP8 10.4 (one launch).
+// Measured: 691200 x 256 bf16 with SiLU 177 us (4.0 TB/s of bytes read and
+// written once, where a large copy reaches 4.8), 13 x 1350 x 512 17.5 us (9 + 8:
+// the statistics of 18 MB are two rounds of loads of 32-byte pieces in 416
+// workgroups), to FP8 21 (9 + 12), 2 x 77 x 300 fp32 5.9 us (one launch's
+// latency), 225 x 320 to FP8 10.9 (one launch whose 15 workgroups each read the
+// sample's 144 KB).
 //
 // Statistics: a thread takes up to 16 rows at a time into registers, sums each
 // channel's values (relative to the first) and then the squared deviations from
@@ -247,8 +249,9 @@ __device__ __forceinline__ void gn_stream(const T* p, int64_t step, int cnt, GnS
   }
 }
 
-// A thread's pairs from sums made anew in float64 (gn_put).  Out of the ordinary
-// path's way: between it and the join, these instructions cost it 0.5 us.
+// A thread's pairs from sums made anew in float64 (gn_put).  That it is there costs
+// the statistics of 13 x 1350 x 512 0.2 to 0.4 us of 9 (0.6 where the test for it
+// branched for each channel).
 template <bool MERGE, int V, typename T>
 __device__ __forceinline__ void gn_put_wide(float2* to, const T* p, int64_t step, int cnt) {
   double sd = 0.0, s2 = 0.0, ref = 0.0;  // MERGE: sums of d and M2 / cnt + d^2, d a channel's distance from ref
@@ -648,7 +651,8 @@ __device__ __forceinline__ void gn_code_chunk(float (&y)[8], bool in, int lane, 
 // numbering gives it), whose coefficients it keeps over the rows of its chunk.
 // The loads of kGnRows row groups are in flight together.  (32 channels a lane,
 // as in the quantizer, take 96 registers of coefficients: 20.1 us for 13 x 1350
-// x 512, this form 8.)
+// x 512, this form 11 to 12.)  That is 2.4 TB/s of the rows and codes: with 16
+// rows a workgroup, a lane loads 96 bytes of coefficients for 64 of x.
 template <typename TI, int HB, bool JOIN>
 __global__ __launch_bounds__(kGnCodeThreads) void k_gn_apply_fp8(const TI* __restrict__ x, int64_t length, int C, int chunks,
                                                       int64_t rows_per, GnFrom from, int act, float c_b, int kb,

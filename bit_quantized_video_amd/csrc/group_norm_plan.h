@@ -19,9 +19,11 @@ constexpr int kGnCodeThreads = 256;  // of k_gn_apply_fp8
 constexpr int kGnRows = 4;           // its row groups in flight
 
 // Chunks of a sample's rows for a pass of about `total` workgroups that take
-// `per` rows at least.  The statistics take 512, the two per CU that run at a
-// time (1 x 691200 x 256: 88 us, 1024 of them 94); the normalization 8192 (172
-// us with the statistics, 1024 of them 182).
+// `per` rows at least.  The statistics take 512, though bf16's registers leave one
+// at a time per CU: with 256 some are shorter (1 x 691200 x 256 with SiLU 166 us
+// a call, 512 of them 174) and some longer (100 x 6000 x 256, three chunks each,
+// 166 and 154; 50000 x 301 39 and 35).  The normalization takes 8192 (175 us for
+// the call above, 1024 of them 182).
 inline void gn_chunks(int64_t total, int64_t n, int64_t length, int64_t per, int64_t& chunks, int64_t& rows_per) {
   int64_t want = (total + n - 1) / n;
   if (want > (length + per - 1) / per) want = (length + per - 1) / per;
@@ -85,28 +87,29 @@ inline GnPlan gn_plan(int64_t n, int64_t length, int64_t C, int64_t groups, bool
   }
   // Kept in registers: up to 16 rows of 128 bytes or more; 8 of narrower ones,
   // whose lines several workgroups share (13 x 675 x 512, 6 rows of 32 bytes:
-  // 11.9 us, with two launches 13.6; 13 x 4000 x 512, 16 rows: 53.9 and 40.1).
+  // 10.8 us, with two launches 12.1; 13 x 4000 x 512, 16 rows of 512 threads: 53.9
+  // and 40.1).
   p.keep = p.threads == 256 && p.rows <= (p.width * (f32 ? 4 : 2) >= 128 ? kGnKeep : kGnKeep / 2);
   // A larger slab is streamed by one workgroup only where there is one for every
   // CU: with few of them the chunks' three launches are faster (1 x 16384 x 128:
-  // 15.5 us against 47.0).
+  // 12.4 us against 26.0).
   p.slab = p.keep || (p.threads == 256 && p.rows <= kGnKeep) || (p.rows <= kGnStream && n * p.slabs >= 256);
-  // As long on the GPU as two launches (225 x 320: 10.4 us and 9.8; 64 x 512: 7.5
-  // and 8.2; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
+  // About as long on the GPU as two launches (225 x 320: 10.7 us and 9.5; 64 x 512:
+  // 8.0 and 8.2; longer or wider samples lose: 225 x 1280 22.8 and 9.2), for one
   // launch's host time and no workspace.  A sample's workgroups read it again
-  // each, so either it has one (1000 x 16 x 512: 26.2 and 49.8) or all run at a
-  // time (13 x 225 x 320: 12.0 and 10.6; 64 x 225 x 320, 960 of them: 42.6 and 15.9).
+  // each, so either it has one (1000 x 16 x 512: 26.2 and 50.8) or all run at a
+  // time (13 x 225 x 320: 11.0 and 9.8; 64 x 225 x 320, 960 of them: 41.7 and 14.7).
   p.brief = C <= kGnBriefChannels && length * C <= kGnBriefSample &&
             (length <= kGnBriefRows || n * ((length + kGnBriefRows - 1) / kGnBriefRows) <= 256);
   gn_chunks(kGnMaxChunks, n, length, 8 * gn_rpar(C, p.vec), p.chunks, p.rows_per);
-  // A launch less, and no longer on the GPU: 984 x 537, one group 12.7 us, joined
-  // here 9.5; 6469 x 64 fp32 (832 pairs) 12.2 and 11.3; 2 x 3000 x 256 to FP8 16.2
-  // and 15.4.  With more rows or pairs it is longer (16384 x 128, 256 pairs 12.6
-  // and 13.9; 5000 x 256, 1280 pairs 14.4 and 16.0).
+  // A launch less, and no longer on the GPU: 984 x 537, one group 13.5 us, joined
+  // here 10.3; 6469 x 64 fp32 (832 pairs) 11.5 and 10.6; 2 x 3000 x 256 to FP8 14.1
+  // and 13.6.  With more rows or pairs it is longer (16384 x 128, 256 pairs 12.4
+  // and 13.8; 5000 x 256, 1280 pairs 12.7 and 14.7).
   p.join = !p.slab && n * length * C <= kGnJoinElements && p.chunks * groups <= kGnJoinPairs;
   gn_chunks(8192, n, length, 4 * gn_rpar(C, p.vec), p.apply_chunks, p.apply_rows);
   // One pass of a wave's loop: more rows a workgroup were slower (13 x 1350 x
-  // 512 with its statistics: 21.3 us, 32 rows 23.2; 17776 x 1280: 46.0 and 51.9),
+  // 512 with its statistics: 21.3 us, 32 rows 22.5; 17776 x 1280: 41.0 and 43.2),
   // but for a grid past kWideRow workgroups.
   const int64_t kgroups = ((C + 127) / 128 + 3) / 4, passes = (length + 4 * kGnRows - 1) / (4 * kGnRows);
   const int64_t most = std::max<int64_t>(1, kWideRow / (n * kgroups));

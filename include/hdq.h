@@ -546,7 +546,8 @@ typedef struct hdq_fp8_tensor {
  *   x        : device bf16 [rows, cols], 16-byte aligned; cols a multiple of
  *              8 and of had_block, at most HDQ_FP8_MAX_COLS; rows at most
  *              HDQ_FP8_MAX_ROWS.
- *   had_block: power of two in [1, 128]; 1 rotates nothing.
+ *   had_block: power of two in [1, 128]; 1 rotates nothing.  Sums are taken in
+ *              float32 and scaled last: one past its range makes the block NaN.
  *   out      : host struct with caller-allocated codes and scale; layout,
  *              had_block, rows, cols are written.
  */
@@ -578,7 +579,9 @@ size_t hdq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t y
  * sums run on the FP8 matrix instructions, whose products are aligned to the
  * largest one of an instruction (at least 14 fraction bits: about 1.3e-5 of
  * the result in the 2-norm, where rounding to bf16 costs 1.7e-3); with an fp32
- * output on the bf16 ones (codes are exact in bf16), with float32 sums.
+ * output on the bf16 ones (codes are exact in bf16), with float32 sums (up to
+ * 1e-7 of the result): the one to take, and round, where a bf16 result from
+ * float32 sums is wanted.
  */
 int hdq_fp8_linear(const void *x, const hdq_fp8_tensor *xq, int64_t M, int64_t K, const hdq_fp8_tensor *w,
                    void *y, int32_t y_dtype, void *ws, size_t ws_bytes, void *stream);
