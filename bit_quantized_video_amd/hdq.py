@@ -33,6 +33,16 @@ FP8_MAX_COLS, FP8_MAX_ROWS = 1 << 22, 0x7ffffc00   # HDQ_FP8_MAX_*
 # activations of the group norms
 ACT_NONE, ACT_SILU = 0, 1
 GROUP_NORM_MAX_CHANNELS = 8192   # HDQ_GROUP_NORM_MAX_CHANNELS
+# buffers of 4-bit weights
+W4_CODES, W4_SCALE, W4_ZERO = 0, 1, 2
+W4_MAX_ROWS, W4_MAX_TOKENS = 1 << 27, 1 << 20   # HDQ_W4_MAX_*
+# head norms, rotary layouts and frequency scalings, cache formats
+HEAD_MAX_DIM, HEAD_MAX_HEADS = 512, 1 << 20   # HDQ_HEAD_MAX_*
+HEAD_NORM_NONE, HEAD_NORM_LAYER, HEAD_NORM_RMS = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_MAX_AXES = 3
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_RAMP = 0, 1, 2, 3
+CACHE_INT8, CACHE_FP8, CACHE_INT4 = 0, 1, 2
 
 EXPORTS = ("hdq_select_precision", "hdq_delta_sums", "hdq_select_precision_sums",
            "hdq_select_quantize_int8", "hdq_select_quantize_int8_noalloc", "hdq_linear_dispatch", "hdq_linear_dispatch_delta",
@@ -40,6 +50,8 @@ EXPORTS = ("hdq_select_precision", "hdq_delta_sums", "hdq_select_precision_sums"
            "hdq_dq_linear", "hdq_dq_linear_workspace_bytes",
            "hdq_fp8_quantize", "hdq_fp8_linear_workspace_bytes", "hdq_fp8_linear",
            "hdq_group_norm_workspace_bytes", "hdq_group_norm", "hdq_group_norm_fp8",
+           "hdq_w4_bytes", "hdq_w4_pack", "hdq_w4_quantize", "hdq_w4_linear",
+           "hdq_rope_turns", "hdq_qk_norm_rope", "hdq_qkv_to_cache", "hdq_cache_read",
            "hdq_linear", "hdq_workspace_bytes",
            "hdq_status_string", "hdq_version")
 
@@ -79,6 +91,37 @@ class Fp8TensorDesc(_c.Structure):
     """hdq_fp8_tensor."""
     _fields_ = [("layout", _c.c_int32), ("had_block", _c.c_int32), ("rows", _c.c_int64), ("cols", _c.c_int64),
                 ("codes", _p), ("scale", _p)]
+
+
+class W4TensorDesc(_c.Structure):
+    """hdq_w4_tensor."""
+    _fields_ = [("N", _c.c_int64), ("K", _c.c_int64), ("group", _c.c_int32), ("codes", _p), ("scale", _p), ("zero", _p)]
+
+
+class HeadsDesc(_c.Structure):
+    """hdq_heads."""
+    _fields_ = [("data", _p), ("dtype", _c.c_int32), ("heads", _c.c_int32), ("batch_stride", _c.c_int64),
+                ("token_stride", _c.c_int64), ("head_stride", _c.c_int64)]
+
+
+class HeadNormDesc(_c.Structure):
+    """hdq_head_norm."""
+    _fields_ = [("kind", _c.c_int32), ("eps", _c.c_float), ("q_weight", _p), ("q_bias", _p), ("k_weight", _p),
+                ("k_bias", _p)]
+
+
+class RopeDesc(_c.Structure):
+    """hdq_rope."""
+    _fields_ = [("layout", _c.c_int32), ("dim", _c.c_int32), ("axes", _c.c_int32), ("axis_dim", _c.c_int32 * 3),
+                ("scale", _c.c_float), ("turns", _p), ("positions", _p), ("pos_axis_stride", _c.c_int64),
+                ("pos_batch_stride", _c.c_int64), ("pos_token_stride", _c.c_int64)]
+
+
+class KvCacheDesc(_c.Structure):
+    """hdq_kv_cache."""
+    _fields_ = [("fmt", _c.c_int32), ("group", _c.c_int32), ("had_block", _c.c_int32), ("heads", _c.c_int32),
+                ("dim", _c.c_int32), ("slots", _c.c_int64), ("k_codes", _p), ("k_scale", _p), ("v_codes", _p),
+                ("v_scale", _p)]
 
 
 class WeightsDesc(_c.Structure):
@@ -148,6 +191,25 @@ def _load():
     L.hdq_group_norm.argtypes = norm + [_p, _c.c_int32, _p, _c.c_size_t, _p]
     L.hdq_group_norm_fp8.restype = _c.c_int
     L.hdq_group_norm_fp8.argtypes = norm + [_c.c_int32, _c.POINTER(Fp8TensorDesc), _p, _c.c_size_t, _p]
+    L.hdq_w4_bytes.restype = _c.c_size_t
+    L.hdq_w4_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32]
+    w4 = _c.POINTER(W4TensorDesc)
+    L.hdq_w4_pack.restype = _c.c_int
+    L.hdq_w4_pack.argtypes = [_p, _p, _p, w4, _p]
+    L.hdq_w4_quantize.restype = _c.c_int
+    L.hdq_w4_quantize.argtypes = [_p, w4, _p]
+    L.hdq_w4_linear.restype = _c.c_int
+    L.hdq_w4_linear.argtypes = [_p, _c.c_int64, w4, _p, _c.c_int32, _p]
+    L.hdq_rope_turns.restype = _c.c_int
+    L.hdq_rope_turns.argtypes = [_c.c_int32, _c.c_double, _c.c_int32, _c.c_double, _c.c_double, _c.c_double,
+                                 _c.c_double, _c.POINTER(_c.c_double)]
+    heads, norm, rope, cache = (_c.POINTER(t) for t in (HeadsDesc, HeadNormDesc, RopeDesc, KvCacheDesc))
+    L.hdq_qk_norm_rope.restype = _c.c_int
+    L.hdq_qk_norm_rope.argtypes = [heads, heads, _c.c_int64, _c.c_int64, _c.c_int32, norm, rope, heads, heads, _p]
+    L.hdq_qkv_to_cache.restype = _c.c_int
+    L.hdq_qkv_to_cache.argtypes = [heads, heads, heads, _c.c_int64, _c.c_int64, norm, rope, heads, _p, cache, _p]
+    L.hdq_cache_read.restype = _c.c_int
+    L.hdq_cache_read.argtypes = [cache, _p, _c.c_int64, _p, _p, _c.c_int32, _p]
     L.hdq_workspace_bytes.restype = _c.c_size_t
     L.hdq_workspace_bytes.argtypes = [_c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32]
     L.hdq_status_string.restype = _c.c_char_p
@@ -753,4 +815,308 @@ def group_norm_fp8(x, groups, weight=None, bias=None, eps=1e-5, act=ACT_NONE, ha
         _check("hdq_group_norm_fp8", st)
         q.had_block = had_block
         return q
+    return _launch(dev, stream, call)
+
+
+# ---- linear layers of few tokens, 4-bit weights in groups ---------------------------
+
+class W4Weights:
+    """4-bit weights [N, K] with one bf16 scale (and, with zero_points, a zero
+    point) per group of 32, 64 or 128 columns of a row, packed in tiles as
+    hdq_w4_tensor describes.  w4_pack and w4_quantize make them."""
+
+    def __init__(self, N, K, group=128, zero_points=False, device=None):
+        sizes = [lib.hdq_w4_bytes(N, K, group, b) for b in (W4_CODES, W4_SCALE, W4_ZERO)]
+        if sizes[0] == 0:
+            raise ValueError(f"no 4-bit weights of {N} x {K} in groups of {group}")
+        self.N, self.K, self.group = N, K, group
+        self.codes = torch.empty(sizes[0], dtype=torch.uint8, device=device)
+        self.scale = torch.empty(sizes[1] // 2, dtype=torch.bfloat16, device=device)
+        self.zero = torch.empty(sizes[2], dtype=torch.uint8, device=device) if zero_points else None
+        self._desc = W4TensorDesc(N, K, group, self.codes.data_ptr(), self.scale.data_ptr(),
+                                  self.zero.data_ptr() if zero_points else None)
+
+    def desc(self):
+        return self._desc
+
+
+def w4_pack(codes, scale, zero=None, stream=None):
+    """hdq_w4_pack: codes uint8 [N, K / 2] (even columns in the low nibbles),
+    scale bf16 [N, K / group] and zero points uint8 [N, K / group] or None, as
+    4-bit checkpoints hold them, to W4Weights."""
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or scale.dim() != 2 or scale.shape[1] == 0:
+        raise ValueError("expected uint8 codes [N, K / 2] and scales [N, K / group]")
+    (N, half), dev = codes.shape, codes.device
+    K, group = 2 * half, 2 * half // scale.shape[1]
+    _operand(codes, "codes", torch.uint8, (N, half), dev)
+    if K % group:
+        raise ValueError(f"{scale.shape[1]} scales a row do not divide {K} columns")
+    _operand(scale, "scale", torch.bfloat16, (N, K // group), dev)
+    if zero is not None:
+        _operand(zero, "zero", torch.uint8, (N, K // group), dev)
+
+    def call(s):
+        w = W4Weights(N, K, group, zero is not None, dev)
+        _check("hdq_w4_pack", lib.hdq_w4_pack(codes.data_ptr(), scale.data_ptr(), zero.data_ptr() if zero is not None else None,
+                                              w.desc(), s))
+        return w
+    return _launch(dev, stream, call)
+
+
+def w4_quantize(w, group=128, zero_points=False, stream=None):
+    """hdq_w4_quantize: bf16 weights [N, K], rounded to nearest, to W4Weights."""
+    w = _bf16(w, "w")
+    N, K = w.shape
+
+    def call(s):
+        q = W4Weights(N, K, group, zero_points, w.device)
+        _check("hdq_w4_quantize", lib.hdq_w4_quantize(w.data_ptr(), q.desc(), s))
+        return q
+    return _launch(w.device, stream, call)
+
+
+def w4_linear(x, w, y=None, y_dtype=DTYPE_BF16, stream=None):
+    """hdq_w4_linear: Y[M, N] = X[M, K] @ W[N, K]^T, x bf16, w W4Weights."""
+    x = _bf16(x, "x")
+    (M, K), dev = x.shape, x.device
+    if K != w.K or w.codes.device != dev:
+        raise ValueError(f"the weights are {w.N} x {w.K} on {w.codes.device}, x {M} x {K} on {dev}")
+    dt = torch.float32 if y_dtype == DTYPE_F32 else torch.bfloat16
+    if y is not None:
+        _operand(y, "y", dt, (M, w.N), dev)
+
+    def call(s):
+        out = torch.empty(M, w.N, dtype=dt, device=dev) if y is None else y
+        _check("hdq_w4_linear", lib.hdq_w4_linear(x.data_ptr(), M, w.desc(), out.data_ptr(), y_dtype, s))
+        return out
+    return _launch(dev, stream, call)
+
+
+# ---- heads: norms, rotary positions, a quantized key-value cache ----------------------
+
+def rope_turns(dim, base=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0, length=0.0, ramp=(1.0, 32.0)):
+    """hdq_rope_turns: float64 [dim / 2] (on the host) of one axis' turns per
+    position; ramp is (slow, fast) of ROPE_SCALE_RAMP."""
+    out = torch.empty(max(dim, 0) // 2, dtype=torch.float64)
+    ptr = _c.cast(out.data_ptr(), _c.POINTER(_c.c_double)) if out.numel() else (_c.c_double * 1)()
+    _check("hdq_rope_turns", lib.hdq_rope_turns(dim, base, scaling, factor, length, *ramp, ptr))
+    return out
+
+
+class Rope:
+    """Rotary positions (hdq_rope without the positions): dims are the rotated
+    elements of each position axis (one to three, even), layout ROPE_HALF or
+    ROPE_INTERLEAVED; scale multiplies the rotated elements.  turns: float64
+    [sum(dims) / 2] on the device, or None for rope_turns of each axis with the
+    remaining arguments."""
+
+    def __init__(self, dims, layout=ROPE_INTERLEAVED, base=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0, length=0.0,
+                 ramp=(1.0, 32.0), scale=1.0, turns=None, device=None):
+        dims = (dims,) if isinstance(dims, int) else tuple(dims)
+        if not 1 <= len(dims) <= ROPE_MAX_AXES or any(d <= 0 or d % 2 for d in dims):
+            raise ValueError(f"rotary dims {dims}: one to {ROPE_MAX_AXES} even numbers")
+        if layout not in (ROPE_INTERLEAVED, ROPE_HALF):
+            raise ValueError(f"unknown rotary layout {layout}")
+        if turns is None:
+            turns = torch.cat([rope_turns(d, base, scaling, factor, length, ramp) for d in dims]).to(device or "cuda")
+        _operand(turns, "turns", torch.float64, (sum(dims) // 2,), turns.device)
+        self.dims, self.dim, self.axes, self.layout, self.scale, self.turns = dims, sum(dims), len(dims), layout, scale, turns
+        self._dims = (_c.c_int32 * 3)(*dims)
+        self._turns = turns.data_ptr()
+
+    def desc(self, positions, batch, length, dev):
+        """RopeDesc with positions int64 [axes, batch, length]; [batch, length] or
+        [length] for one axis and [axes, length], the same in every sequence."""
+        if positions.dtype != torch.int64 or positions.device != dev or self.turns.device != dev:
+            raise ValueError(f"positions: expected int64 on {dev}, got {positions.dtype} on {positions.device}; "
+                             f"turns on {self.turns.device}")
+        shape, st, axes = tuple(positions.shape), positions.stride(), self.axes
+        if shape == (axes, batch, length):
+            st = st
+        elif axes == 1 and shape == (batch, length):
+            st = (0, *st)
+        elif axes == 1 and shape == (length,):
+            st = (0, 0, *st)
+        elif shape == (axes, length):
+            st = (st[0], 0, st[1])
+        else:
+            raise ValueError(f"positions {shape} for {axes} axes, {batch} sequences of {length}")
+        return RopeDesc(self.layout, self.dim, axes, self._dims, self.scale, self._turns, positions.data_ptr(), *st)
+
+
+_ROW_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _head_shape(x, name):
+    """(batch, length, heads, dim) of a view [batch, length, heads, dim] or [length, heads, dim]."""
+    shape = x.shape
+    if len(shape) == 3:
+        shape = (1, *shape)
+    if len(shape) != 4:
+        raise ValueError(f"{name}: expected [batch, length, heads, dim] or [length, heads, dim], got {tuple(x.shape)}")
+    return shape
+
+
+def _heads(x, name, dev):
+    """hdq_heads of a view whose last dimension is contiguous."""
+    st, dt = x.stride(), _ROW_DTYPES.get(x.dtype)
+    if dt is None or x.device != dev or (st[-1] != 1 and x.shape[-1] != 1):
+        raise ValueError(f"{name}: expected bfloat16 or float32 on {dev} with contiguous heads, got {x.dtype} on "
+                         f"{x.device}, strides {st}")
+    return HeadsDesc(x.data_ptr(), dt, x.shape[-2], st[0] if len(st) == 4 else 0, st[-3], st[-2])
+
+
+def _head_norm(norm, eps, dim, dev, *weights):
+    if norm == HEAD_NORM_NONE:
+        return None
+    ptrs = [_operand(w, "norm weight or bias", torch.float32, (dim,), dev).data_ptr() if w is not None else None
+            for w in weights]
+    return HeadNormDesc(norm, eps, *ptrs)
+
+
+def _new_heads(out, x, dtype):
+    """out, checked against x's shape, or a new contiguous tensor (dtype None: x's)."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype if dtype is None else torch.float32 if dtype == DTYPE_F32 else torch.bfloat16,
+                           device=x.device)
+    if out.shape != x.shape:
+        raise ValueError(f"output {tuple(out.shape)} for an input {tuple(x.shape)}")
+    return out
+
+
+def _rope_desc(rope, positions, batch, length, dev):
+    if rope is None:
+        return None
+    if positions is None:
+        raise ValueError("rotary positions are missing")
+    return rope.desc(positions, batch, length, dev)
+
+
+def qk_norm_rope(q, k=None, norm=HEAD_NORM_NONE, q_weight=None, k_weight=None, q_bias=None, k_bias=None, eps=1e-6,
+                 positions=None, rope=None, q_out=None, k_out=None, y_dtype=None, stream=None):
+    """hdq_qk_norm_rope: queries [batch, length, heads, dim] (or [length, heads,
+    dim]) and, with their own number of heads, keys, normed over each head and
+    rotated.  Any strides but the last; outputs are new contiguous tensors (of
+    y_dtype, None: the input's) or q_out and k_out (which may be q and k).
+    Returns (q_out, k_out), or q_out alone without k."""
+    B, T, _, D = _head_shape(q, "q")
+    dev = q.device
+    if k is not None:
+        kb, kt, _, kd = _head_shape(k, "k")
+        if (kb, kt, kd) != (B, T, D):
+            raise ValueError(f"queries {tuple(q.shape)}, keys {tuple(k.shape)}")
+
+    def call(s):
+        qo = _new_heads(q_out, q, y_dtype)
+        ko = _new_heads(k_out, k, y_dtype) if k is not None else None
+        if B * T == 0:
+            return qo if k is None else (qo, ko)
+        st = lib.hdq_qk_norm_rope(_heads(q, "q", dev), _heads(k, "k", dev) if k is not None else None, B, T, D,
+                                  _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias),
+                                  _rope_desc(rope, positions, B, T, dev), _heads(qo, "q_out", dev),
+                                  _heads(ko, "k_out", dev) if k is not None else None, s)
+        _check("hdq_qk_norm_rope", st)
+        return qo if k is None else (qo, ko)
+    return _launch(dev, stream, call)
+
+
+def rope(x, positions, rope, out=None, y_dtype=None, stream=None):
+    """Rotary positions of one tensor [batch, length, heads, dim] (hdq_qk_norm_rope
+    without a norm); out may be x."""
+    return qk_norm_rope(x, positions=positions, rope=rope, q_out=out, y_dtype=y_dtype, stream=stream)
+
+
+class KvCache:
+    """A cache of `slots` tokens' keys and values (hdq_kv_cache): CACHE_INT8,
+    CACHE_FP8 or CACHE_INT4 codes with a float32 scale per group of elements
+    (None: the head), rotated in Hadamard blocks of had_block.  Buffers
+    (k_codes and v_codes uint8 [slots, heads, dim], or dim / 2 for INT4;
+    k_scale and v_scale float32 [slots, heads, dim / group]) are the given
+    ones or new ones on `device`, zeroed."""
+
+    def __init__(self, slots, heads, dim, fmt=CACHE_FP8, group=None, had_block=1, device=None, k_codes=None, k_scale=None,
+                 v_codes=None, v_scale=None):
+        group = dim if group is None else group
+        if fmt not in (CACHE_INT8, CACHE_FP8, CACHE_INT4) or group < 1 or dim % group or dim % 8:
+            raise ValueError(f"no cache of format {fmt}, dim {dim}, groups of {group}")
+        cshape, sshape = (slots, heads, dim // 2 if fmt == CACHE_INT4 else dim), (slots, heads, dim // group)
+        given = next((t for t in (k_codes, k_scale, v_codes, v_scale) if t is not None), None)
+        dev = given.device if given is not None else torch.device(device or "cuda")
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+
+        def buffer(t, name, dtype, shape):
+            return torch.zeros(shape, dtype=dtype, device=dev) if t is None else _operand(t, name, dtype, shape, dev)
+        self.slots, self.heads, self.dim, self.fmt, self.group, self.had_block = slots, heads, dim, fmt, group, had_block
+        self.device = dev
+        self.k_codes = buffer(k_codes, "k_codes", torch.uint8, cshape)
+        self.k_scale = buffer(k_scale, "k_scale", torch.float32, sshape)
+        self.v_codes = buffer(v_codes, "v_codes", torch.uint8, cshape)
+        self.v_scale = buffer(v_scale, "v_scale", torch.float32, sshape)
+        self._desc = KvCacheDesc(fmt, group, had_block, heads, dim, slots, self.k_codes.data_ptr(), self.k_scale.data_ptr(),
+                                 self.v_codes.data_ptr(), self.v_scale.data_ptr())
+
+    def desc(self):
+        return self._desc
+
+
+def _slots(slots, n, dev):
+    if slots.dtype != torch.int64 or slots.numel() != n or not slots.is_contiguous() or slots.device != dev:
+        raise ValueError(f"slots: expected {n} contiguous int64 on {dev}, got {slots.dtype} {tuple(slots.shape)} on {slots.device}")
+    return slots.data_ptr()
+
+
+def qkv_to_cache(cache, q, k, v, slots, norm=HEAD_NORM_NONE, q_weight=None, k_weight=None, q_bias=None, k_bias=None, eps=1e-6,
+                 positions=None, rope=None, q_out=None, y_dtype=None, stream=None):
+    """hdq_qkv_to_cache: queries normed and rotated, keys normed, rotated and
+    quantized into the cache's slots (int64 [batch * length]), values quantized
+    as they are.  Views as qk_norm_rope's.  Returns q_out (None without q)."""
+    B, T, Hk, D = _head_shape(k, "k")
+    dev = k.device
+    for t, name in ((v, "v"), (q, "q")):
+        if t is None:
+            if name == "v":
+                raise ValueError("v is missing")
+            continue
+        b, n, h, d = _head_shape(t, name)
+        if (b, n, d) != (B, T, D) or (name == "v" and h != Hk):
+            raise ValueError(f"{name} {tuple(t.shape)}, keys {tuple(k.shape)}")
+    if (Hk, D) != (cache.heads, cache.dim) or cache.device != dev:
+        raise ValueError(f"keys {tuple(k.shape)} on {dev}, a cache of {cache.heads} heads of {cache.dim} on {cache.device}")
+
+    def call(s):
+        qo = _new_heads(q_out, q, y_dtype) if q is not None else None
+        if B * T == 0:
+            return qo
+        st = lib.hdq_qkv_to_cache(_heads(q, "q", dev) if q is not None else None, _heads(k, "k", dev), _heads(v, "v", dev),
+                                  B, T, _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias),
+                                  _rope_desc(rope, positions, B, T, dev), _heads(qo, "q_out", dev) if q is not None else None,
+                                  _slots(slots, B * T, dev), cache.desc(), s)
+        _check("hdq_qkv_to_cache", st)
+        return qo
+    return _launch(dev, stream, call)
+
+
+def cache_write(cache, k, v, slots, stream=None):
+    """Keys and values as they are, quantized into the cache's slots
+    (hdq_qkv_to_cache without queries, norm and rotation)."""
+    qkv_to_cache(cache, None, k, v, slots, stream=stream)
+
+
+def cache_read(cache, slots, k_out=None, v_out=None, y_dtype=DTYPE_BF16, stream=None):
+    """hdq_cache_read: (keys, values) [tokens, heads, dim] of slots (int64
+    [tokens]), new or k_out and v_out; slots that are not there read zeros."""
+    n, dev = slots.numel(), cache.device
+    shape, dt = (n, cache.heads, cache.dim), torch.float32 if y_dtype == DTYPE_F32 else torch.bfloat16
+    sp = _slots(slots, n, dev)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _operand(t, name, dt, shape, dev)
+
+    def call(s):
+        ko = torch.empty(shape, dtype=dt, device=dev) if k_out is None else k_out
+        vo = torch.empty(shape, dtype=dt, device=dev) if v_out is None else v_out
+        if n:
+            _check("hdq_cache_read", lib.hdq_cache_read(cache.desc(), sp, n, ko.data_ptr(), vo.data_ptr(), y_dtype, s))
+        return ko, vo
     return _launch(dev, stream, call)

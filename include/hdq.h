@@ -640,6 +640,217 @@ int hdq_group_norm_fp8(const void *x, int32_t x_dtype, int64_t n, int64_t length
                        const float *weight, const float *bias, float eps, int32_t act, int32_t had_block,
                        hdq_fp8_tensor *out, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- linear layers of few tokens with 4-bit weights in groups ----------------
+ * y[m, n] = sum over groups g of s[n, g] sum_{k in g} (u[n, k] - z[n, g]) x[m, k]:
+ * activations stay bf16, weights are codes u of 0 to 15 with one bf16 scale s
+ * and, optionally, a zero point z (0 to 255; 8 without) for each group of 32,
+ * 64 or 128 columns of a row.  For one to a few dozen tokens (conditioning
+ * vectors, single-token serving), where reading the weights is what takes the
+ * time; any number of tokens is taken.
+ *
+ * A tensor [N, K] is kept packed in tiles of 16 rows x 128 columns, both
+ * rounded up (hdq_w4_pack and hdq_w4_quantize write it, padding included):
+ *   codes : device, hdq_w4_bytes(..., HDQ_W4_CODES) bytes, 16-byte aligned;
+ *   scale : device bf16, hdq_w4_bytes(..., HDQ_W4_SCALE) bytes, 8-byte aligned;
+ *   zero  : NULL, or device, hdq_w4_bytes(..., HDQ_W4_ZERO) bytes, 4-byte aligned.
+ * N at most HDQ_W4_MAX_ROWS, K a multiple of 32 and of the group, at most
+ * HDQ_FP8_MAX_COLS. */
+#define HDQ_W4_CODES 0
+#define HDQ_W4_SCALE 1
+#define HDQ_W4_ZERO 2
+#define HDQ_W4_MAX_ROWS (1 << 27)
+#define HDQ_W4_MAX_TOKENS (1 << 20)
+typedef struct hdq_w4_tensor {
+  int64_t N;
+  int64_t K;
+  int32_t group;
+  uint8_t *codes;
+  uint16_t *scale;
+  uint8_t *zero;
+} hdq_w4_tensor;
+
+/* Bytes of one of a packed tensor's buffers; 0 on bad arguments. */
+size_t hdq_w4_bytes(int64_t N, int64_t K, int32_t group, int32_t buffer);
+
+/*
+ * hdq_w4_pack -- weights as 4-bit checkpoints hold them, into tiles.
+ *   codes : device uint8 [N, K / 2], the even column in the low nibble.
+ *   scale : device bf16 [N, K / group].
+ *   zero  : device uint8 [N, K / group]; given exactly when out->zero is.
+ *   out   : N, K, group and the buffers set by the caller.
+ */
+int hdq_w4_pack(const uint8_t *codes, const void *scale, const uint8_t *zero, const hdq_w4_tensor *out, void *stream);
+
+/*
+ * hdq_w4_quantize -- bf16 weights [N, K] (16-byte aligned), rounded to nearest.
+ * Without out->zero s = bf16(max|w| / 7), u = clamp(rne(w / s) + 8, 0, 15); with it
+ * s = bf16((max - min) / 15), z = rne(-min / s), u = clamp(rne(w / s) + z, 0, 15),
+ * 0 counted among the values.  A group whose scale would be below 2^-100 gets
+ * s = 0; one with a NaN or an infinity s = NaN.
+ */
+int hdq_w4_quantize(const void *w, const hdq_w4_tensor *out, void *stream);
+
+/*
+ * hdq_w4_linear
+ *   x : device bf16 [M, K], 16-byte aligned; M 0 (nothing is done) to
+ *       HDQ_W4_MAX_TOKENS.
+ *   y : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32, aligned to an element.
+ * A group's sum is taken in float32 on the matrix instructions, as
+ * sum (16 + u) x - (16 + z) sum x with exact products, and scaled and added in
+ * float32; the error is that of a float32 sum over terms (32 + z) / |u - z| times
+ * as large.  No workspace.
+ */
+int hdq_w4_linear(const void *x, int64_t M, const hdq_w4_tensor *w, void *y, int32_t y_dtype, void *stream);
+
+/* ---- heads: norms, rotary positions, a quantized key-value cache ---------------
+ * What lies between a QKV projection and the attention.  A tensor of heads is
+ * a view [batch, length, heads, dim] of bf16 or fp32 elements, dim (1 to
+ * HDQ_HEAD_MAX_DIM) contiguous and the other strides free, in elements: the
+ * slice of a projection's output that holds the queries, say.  Bases and
+ * strides of whole 16 bytes, and dim a multiple of 8, are the fast ones.
+ * batch * length is 0 (nothing is done) to HDQ_FP8_MAX_ROWS, heads of a call
+ * together at most HDQ_HEAD_MAX_HEADS.  An output may be its own input (same
+ * type and strides); otherwise nothing written may overlap anything read. */
+#define HDQ_HEAD_MAX_DIM 512
+#define HDQ_HEAD_MAX_HEADS (1 << 20)
+typedef struct hdq_heads {
+  void *data;           /* device                                          */
+  int32_t dtype;        /* HDQ_DTYPE_BF16 or HDQ_DTYPE_F32                 */
+  int32_t heads;
+  int64_t batch_stride; /* in elements, >= 0; of an output that has more   */
+  int64_t token_stride; /* than one element along it, >= dim               */
+  int64_t head_stride;
+} hdq_heads;
+
+/* Norm over each head's dim elements, in float32, then weight and bias:
+ *   LAYER: (x - mean) / sqrt(var + eps) w + b;  RMS: x / sqrt(mean(x^2) + eps) w + b.
+ * weight, bias: device fp32 [dim], or NULL for 1 and 0.  eps 0 to 1e30; a
+ * head of zeros stays zero at eps 0.  Finite heads of any size are normed
+ * (sums that leave float32's range are taken again, scaled); a NaN or an
+ * infinity makes its head NaN.  A layer norm's deviations are those from the
+ * mean rounded to float32. */
+#define HDQ_HEAD_NORM_NONE 0
+#define HDQ_HEAD_NORM_LAYER 1
+#define HDQ_HEAD_NORM_RMS 2
+typedef struct hdq_head_norm {
+  int32_t kind;
+  float eps;
+  const float *q_weight;
+  const float *q_bias;
+  const float *k_weight;
+  const float *k_bias;
+} hdq_head_norm;
+
+/* Rotary positions: of a head's first `dim` elements (even), pair j -- elements
+ * 2j and 2j + 1 (INTERLEAVED) or j and j + dim / 2 (HALF) -- is turned by
+ * t = 2 pi frac(p turns[j]): (a, b) <- scale (a cos t - b sin t, b cos t + a sin t).
+ * p is the token's position on the pair's axis: the first axis_dim[0] / 2 pairs
+ * belong to axis 0, the next axis_dim[1] / 2 to axis 1, and so on (axis_dim of
+ * the `axes` axes add up to dim).  A token with a negative position on any
+ * axis is not rotated (text tokens in front of a video's).  p turns[j] is taken
+ * in float64 in two parts, so its fraction is off by the rounding of turns[j]
+ * alone, p 2^-53 turns[j]; cosine and sine are float32. */
+#define HDQ_ROPE_INTERLEAVED 0
+#define HDQ_ROPE_HALF 1
+#define HDQ_ROPE_MAX_AXES 3
+typedef struct hdq_rope {
+  int32_t layout;
+  int32_t dim;             /* rotated elements, 0: none (the rest is ignored) */
+  int32_t axes;            /* 1 to HDQ_ROPE_MAX_AXES                          */
+  int32_t axis_dim[3];
+  float scale;
+  const double *turns;     /* device [dim / 2], turns per position            */
+  const int64_t *positions; /* device, element (axis, batch, token) at        */
+  int64_t pos_axis_stride; /* axis pos_axis_stride + ...                      */
+  int64_t pos_batch_stride;
+  int64_t pos_token_stride;
+} hdq_rope;
+
+/* Frequencies on the host: turns[j] = base^(-2 j / dim) / (2 pi), j < dim / 2, with
+ * one axis' dim, and a long context's scaling:
+ *   NONE;
+ *   LINEAR: all divided by factor;
+ *   BASE  : base times factor^(dim / (dim - 2)), so that the slowest pair is
+ *           divided by factor and the fastest kept (dim > 2);
+ *   RAMP  : turns[j] / factor where a pair makes at most `slow` turns over
+ *           `length` positions (the context trained on), turns[j] from `fast`
+ *           turns on, and the blend linear in the turns between.
+ * factor >= 1; length, slow, fast (0 <= slow < fast) count for RAMP alone.
+ * Writes float64 [dim / 2] to host memory. */
+#define HDQ_ROPE_SCALE_NONE 0
+#define HDQ_ROPE_SCALE_LINEAR 1
+#define HDQ_ROPE_SCALE_BASE 2
+#define HDQ_ROPE_SCALE_RAMP 3
+int hdq_rope_turns(int32_t dim, double base, int32_t scaling, double factor, double length, double slow, double fast,
+                   double *turns_host);
+
+/*
+ * hdq_qk_norm_rope -- queries and keys normed and rotated in one pass.
+ *   q, k         : inputs of the same dtype, batch, length and dim; k (and
+ *                  k_out) may be NULL for one tensor alone.
+ *   norm         : NULL or kind NONE: not normed.
+ *   rope         : NULL or dim 0: not rotated.
+ *   q_out, k_out : of the same dtype as each other, heads as q's and k's.
+ */
+int hdq_qk_norm_rope(const hdq_heads *q, const hdq_heads *k, int64_t batch, int64_t length, int32_t dim,
+                     const hdq_head_norm *norm, const hdq_rope *rope, const hdq_heads *q_out,
+                     const hdq_heads *k_out, void *stream);
+
+/* A cache of keys and values, `slots` tokens of heads x dim elements each, in
+ * 8 or 4 bits.  dim is a multiple of 8, at most HDQ_HEAD_MAX_DIM; a group of
+ * elements (dim itself, or a power of two from 8 on that divides it) shares an
+ * fp32 scale; had_block (a power of two to 128 that divides dim, 1: none) is
+ * the block Hadamard rotation the elements are stored with.
+ *   codes : device uint8 [slots, heads, dim] (INT8, FP8: E4M3) or
+ *           [slots, heads, dim / 2] (INT4, even element in the low nibble, two's
+ *           complement), 8-byte aligned.
+ *   scale : device fp32 [slots, heads, dim / group].
+ * With y the rotated values and a = max|y| of a group: scale = fl32(a / top), code =
+ * rne(y * fl32(top / a)), top 127, 448 (E4M3 nearest, ties to even) or 7.  A group
+ * with a < 2^-100 gets scale 0 and zero codes, one with a NaN or an infinity
+ * scale NaN and zero codes. */
+#define HDQ_CACHE_INT8 0
+#define HDQ_CACHE_FP8 1
+#define HDQ_CACHE_INT4 2
+typedef struct hdq_kv_cache {
+  int32_t fmt;
+  int32_t group;
+  int32_t had_block;
+  int32_t heads;
+  int32_t dim;
+  int64_t slots;
+  uint8_t *k_codes;
+  float *k_scale;
+  uint8_t *v_codes;
+  float *v_scale;
+} hdq_kv_cache;
+
+/*
+ * hdq_qkv_to_cache -- the same pass with the keys, normed and rotated, and the
+ * values, as they are, quantized into the cache.
+ *   q, q_out : NULL for keys and values alone.
+ *   k, v     : [batch, length, cache heads, dim] of q's dtype.
+ *   slots    : device int64 [batch * length], each token's slot; tokens with a
+ *              slot below 0 or past the cache's are left out (their queries are
+ *              still written).  Slots of one call are distinct: of two tokens
+ *              with one slot the outcome is a mix.
+ * Slots not named keep their codes and scales.
+ */
+int hdq_qkv_to_cache(const hdq_heads *q, const hdq_heads *k, const hdq_heads *v, int64_t batch, int64_t length,
+                     const hdq_head_norm *norm, const hdq_rope *rope, const hdq_heads *q_out,
+                     const int64_t *slots, const hdq_kv_cache *cache, void *stream);
+
+/*
+ * hdq_cache_read -- slots' keys and values, rotated back.
+ *   slots        : device int64 [tokens] (0 to HDQ_FP8_MAX_ROWS of them); a
+ *                  slot may come more than once, one below 0 or past the
+ *                  cache's reads zeros.
+ *   k_out, v_out : device [tokens, heads, dim], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32,
+ *                  16-byte aligned.
+ */
+int hdq_cache_read(const hdq_kv_cache *cache, const int64_t *slots, int64_t tokens, void *k_out, void *v_out,
+                   int32_t y_dtype, void *stream);
+
 /* Scratch bytes an entry point needs.  op = HDQ_OP_SELECT: (M = rows,
  * K = cols, N = prev_numel); HDQ_OP_SELECT_Q8: (M = rows, K = cols);
  * HDQ_OP_QUANTIZE: (M = rows, K = cols, fmt);
