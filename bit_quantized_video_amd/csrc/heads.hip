@@ -296,7 +296,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
           float a = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            y[e] = g.hb > 1 ? y[e] * sc : y[e];
+            y[e] = g.hb > 1 ? fmaf(y[e], sc, 0.0f) : y[e];  // a difference of 0 has either sign: + 0 is coded
             a = __builtin_elementwise_maximum(a, fabsf(y[e]));
           }
           float scale, inv;

@@ -1,0 +1,201 @@
+"""The quantized key-value cache on the GPU: codes and scales bit for bit for
+keys and values as they are, within the norm's and rotation's bounds in the
+fused pass; reading back bit for bit; slots, ranges, streams, graphs."""
+import math
+
+import pytest
+import torch
+
+import heads_ref as R
+from test_gpu_heads import BF, DEV, F32, KIND, make, plan, positions, reference, weights
+
+pytestmark = pytest.mark.gpu
+from bit_quantized_video_amd import hdq  # noqa: E402
+
+FMT = {"int8": hdq.CACHE_INT8, "fp8": hdq.CACHE_FP8, "int4": hdq.CACHE_INT4}
+
+
+def filled(slots, heads, dim, fmt, group, had, seed):
+    """A cache of random codes and scales, and its buffers' copies."""
+    g = torch.Generator().manual_seed(seed)
+    bufs = {}
+    for n in ("k", "v"):
+        q, s = R.encode(torch.randn(slots, heads, dim, generator=g), fmt, group, had)
+        bufs[n + "_codes"], bufs[n + "_scale"] = R.to_bytes(q, fmt).contiguous(), s
+    c = hdq.KvCache(slots, heads, dim, FMT[fmt], group, had, **{k: v.clone().to(DEV) for k, v in bufs.items()})
+    return c, bufs
+
+
+SHAPES = [(64, 64, 64), (64, 16, 1), (128, 32, 128), (128, 128, 16), (96, 96, 32), (96, 32, 8), (72, 72, 8), (256, 64, 128),
+          (512, 512, 128), (8, 8, 8), (40, 8, 1), (320, 64, 64), (80, 80, 1)]
+
+
+@pytest.mark.parametrize("dim,group,had", SHAPES)
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "int4"])
+def test_write_and_read(dim, group, had, fmt):
+    slots, heads, T = 37, 3, 11
+    c, bufs = filled(slots, heads, dim, fmt, group, had, 1)
+    k, v = make((T, heads, dim), BF, 2, 3.0), make((T, heads, dim), BF, 3, 0.1)
+    g = torch.Generator().manual_seed(4)
+    at = torch.randperm(slots, generator=g)[:T]
+    at[3], at[7] = -1, slots                      # left out
+    live = (at >= 0) & (at < slots)
+    hdq.cache_write(c, k.to(DEV), v.to(DEV), at.to(DEV))
+    for n, x in (("k", k), ("v", v)):
+        q, s = R.encode(x.float(), fmt, group, had)
+        bufs[n + "_codes"][at[live]] = R.to_bytes(q, fmt)[live]
+        bufs[n + "_scale"][at[live]] = s[live]
+        assert torch.equal(getattr(c, n + "_codes").cpu(), bufs[n + "_codes"])
+        assert torch.equal(getattr(c, n + "_scale").cpu(), bufs[n + "_scale"])
+    ids = torch.cat((torch.arange(slots), at, torch.tensor([0, 0, -5, 1 << 40])))
+    for code, dt in ((hdq.DTYPE_BF16, BF), (hdq.DTYPE_F32, F32)):
+        got = hdq.cache_read(c, ids.to(DEV), y_dtype=code)
+        for y, n in zip(got, ("k", "v")):
+            want = R.decode(R.from_bytes(bufs[n + "_codes"], fmt), bufs[n + "_scale"], group, had).to(dt)
+            there = (ids >= 0) & (ids < slots)
+            want = torch.where(there[:, None, None], want[ids.clamp(0, slots - 1)], torch.zeros((), dtype=dt))
+            assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk", [(1, 1, 30, 30), (1, 1, 1, 1), (3, 5, 8, 2), (2, 300, 5, 1), (4, 1, 64, 8), (1, 40, 0, 3)])
+@pytest.mark.parametrize("dim,dims,split,group,had,fmt,kind", [
+    (64, (64,), True, 64, 64, "fp8", "rms"), (64, (16, 24, 24), False, 32, 1, "int8", "layer"), (128, (96,), True, 128, 128, "int4", "rms"),
+    (80, (40,), True, 80, 16, "fp8", "layer"), (96, (48,), False, 32, 32, "int4", "none"), (256, (256,), True, 64, 64, "int8", "rms")])
+def test_step(B, T, Hq, Hk, dim, dims, split, group, had, fmt, kind):
+    n = B * T
+    slots = n + 9
+    c, bufs = filled(slots, Hk, dim, fmt, group, had, 5)
+    qkv = make((B, T, Hq + 2 * Hk, dim), BF, 6)
+    q, k, v = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hk], qkv[:, :, Hq + Hk:]
+    (qw, qb), (kw, kb) = weights(dim, 7), weights(dim, 8)
+    pos = positions(len(dims), B, T, 9, text=1 if T > 3 else 0)
+    turns, r = plan(dims, split)
+    at = torch.randperm(slots, generator=torch.Generator().manual_seed(10))[:n]
+    if n > 5:
+        at[5] = -1
+    dev = qkv.to(DEV)
+    out = hdq.qkv_to_cache(c, dev[:, :, :Hq] if Hq else None, dev[:, :, Hq:Hq + Hk], dev[:, :, Hq + Hk:], at.to(DEV), KIND[kind],
+                           *[t.to(DEV) for t in (qw, kw, qb, kb)], positions=pos.to(DEV), rope=r)
+    if Hq:
+        assert R.close(out, *reference(q, kind, qw, qb, 1e-6, dims, split, turns, pos, 1.0))
+    else:
+        assert out is None
+    live = at >= 0
+    for name, x in (("k", k), ("v", v)):
+        ref, tol = reference(k, kind, kw, kb, 1e-6, dims, split, turns, pos, 1.0) if name == "k" else (
+            x.double(), torch.zeros(x.shape, dtype=torch.float64))
+        z, bound = R.code_bound(ref.flatten(0, 1), tol.flatten(0, 1), fmt, group, had)
+        codes, scale = getattr(c, name + "_codes").cpu(), getattr(c, name + "_scale").cpu()
+        val = R.from_bytes(codes, fmt).double() * scale.double().repeat_interleave(group, 2)
+        assert bool(((val[at[live]] - z[live]).abs() <= bound[live]).all())
+        rest = torch.ones(slots, dtype=torch.bool)
+        rest[at[live]] = False
+        assert torch.equal(codes[rest], bufs[name + "_codes"][rest]) and torch.equal(scale[rest], bufs[name + "_scale"][rest])
+
+
+def test_step_equals_its_parts():
+    """The fused pass against the norm and rotation to float32, then the cache."""
+    B, T, H, dim = 2, 33, 4, 64
+    x = make((B, T, 3 * H, dim), F32, 11).to(DEV)
+    q, k, v = x[:, :, :H], x[:, :, H:2 * H], x[:, :, 2 * H:]
+    pos = positions(3, B, T, 12, text=4).to(DEV)
+    _, r = plan((16, 24, 24), False)
+    at = torch.randperm(100, device=DEV)[:B * T]
+    a, b = (hdq.KvCache(100, H, dim, hdq.CACHE_INT8, 32, 64, device=DEV) for _ in range(2))
+    qo, ko = hdq.qk_norm_rope(q, k, hdq.HEAD_NORM_LAYER, positions=pos, rope=r)
+    hdq.cache_write(a, ko, v, at)
+    qf = hdq.qkv_to_cache(b, q, k, v, at, hdq.HEAD_NORM_LAYER, positions=pos, rope=r)
+    assert torch.equal(qo, qf)
+    for n in ("k_codes", "k_scale", "v_codes", "v_scale"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "int4"])
+@pytest.mark.parametrize("had", [1, 32])
+def test_values_outside_the_range(fmt, had):
+    """Groups of zeros, of tiny values, of large ones, and with NaN or infinities."""
+    k = make((1, 7, 2, 64), F32, 13)
+    k[0, 0, 0], k[0, 1], k[0, 2], k[0, 5, 0] = 0, k[0, 1] * 1e-36, k[0, 2] * 1e30, k[0, 5, 0] * 2.0 ** -99
+    k[0, 3, 0, 3], k[0, 4, 1, 40], k[0, 6, 0, 63] = math.nan, math.inf, -math.inf
+    c = hdq.KvCache(7, 2, 64, FMT[fmt], 32, had, device=DEV)
+    c.k_codes.fill_(0x55)
+    hdq.cache_write(c, k.to(DEV), k.to(DEV), torch.arange(7, device=DEV))
+    q, s = R.encode(k[0], fmt, 32, had)
+    assert torch.equal(c.k_codes.cpu(), R.to_bytes(q, fmt)) and torch.equal(c.k_codes, c.v_codes)
+    assert torch.equal(torch.isnan(c.k_scale.cpu()), torch.isnan(s)) and int(torch.isnan(s).sum()) == 3
+    assert torch.equal(torch.nan_to_num(c.k_scale.cpu(), 7.0), torch.nan_to_num(s, 7.0))
+    y, _ = hdq.cache_read(c, torch.arange(7, device=DEV), y_dtype=hdq.DTYPE_F32)
+    assert torch.equal(torch.isnan(y.cpu()), torch.isnan(s).repeat_interleave(32, 2))
+
+
+def test_views_and_unaligned():
+    """Keys and values with any strides (element loads), the cache's own alignment kept."""
+    T, H, dim = 6, 3, 64
+    flat = make((2 * T * H * dim + 1,), BF, 14)
+    x = flat[1:].view(2, H, T, dim).transpose(1, 2)      # [2, T, H, dim], odd base
+    k, v = x[:1], x[1:]
+    dev = flat.to(DEV)[1:].view(2, H, T, dim).transpose(1, 2)
+    c = hdq.KvCache(T, H, dim, hdq.CACHE_FP8, 64, 64, device=DEV)
+    hdq.cache_write(c, dev[:1], dev[1:], torch.arange(T, device=DEV))
+    for n, t in (("k", k), ("v", v)):
+        q, s = R.encode(t[0].float(), "fp8", 64, 64)
+        assert torch.equal(getattr(c, n + "_codes").cpu(), R.to_bytes(q, "fp8")) and torch.equal(getattr(c, n + "_scale").cpu(), s)
+
+
+def test_stream_and_graph():
+    """A token a replay: slot, position and input change, the graph does not."""
+    H, dim = 5, 64
+    c, w = (hdq.KvCache(20, H, dim, hdq.CACHE_INT4, 32, 32, device=DEV) for _ in range(2))
+    qkv = make((1, 1, 3 * H, dim), BF, 15).to(DEV)
+    slot, pos = torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    ids = torch.arange(20, device=DEV)
+    _, r = plan((dim,), True)
+
+    def step(cache, **kw):
+        q, k, v = qkv[:, :, :H], qkv[:, :, H:2 * H], qkv[:, :, 2 * H:]
+        y = hdq.qkv_to_cache(cache, q, k, v, slot, hdq.HEAD_NORM_RMS, positions=pos, rope=r, **kw)
+        return (y, *hdq.cache_read(cache, ids, **kw))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(c, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step(w)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(c)
+    for i in range(4):
+        qkv.copy_(make(qkv.shape, BF, 40 + i))
+        slot.fill_(3 * i + 1)
+        pos.fill_(100 * i)
+        want = step(w)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_cache_past_32_bits():
+    """Slots whose codes lie past 2^32 bytes."""
+    H, dim = 64, 512
+    slots = (1 << 32) // (H * dim) + 5
+    c = hdq.KvCache(slots, H, dim, hdq.CACHE_FP8, 128, 128, device=DEV)
+    k, v = make((4, H, dim), BF, 16), make((4, H, dim), BF, 17)
+    at = torch.tensor([slots - 1, 0, slots - 2, 1 << 16])
+    hdq.cache_write(c, k.to(DEV), v.to(DEV), at.to(DEV))
+    got = hdq.cache_read(c, at.to(DEV))
+    for y, x, n in zip(got, (k, v), ("k", "v")):
+        q, s = R.encode(x.float(), "fp8", 128, 128)
+        assert torch.equal(getattr(c, n + "_codes")[at.to(DEV)].cpu(), R.to_bytes(q, "fp8"))
+        assert torch.equal(y.cpu(), R.decode(q, s, 128, 128).to(BF))
+
+
+def test_empty():
+    c = hdq.KvCache(4, 2, 64, device=DEV)
+    none = torch.empty(0, dtype=torch.int64, device=DEV)
+    x = torch.empty(0, 2, 64, dtype=BF, device=DEV)
+    hdq.cache_write(c, x, x, none)
+    assert hdq.cache_read(c, none)[0].shape == (0, 2, 64) and not bool(c.k_scale.any())
+    empty = hdq.KvCache(0, 2, 64, device=DEV)     # no slots: nothing is written, zeros are read
+    one = torch.zeros(1, dtype=torch.int64, device=DEV)
+    y = make((1, 2, 64), BF, 18).to(DEV)
+    with pytest.raises(hdq.HdqError):
+        hdq.cache_write(empty, y, y, one)
