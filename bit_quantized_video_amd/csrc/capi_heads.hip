@@ -100,6 +100,7 @@ HeadRows rows(const hdq_heads* in, const hdq_heads* out, const float* weight, co
   HeadRows r{};
   if (in != nullptr) r.x = in->data, r.xb = in->batch_stride, r.xt = in->token_stride, r.xh = in->head_stride;
   if (out != nullptr) r.y = out->data, r.yb = out->batch_stride, r.yt = out->token_stride, r.yh = out->head_stride;
+  r.heads = in != nullptr ? in->heads : 0;
   r.weight = weight;
   r.bias = bias;
   return r;
@@ -218,8 +219,6 @@ int hdq_qk_norm_rope(const hdq_heads* q, const hdq_heads* k, int64_t batch, int6
   HeadArgs g{};
   g.q = rows(q, q_out, norm ? norm->q_weight : nullptr, norm ? norm->q_bias : nullptr);
   g.k = rows(k, k_out, norm ? norm->k_weight : nullptr, norm ? norm->k_bias : nullptr);
-  g.heads[0] = q->heads;
-  g.heads[1] = g.heads[2] = q->heads + (k ? k->heads : 0);
   g.tokens = batch * length;
   g.length = length;
   g.dim = dim;
@@ -255,9 +254,6 @@ int hdq_qkv_to_cache(const hdq_heads* q, const hdq_heads* k, const hdq_heads* v,
   g.q = rows(q, q_out, norm ? norm->q_weight : nullptr, norm ? norm->q_bias : nullptr);
   g.k = rows(k, nullptr, norm ? norm->k_weight : nullptr, norm ? norm->k_bias : nullptr);
   g.v = rows(v, nullptr, nullptr, nullptr);
-  g.heads[0] = q ? q->heads : 0;
-  g.heads[1] = g.heads[0] + k->heads;
-  g.heads[2] = g.heads[1] + v->heads;
   g.tokens = batch * length;
   g.length = length;
   g.dim = dim;
@@ -267,7 +263,6 @@ int hdq_qkv_to_cache(const hdq_heads* q, const hdq_heads* k, const hdq_heads* v,
   g.fmt = cache->fmt;
   g.group = cache->group;
   g.groups = dim / cache->group;
-  g.group_bits = cache_group_bits(dim, cache->group);
   g.hb = cache->had_block;
   g.c_b = hadamard_scale(g.hb);
   g.top = cache_top(g.fmt);

@@ -19,11 +19,11 @@ struct HeadRows {
   int64_t yb, yt, yh;
   const float* weight;
   const float* bias;
+  int heads;
 };
 
 struct HeadArgs {
   HeadRows q, k, v;
-  int heads[3];  // of q; of q and k; of q, k and v
   int64_t tokens, length;
   int dim;
   bool y_f32;
@@ -45,7 +45,7 @@ struct HeadArgs {
   uint8_t* codes[2];
   float* scales[2];
   // the plan's
-  int lane_bits, slot_bits, steps, slices;
+  int lane_bits, slot_bits, steps, slices, step_end[3];
 };
 
 // Reading slots back: token t's keys and values go to row t of the outputs.
@@ -58,14 +58,12 @@ struct CacheReadArgs {
   int heads, dim, fmt, group, groups, hb;
   float c_b;
   bool y_f32;
-  int lane_bits, slot_bits, steps, slices;
+  int lane_bits, slot_bits, steps, slices, step_end[3];
 };
 
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s);
 hipError_t launch_cache_read(CacheReadArgs g, hipStream_t s);
 
-// Lanes of a group: all of a head's when the group is the head, else group / 8.
-inline int cache_group_bits(int dim, int group) { return bits_for(((group == dim ? dim : group) + 7) / 8); }
 inline float cache_top(int fmt) { return fmt == kCacheInt8 ? 127.0f : fmt == kCacheFp8 ? kFp8Max : 7.0f; }
 
 // Sum over the 2^bits lanes (aligned) that hold a head; the same in each.
@@ -100,32 +98,28 @@ __device__ __forceinline__ void code_scales(float a, float top, float& scale, fl
   inv = live ? top / a : 0.0f;
 }
 
-// Eight integer codes of y * inv, rounded to even, |code| <= top; inv 0: zeros.
-__device__ __forceinline__ void int_codes(const float (&y)[8], float inv, float top, int (&q)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = inv != 0.0f ? (int)fminf(fmaxf(rintf(y[e] * inv), -top), top) : 0;
-}
-
-// Codes the lane's chunk at element `at` (a multiple of 8) of a cache's codes.
+// Codes the lane's chunk at element `at` (a multiple of 8) of a cache's codes,
+// rounded to even; inv 0 gives zeros whatever y holds.  Integers: adding
+// 1.5 2^23 leaves the rounded value in the sum's low bits, two's complement;
+// |y * inv| passes top by less than half.
 __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t at, const float (&y)[8], float inv, int fmt) {
   if (fmt == kCacheFp8) {
     *reinterpret_cast<uint2*>(codes + at) = fp8_encode8(y, inv);
     return;
   }
-  int q[8];
-  int_codes(y, inv, fmt == kCacheInt8 ? 127.0f : 7.0f, q);
+  uint32_t q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(y[e] * inv + 12582912.0f);
+  // bytes of four elements: v_perm takes byte 0 of each
+  const auto bytes = [&](int a, int b, int c, int d) {
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[d], q[c], 0x0c0c0400u), __builtin_amdgcn_perm(q[b], q[a], 0x0c0c0400u), 0x05040100u);
+  };
   if (fmt == kCacheInt8) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[i] = (uint32_t)(q[4 * i] & 255) | (uint32_t)(q[4 * i + 1] & 255) << 8 | (uint32_t)(q[4 * i + 2] & 255) << 16 |
-             (uint32_t)q[4 * i + 3] << 24;
-    *reinterpret_cast<uint2*>(codes + at) = make_uint2(w[0], w[1]);
+    const uint32_t lo = bytes(0, 1, 2, 3), hi = bytes(4, 5, 6, 7);
+    *reinterpret_cast<uint2*>(codes + at) = inv != 0.0f ? make_uint2(lo, hi) : make_uint2(0u, 0u);
   } else {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w |= (uint32_t)(q[e] & 15) << (4 * e);
-    *reinterpret_cast<uint32_t*>(codes + at / 2) = w;
+    const uint32_t w = (bytes(0, 2, 4, 6) & 0x0f0f0f0fu) | (bytes(1, 3, 5, 7) & 0x0f0f0f0fu) << 4;
+    *reinterpret_cast<uint32_t*>(codes + at / 2) = inv != 0.0f ? w : 0u;
   }
 }
 

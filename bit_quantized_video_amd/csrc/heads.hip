@@ -21,7 +21,7 @@ namespace hdq {
 namespace {
 
 constexpr int kWaves = 4;        // waves of a workgroup
-constexpr int kUnroll = 4;       // head steps whose loads are in flight together
+constexpr int kUnroll = 2;       // head steps whose loads are in flight together
 constexpr int kMaxPairs = 256;   // rotated pairs a wave's tokens have (dim 512, or more tokens of smaller heads)
 
 // Eight elements, the chunk a lane holds, as loaded.
@@ -95,52 +95,113 @@ __device__ __forceinline__ void store_chunk(void* p, bool f32, const float (&y)[
   }
 }
 
-// A head's scale 1 / sqrt(mean square + eps) and its centred values in place.
-// Sums outside what float32 squares hold (and NaN, infinities) are taken
-// again from values scaled by a power of two, which cancels in the result;
-// a head with a NaN or an infinity becomes NaN.
-__device__ __forceinline__ float head_norm(float (&x)[8], int n, bool layer, float inv_dim, float eps, int ll) {
-  float raw[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) raw[e] = x[e];
-  float scaled_eps = eps, ss = 0.0f;
-  for (int pass = 0; pass < 2; ++pass) {
-    if (layer) {
-      float s = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-      const float mean = lanes_sum(s, ll) * inv_dim;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] - mean : 0.0f;
-    }
-    float a = x[0] * x[0], b = x[1] * x[1];
-#pragma unroll
-    for (int e = 2; e < 8; e += 2) {
-      a = fmaf(x[e], x[e], a);
-      b = fmaf(x[e + 1], x[e + 1], b);
-    }
-    ss = lanes_sum(a + b, ll);
-    const bool ok = ss < 0x1p100f && (ss > 0x1p-80f || eps > 0x1p-60f);
-    if (pass == 1 || __ballot(!ok) == 0) break;
-    float m = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(raw[e]));
-    m = lanes_max(m, ll);
-    int k = 0;
-    if (m > 0.0f && m < __builtin_inff()) k = ilogbf(fmaxf(m, sqrtf(eps))) + 1;
-    if (ok) k = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = ldexpf(raw[e], -k);
-    scaled_eps = ldexpf(ldexpf(eps, -k), -k);
-    if (!(m < __builtin_inff())) scaled_eps = __builtin_nanf("");
-  }
-  const float d = ss * inv_dim + scaled_eps;
-  return d == 0.0f ? 0.0f : rsqrtf(d);  // a head of zeros stays zero at eps 0
+__device__ __forceinline__ float sum8(const float (&x)[8]) {
+  return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 
-template <bool F32, bool VEC, bool CACHE>
+__device__ __forceinline__ float squares8(const float (&x)[8]) {
+  float a = x[0] * x[0], b = x[1] * x[1];
+#pragma unroll
+  for (int e = 2; e < 8; e += 2) {
+    a = fmaf(x[e], x[e], a);
+    b = fmaf(x[e + 1], x[e + 1], b);
+  }
+  return a + b;
+}
+
+// Centres the lane's n elements (layer) and returns the head's sum of squares.
+__device__ __forceinline__ float centred_squares(float (&x)[8], int n, bool layer, float inv_dim, int ll) {
+  if (layer) {
+    const float mean = lanes_sum(sum8(x), ll) * inv_dim;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] - mean : 0.0f;
+  }
+  return lanes_sum(squares8(x), ll);
+}
+
+// The power of two that brings a head of largest magnitude m, and eps with it, near 1.
+__device__ __forceinline__ int norm_exponent(float m, float eps) {
+  const float big = fmaxf(m, sqrtf(eps));
+  return big > 0.0f && big < __builtin_inff() ? ilogbf(big) + 1 : 0;
+}
+
+// Whether a sum of squares is one that float32 holds well.
+__device__ __forceinline__ bool squares_hold(float ss, float eps) { return ss < 0x1p100f && (ss > 0x1p-80f || eps > 0x1p-60f); }
+
+// 1 / sqrt(mean square + eps); sums outside that range come scaled, so the
+// argument is normal (or 0: a head of zeros stays zero at eps 0).
+__device__ __forceinline__ float norm_scale(float ss, float inv_dim, float eps) {
+  const float d = fmaf(ss, inv_dim, eps);
+  return d == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(d);
+}
+
+// A head's scale and its centred values in place.  Sums that do not hold
+// are taken again from values scaled by a power of two, which cancels in the
+// result; a head with a NaN or an infinity becomes NaN.
+template <bool F32>
+__device__ __forceinline__ float head_norm(const Chunk<F32>& raw, float (&x)[8], int n, bool layer, float inv_dim,
+                                           float eps, int ll) {
+  float ss = centred_squares(x, n, layer, inv_dim, ll);
+  const bool ok = squares_hold(ss, eps);
+  if (__ballot(!ok) != 0) {
+    float v[8], m = 0.0f;
+    raw.to_f32(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(v[e]));
+    m = lanes_max(m, ll);
+    const int k = norm_exponent(m, eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
+    const float again = centred_squares(v, n, layer, inv_dim, ll);
+    if (!ok) {
+      ss = again;
+      eps = m < __builtin_inff() ? ldexpf(ldexpf(eps, -k), -k) : __builtin_nanf("");
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = v[e];
+    }
+  }
+  return norm_scale(ss, inv_dim, eps);
+}
+
+// LDS between lanes of one wave: what was written is there, and stays until read.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// What a chunk's elements allow: element loads and any rotation; vector loads;
+// and also a rotation whose pairs are whole chunks
+// (k_heads), or whole heads on 16 elements a lane (k_heads16).
+enum Mode : int { kElements = 0, kVectors = 1, kChunks = 2, kPairs = 3 };
+
+// Scaled cosine and sine of pair j at a token's positions.
+__device__ __forceinline__ float2 pair_angle(const HeadArgs& g, int64_t p0, int64_t p1, int64_t p2, int j) {
+  const double p = (double)(j < g.axis_end[0] ? p0 : j < g.axis_end[1] ? p1 : p2);
+  const double f = g.turns[j];
+  const double t = p * f, lost = fma(p, f, -t);  // the product in two parts
+  const float r = (float)((t - rint(t)) + lost);
+  float s, co;
+  sincospif(2.0f * r, &s, &co);
+  return make_float2(co * g.scale, s * g.scale);
+}
+
+// Weights and biases of a lane's chunk (null: 1 and 0), aligned to an element.
+__device__ __forceinline__ void load_weights(const float* p, int at, float other, float (&w)[8]) {
+  if (p != nullptr) {
+    __builtin_memcpy(w, p + at, 32);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = other;
+  }
+}
+
+template <bool F32, int MODE, bool CACHE>
 __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
-  __shared__ float2 s_trig[kWaves][kMaxPairs];
+  constexpr bool VEC = MODE != kElements;
+  __shared__ __align__(16) float2 s_trig[kWaves][kMaxPairs];
   __shared__ __align__(16) float s_swap[kWaves][64 * 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // 32 bits hold the wave's number: one token a wave at most, and slices only with few tokens
   const uint32_t work = wide_block() * kWaves + wave;
   const uint32_t tgroup = work / (uint32_t)g.slices;
@@ -151,10 +212,36 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
   const int64_t first = (int64_t)tgroup * (64 >> (ll + sl)), token = first + (lane >> (ll + sl));
   if (first >= g.tokens) return;  // whole waves
-  const bool in_token = token < g.tokens;
-  const uint32_t tok = in_token ? (uint32_t)token : 0u, bi = tok / (uint32_t)g.length, ti = tok - bi * (uint32_t)g.length;
+  const uint32_t tok = token < g.tokens ? (uint32_t)token : 0u, bi = tok / (uint32_t)g.length, ti = tok - bi * (uint32_t)g.length;
   const int n = min(8, g.dim - c * 8);  // the lane's elements, <= 0 past the head
-  const bool in_head = n > 0;
+  const bool in = token < g.tokens && n > 0;
+
+  // Steps: 2^sl heads of a tensor each, the queries' first.  A step's tensor is
+  // the same for the whole wave.
+  const int step0 = slice * g.steps, step1 = min(step0 + g.steps, g.step_end[2]);
+  auto tensor = [&](int s) { return s < g.step_end[0] ? 0 : !CACHE || s < g.step_end[1] ? 1 : 2; };
+  auto block = [&](int t, int s) { return (s - (t == 0 ? 0 : t == 1 ? g.step_end[0] : g.step_end[1])) << sl; };
+  auto rows = [&](int t) -> const HeadRows& { return t == 0 ? g.q : !CACHE || t == 1 ? g.k : g.v; };
+  constexpr int kIn = F32 ? 4 : 2;
+  const int out_size = g.y_f32 ? 4 : 2;
+
+  int x_of = -1;  // whose lane base this is
+  const char* x_base = nullptr;
+  auto load = [&](Chunk<F32>& raw, int s) {
+    raw.zero();
+    if (s >= step1) return;
+    const int t = tensor(s), h0 = block(t, s);
+    const HeadRows& r = rows(t);
+    if (t != x_of) {
+      x_of = t;
+      x_base = static_cast<const char*>(r.x) + (bi * r.xb + ti * r.xt + hslot * r.xh + c * 8) * kIn;
+    }
+    if (in && h0 + hslot < r.heads) raw.template load<VEC>(x_base + h0 * r.xh * kIn, n);
+  };
+
+  Chunk<F32> raw[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) load(raw[u], step0 + u);
 
   // angles of the wave's tokens: pair j of a token by lane j, j + lanes, ... of it
   float cs[8], sn[8];
@@ -170,174 +257,422 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
     }
     const int per = 1 << (ll + sl);
     float2* trig = s_trig[wave] + (lane >> (ll + sl)) * g.half;
-    for (int j = lane & (per - 1); j < g.half; j += per) {
-      const double p = (double)(j < g.axis_end[0] ? pos[0] : j < g.axis_end[1] ? pos[1] : pos[2]);
-      const double f = g.turns[j];
-      const double t = p * f, lost = fma(p, f, -t);  // the product in two parts
-      const float r = (float)((t - rint(t)) + lost);
-      float s, co;
-      sincospif(2.0f * r, &s, &co);
-      trig[j] = make_float2(co * g.scale, s * g.scale);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos[0], pos[1], pos[2], j);
+    wave_lds_fence();
+    if (g.split) {  // element i of pair i or i - half, the sine negative for the first
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = c * 8 + e;
-      const int j = g.split ? (i < g.half ? i : i - g.half) : (c * 4 + (e >> 1));
-      const float2 v = j < g.half ? trig[j] : make_float2(1.0f, 0.0f);
-      cs[e] = v.x;
-      // y[i] = x[i] cos + x[partner] sin, the sine negative for a pair's first element
-      sn[e] = (g.split ? i < g.half : (e & 1) == 0) ? -v.y : v.y;
+      for (int e = 0; e < 8; ++e) {
+        const int i = c * 8 + e, j = i < g.half ? i : i - g.half;
+        const float2 v = j < g.half ? trig[j] : make_float2(1.0f, 0.0f);
+        cs[e] = v.x;
+        sn[e] = i < g.half ? -v.y : v.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = c * 4 + e;
+        const float2 v = j < g.half ? trig[j] : make_float2(1.0f, 0.0f);
+        cs[e] = v.x;
+        sn[e] = v.y;
+      }
     }
+    if (MODE == kChunks) live = live && c * 8 < 2 * g.half;
   }
-
-  // head h of the call is head h - start of one of its tensors
-  constexpr int kIn = F32 ? 4 : 2;
-  const int out_size = g.y_f32 ? 4 : 2;
-  const char* qx = static_cast<const char*>(g.q.x) + (bi * g.q.xb + ti * g.q.xt + c * 8) * kIn;
-  const char* kx = static_cast<const char*>(g.k.x) + (bi * g.k.xb + ti * g.k.xt + c * 8) * kIn;
-  const char* vx = CACHE ? static_cast<const char*>(g.v.x) + (bi * g.v.xb + ti * g.v.xt + c * 8) * kIn : nullptr;
-  char* qy = static_cast<char*>(g.q.y) + (bi * g.q.yb + ti * g.q.yt + c * 8) * out_size;
-  char* ky = CACHE ? nullptr : static_cast<char*>(g.k.y) + (bi * g.k.yb + ti * g.k.yt + c * 8) * out_size;
-  const int heads = g.heads[2];
-  auto tensor = [&](int h) { return h < g.heads[0] ? 0 : !CACHE || h < g.heads[1] ? 1 : 2; };
-  auto start = [&](int t) { return t == 0 ? 0 : !CACHE || t == 1 ? g.heads[0] : g.heads[1]; };
 
   float wt[8], bs[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) wt[e] = 1.0f, bs[e] = 0.0f;
-  int loaded = -1;  // whose weights these are
-  const int64_t slot = CACHE && in_token ? g.slots[tok] : -1;
+  int w_of = -1, y_of = -1;  // whose weights, whose lane base
+  char* y_base = nullptr;
+  const int64_t slot = CACHE && in ? g.slots[tok] : -1;
   const bool in_cache = slot >= 0 && slot < g.n_slots;
 
-  for (int i0 = 0; i0 < g.steps; i0 += kUnroll) {
-    Chunk<F32> raw[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = (slice * g.steps + i0 + u) << sl | hslot;
-      raw[u].zero();
-      if (i0 + u < g.steps && h < heads && in_token && in_head) {
-        const int t = tensor(h);
-        const int64_t xh = t == 0 ? g.q.xh : !CACHE || t == 1 ? g.k.xh : g.v.xh;
-        raw[u].template load<VEC>((t == 0 ? qx : !CACHE || t == 1 ? kx : vx) + (h - start(t)) * xh * kIn, n);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (i0 + u >= g.steps) break;
-      const int h = (slice * g.steps + i0 + u) << sl | hslot;
-      const bool ok = h < heads && in_token && in_head;
-      const int t = tensor(h);
-      float x[8];
-      raw[u].to_f32(x);
-      const bool plain = t == 2;  // values: neither norm nor rotation
-      if (g.norm != 0 && __ballot(!plain) != 0) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
-        const float r = head_norm(y, n, g.norm == 1, g.inv_dim, g.eps, ll);
-        if (!plain && loaded != t && in_head) {
-          loaded = t;
-          const float* w = t == 0 ? g.q.weight : g.k.weight;
-          const float* b = t == 0 ? g.q.bias : g.k.bias;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            wt[e] = w != nullptr && e < n ? w[c * 8 + e] : 1.0f;
-            bs[e] = b != nullptr && e < n ? b[c * 8 + e] : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = plain ? x[e] : fmaf(y[e] * r, wt[e], bs[e]);
-      }
-      if (g.half > 0) {
-        float p[8];
-        if (g.split) {
-          float* sw = s_swap[wave] + (lane >> ll << ll) * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sw[c * 8 + e] = x[e];
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-          __builtin_amdgcn_wave_barrier();
-          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-          if (g.half % 4 == 0) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const int i = c * 8 + e;
-              const float4 v = *reinterpret_cast<const float4*>(sw + (i < g.half ? i + g.half : i < 2 * g.half ? i - g.half : i));
-              p[e] = v.x, p[e + 1] = v.y, p[e + 2] = v.z, p[e + 3] = v.w;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int i = c * 8 + e;
-              p[e] = sw[i < g.half ? i + g.half : i < 2 * g.half ? i - g.half : i];
-            }
-          }
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-          __builtin_amdgcn_wave_barrier();
+  auto process = [&](const Chunk<F32>& raw, int s) {
+    const int t = tensor(s), h = block(t, s) + hslot;
+    const HeadRows& r = rows(t);
+    const bool ok = in && h < r.heads;
+    float x[8];
+    raw.to_f32(x);
+    if (g.norm != kHeadNormNone && t != 2) {
+      if (w_of != t) {
+        w_of = t;
+        if (VEC) {
+          load_weights(r.weight, n > 0 ? c * 8 : 0, 1.0f, wt);
+          load_weights(r.bias, n > 0 ? c * 8 : 0, 0.0f, bs);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool turn = live && !plain && (g.split ? c * 8 + e < 2 * g.half : c * 4 + (e >> 1) < g.half);
-          x[e] = turn ? fmaf(p[e], sn[e], x[e] * cs[e]) : x[e];
+          for (int e = 0; e < 8; ++e) {
+            wt[e] = r.weight != nullptr && e < n ? r.weight[c * 8 + e] : 1.0f;
+            bs[e] = r.bias != nullptr && e < n ? r.bias[c * 8 + e] : 0.0f;
+          }
         }
       }
-      if (CACHE) {
-        const bool coded = t != 0;
-        if (__ballot(coded) != 0) {
-          float y[8];
+      const float rs = head_norm<F32>(raw, x, n, g.norm == kHeadNormLayer, g.inv_dim, g.eps, ll);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e];
-          const float sc = fwht8(y, lane, g.hb) * g.c_b;
-          float a = 0.0f;
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e] * rs, wt[e], bs[e]);
+    }
+    if (g.half > 0 && t != 2) {
+      if (g.split) {
+        float p[8];
+        float* sw = s_swap[wave] + (lane >> ll << ll) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sw[c * 8 + e] = x[e];
+        wave_lds_fence();
+        if (MODE == kChunks || g.half % 4 == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const int i = c * 8 + e;
+            const float4 v = *reinterpret_cast<const float4*>(sw + (i < g.half ? i + g.half : i < 2 * g.half ? i - g.half : i));
+            p[e] = v.x, p[e + 1] = v.y, p[e + 2] = v.z, p[e + 3] = v.w;
+          }
+        } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            y[e] = g.hb > 1 ? fmaf(y[e], sc, 0.0f) : y[e];  // a difference of 0 has either sign: + 0 is coded
-            a = __builtin_elementwise_maximum(a, fabsf(y[e]));
-          }
-          float scale, inv;
-          code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
-          if (coded && ok && in_cache) {
-            const int64_t row = slot * (heads - g.heads[1]) + (h - start(t));
-            store_codes(t == 1 ? g.codes[0] : g.codes[1], row * g.dim + c * 8, y, inv, g.fmt);
-            if ((c * 8) % g.group == 0) (t == 1 ? g.scales[0] : g.scales[1])[row * g.groups + c * 8 / g.group] = scale;
+            const int i = c * 8 + e;
+            p[e] = sw[i < g.half ? i + g.half : i < 2 * g.half ? i - g.half : i];
           }
         }
-        if (coded) continue;
-      }
-      if (ok) {
-        char* y = t == 0 ? qy : ky;
-        store_chunk<VEC>(y + (h - start(t)) * (t == 0 ? g.q.yh : g.k.yh) * out_size, g.y_f32, x, n);
+        wave_lds_fence();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (MODE == kChunks || c * 8 + e < 2 * g.half) x[e] = fmaf(p[e], sn[e], x[e] * cs[e]);
+        }
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (MODE == kChunks || c * 4 + e < g.half) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = fmaf(-b, sn[e], a * cs[e]);
+            x[2 * e + 1] = fmaf(a, sn[e], b * cs[e]);
+          }
       }
     }
+    if (CACHE && t != 0) {
+      const float sc = fwht8(x, lane, g.hb) * g.c_b;
+      float a = 0.0f;
+      if (g.hb > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], sc, 0.0f);  // a difference of 0 has either sign: + 0 is coded
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = __builtin_elementwise_maximum(a, fabsf(x[e]));
+      float scale, inv;
+      code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
+      if (ok && in_cache) {
+        const int64_t row = slot * r.heads + h;
+        store_codes(g.codes[t - 1], row * g.dim + c * 8, x, inv, g.fmt);
+        if ((c * 8) % g.group == 0) g.scales[t - 1][row * g.groups + c * 8 / g.group] = scale;
+      }
+    } else {
+      if (y_of != t) {
+        y_of = t;
+        y_base = static_cast<char*>(r.y) + (bi * r.yb + ti * r.yt + hslot * r.yh + c * 8) * out_size;
+      }
+      if (ok) store_chunk<VEC>(y_base + (h - hslot) * r.yh * out_size, g.y_f32, x, n);
+    }
+  };
+
+  for (int s = step0; s < step1; s += kUnroll) {
+    Chunk<F32> now[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) load(raw[u], s + kUnroll + u);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (s + u < step1) process(now[u], s + u);
   }
+}
+
+// The same for heads of 16 elements a lane, most calls' form: a lane holds
+// chunks c and c + dim / 16 of a head, so both elements of a pair, in either
+// layout, are its own, and a step's addresses, reductions and tests serve
+// twice the elements (half the instructions an element).  dim is a
+// multiple of 16 on LL bits of lanes (LL < 0: g.lane_bits), the rotation none,
+// interleaved in whole chunks or split over the whole head, a Hadamard block
+// and a group within half a head or the whole.
+template <bool F32, int LL, bool CACHE>
+__global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
+  __shared__ __align__(16) float2 s_trig[kWaves][2 * kMaxPairs];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t work = wide_block() * kWaves + wave;
+  const uint32_t tgroup = work / (uint32_t)g.slices;
+  const int slice = (int)(work - tgroup * (uint32_t)g.slices);
+  const int ll = LL < 0 ? g.lane_bits : LL, sl = g.slot_bits;
+  const int far = g.dim >> 4;  // chunks from a lane's first to its second
+  const int hb1 = CACHE ? min(g.hb, g.dim >> 1) : 1;
+  const int c = CACHE ? (int)fwht_src(lane & ((1 << ll) - 1), lane, hb1) : lane & ((1 << ll) - 1);
+  const int hslot = (lane >> ll) & ((1 << sl) - 1);
+  const int64_t first = (int64_t)tgroup * (64 >> (ll + sl)), token = first + (lane >> (ll + sl));
+  if (first >= g.tokens) return;  // whole waves
+  const uint32_t tok = token < g.tokens ? (uint32_t)token : 0u, bi = tok / (uint32_t)g.length, ti = tok - bi * (uint32_t)g.length;
+  const bool in = token < g.tokens && c < far;
+
+  const int step0 = slice * g.steps, step1 = min(step0 + g.steps, g.step_end[2]);
+  auto tensor = [&](int s) { return s < g.step_end[0] ? 0 : !CACHE || s < g.step_end[1] ? 1 : 2; };
+  auto block = [&](int t, int s) { return (s - (t == 0 ? 0 : t == 1 ? g.step_end[0] : g.step_end[1])) << sl; };
+  auto rows = [&](int t) -> const HeadRows& { return t == 0 ? g.q : !CACHE || t == 1 ? g.k : g.v; };
+  constexpr int kIn = F32 ? 4 : 2;
+  const int out_size = g.y_f32 ? 4 : 2;
+
+  struct Pair {
+    Chunk<F32> a, b;
+  };
+  int x_of = -1;  // whose lane base this is
+  const char* x_base = nullptr;
+  auto load = [&](Pair& raw, int s) {
+    raw.a.zero();
+    raw.b.zero();
+    if (s >= step1) return;
+    const int t = tensor(s), h0 = block(t, s);
+    const HeadRows& r = rows(t);
+    if (t != x_of) {
+      x_of = t;
+      x_base = static_cast<const char*>(r.x) + (bi * r.xb + ti * r.xt + hslot * r.xh + c * 8) * kIn;
+    }
+    if (in && h0 + hslot < r.heads) {
+      const char* p = x_base + h0 * r.xh * kIn;
+      raw.a.template load<true>(p, 8);
+      raw.b.template load<true>(p + far * (8 * kIn), 8);
+    }
+  };
+
+  Pair raw[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) load(raw[u], step0 + u);
+
+  // angles of the wave's tokens, as above; cs, sn: of the lane's eight pairs
+  float cs[8], sn[8];
+  bool live = false, live2 = false;
+  if (g.half > 0) {
+    const int64_t* pp = g.positions + bi * g.pos_batch + ti * g.pos_token;
+    int64_t pos[3];
+    live = true;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+      pos[a] = a < g.axes ? pp[a * g.pos_axis] : 0;
+      live = live && pos[a] >= 0;
+    }
+    const int per = 1 << (ll + sl);
+    float2* trig = s_trig[wave] + (lane >> (ll + sl)) * g.half;
+    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos[0], pos[1], pos[2], j);
+    wave_lds_fence();
+    const int j0 = g.split ? c * 8 : c * 4, j1 = g.split ? c * 8 + 4 : (c + far) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = j0 + e < g.half ? trig[j0 + e] : make_float2(1.0f, 0.0f);
+      const float2 w = j1 + e < g.half ? trig[j1 + e] : make_float2(1.0f, 0.0f);
+      cs[e] = v.x, sn[e] = v.y;
+      cs[4 + e] = w.x, sn[4 + e] = w.y;
+    }
+    live2 = live && (c + far) * 8 < 2 * g.half;  // interleaved: each chunk is turned or not
+    live = live && c * 8 < 2 * g.half;
+  }
+
+  float wt[2][8], bs[2][8];
+  int w_of = -1, y_of = -1;  // whose weights, whose lane base
+  char* y_base = nullptr;
+  const int64_t slot = CACHE && in ? g.slots[tok] : -1;
+  const bool in_cache = slot >= 0 && slot < g.n_slots;
+
+  auto process = [&](const Pair& raw, int s) {
+    const int t = tensor(s), h = block(t, s) + hslot;
+    const HeadRows& r = rows(t);
+    const bool ok = in && h < r.heads;
+    float x[8], y[8];
+    raw.a.to_f32(x);
+    raw.b.to_f32(y);
+    if (g.norm != kHeadNormNone && t != 2) {
+      if (w_of != t) {
+        w_of = t;
+        const int at = c < far ? c * 8 : 0;
+        load_weights(r.weight, at, 1.0f, wt[0]);
+        load_weights(r.weight, at + far * 8, 1.0f, wt[1]);
+        load_weights(r.bias, at, 0.0f, bs[0]);
+        load_weights(r.bias, at + far * 8, 0.0f, bs[1]);
+      }
+      float eps = g.eps;
+      auto squares = [&]() {
+        if (g.norm == kHeadNormLayer) {
+          const float mean = lanes_sum(sum8(x) + sum8(y), ll) * g.inv_dim;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = x[e] - mean;
+            y[e] = y[e] - mean;
+          }
+          const float q = squares8(x) + squares8(y);
+          return lanes_sum(c < far ? q : 0.0f, ll);  // lanes past the head hold -mean
+        }
+        return lanes_sum(squares8(x) + squares8(y), ll);
+      };
+      float ss = squares();
+      const bool holds = squares_hold(ss, eps);
+      if (__ballot(!holds) != 0) {
+        float keep[2][8], m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) keep[0][e] = x[e], keep[1][e] = y[e];
+        raw.a.to_f32(x);
+        raw.b.to_f32(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, __builtin_elementwise_maximum(fabsf(x[e]), fabsf(y[e])));
+        m = lanes_max(m, ll);
+        const int k = norm_exponent(m, eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = ldexpf(x[e], -k), y[e] = ldexpf(y[e], -k);
+        const float again = squares();
+        if (holds) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = keep[0][e], y[e] = keep[1][e];
+        } else {
+          ss = again;
+          eps = m < __builtin_inff() ? ldexpf(ldexpf(eps, -k), -k) : __builtin_nanf("");
+        }
+      }
+      const float rs = norm_scale(ss, g.inv_dim, eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = fmaf(x[e] * rs, wt[0][e], bs[0][e]);
+        y[e] = fmaf(y[e] * rs, wt[1][e], bs[1][e]);
+      }
+    }
+    if (g.half > 0 && t != 2) {
+      if (g.split) {
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = y[e];
+            x[e] = fmaf(-b, sn[e], a * cs[e]);
+            y[e] = fmaf(a, sn[e], b * cs[e]);
+          }
+        }
+      } else {
+        auto turn = [&](float (&v)[8], int at) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = v[2 * e], b = v[2 * e + 1];
+            v[2 * e] = fmaf(-b, sn[at + e], a * cs[at + e]);
+            v[2 * e + 1] = fmaf(a, sn[at + e], b * cs[at + e]);
+          }
+        };
+        if (live) turn(x, 0);
+        if (live2) turn(y, 4);
+      }
+    }
+    if (CACHE && t != 0) {
+      if (g.hb > 1) {
+        float sc = fwht8(x, lane, hb1) * g.c_b;
+        fwht8(y, lane, hb1);
+        if (g.hb != hb1) {  // the last stage, half a head apart
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = y[e];
+            x[e] = a + b;
+            y[e] = a - b;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // + 0: a difference of 0 has either sign, + 0 is coded
+          x[e] = fmaf(x[e], sc, 0.0f);
+          y[e] = fmaf(y[e], sc, 0.0f);
+        }
+      }
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a = __builtin_elementwise_maximum(a, fabsf(x[e]));
+        b = __builtin_elementwise_maximum(b, fabsf(y[e]));
+      }
+      const bool whole = g.group == g.dim;
+      if (whole) a = __builtin_elementwise_maximum(a, b);
+      float scale, inv, scale2, inv2;
+      code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
+      if (whole)
+        scale2 = scale, inv2 = inv;
+      else
+        code_scales(lanes_max(b, g.group_bits), g.top, scale2, inv2);
+      if (ok && in_cache) {
+        const int64_t row = slot * r.heads + h;
+        store_codes(g.codes[t - 1], row * g.dim + c * 8, x, inv, g.fmt);
+        store_codes(g.codes[t - 1], row * g.dim + (c + far) * 8, y, inv2, g.fmt);
+        float* to = g.scales[t - 1] + row * g.groups;
+        if (whole) {
+          if (c == 0) to[0] = scale;
+        } else if ((c * 8) % g.group == 0) {
+          to[c * 8 / g.group] = scale;
+          to[(c + far) * 8 / g.group] = scale2;
+        }
+      }
+    } else {
+      if (y_of != t) {
+        y_of = t;
+        y_base = static_cast<char*>(r.y) + (bi * r.yb + ti * r.yt + hslot * r.yh + c * 8) * out_size;
+      }
+      if (ok) {
+        char* p = y_base + (h - hslot) * r.yh * out_size;
+        store_chunk<true>(p, g.y_f32, x, 8);
+        store_chunk<true>(p + far * 8 * out_size, g.y_f32, y, 8);
+      }
+    }
+  };
+
+  for (int s = step0; s < step1; s += kUnroll) {
+    Pair now[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) load(raw[u], s + kUnroll + u);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (s + u < step1) process(now[u], s + u);
+  }
+}
+
+template <bool F32, bool CACHE>
+void run(const HeadArgs& g, int mode, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kWaves);
+  if (mode == kPairs) {
+    if (g.dim == 64)
+      k_heads16<F32, 2, CACHE><<<grid, block, 0, s>>>(g);
+    else if (g.dim == 128)
+      k_heads16<F32, 3, CACHE><<<grid, block, 0, s>>>(g);
+    else
+      k_heads16<F32, -1, CACHE><<<grid, block, 0, s>>>(g);
+  } else if (mode == kChunks) {
+    k_heads<F32, kChunks, CACHE><<<grid, block, 0, s>>>(g);
+  } else if (mode == kVectors) {
+    k_heads<F32, kVectors, CACHE><<<grid, block, 0, s>>>(g);
+  } else {
+    k_heads<F32, kElements, CACHE><<<grid, block, 0, s>>>(g);
+  }
+}
+
+// The kernel a call takes.
+int mode_of(const HeadArgs& g, bool vec, bool cache) {
+  if (!vec) return kElements;
+  const bool chunks = g.half % (g.split ? 8 : 4) == 0;
+  const int whole = g.dim, part = g.dim / 2;
+  const auto within = [&](int v) { return v == whole || part % v == 0; };
+  if (g.dim % 16 == 0 && chunks && (!g.split || g.half == 0 || g.half == part) && (!cache || (within(g.hb) && within(g.group))))
+    return kPairs;
+  return chunks ? kChunks : kVectors;
 }
 
 }  // namespace
 
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s) {
-  const HeadPlan p = plan_heads(g.tokens, g.heads[2], g.dim);
+  const int mode = mode_of(g, vec, cache);
+  const HeadPlan p = plan_heads(g.tokens, g.q.heads, g.k.heads, g.v.heads, g.dim, mode == kPairs ? 16 : 8);
   g.lane_bits = p.lane_bits;
   g.slot_bits = p.slot_bits;
   g.steps = p.steps;
   g.slices = p.slices;
+  for (int i = 0; i < 3; ++i) g.step_end[i] = p.step_end[i];
   g.inv_dim = 1.0f / (float)g.dim;
-  const dim3 grid = wide_grid((p.waves + kWaves - 1) / kWaves), block(64 * kWaves);
-  if (cache) {
-    if (f32)
-      vec ? k_heads<true, true, true><<<grid, block, 0, s>>>(g) : k_heads<true, false, true><<<grid, block, 0, s>>>(g);
-    else
-      vec ? k_heads<false, true, true><<<grid, block, 0, s>>>(g) : k_heads<false, false, true><<<grid, block, 0, s>>>(g);
-  } else {
-    if (f32)
-      vec ? k_heads<true, true, false><<<grid, block, 0, s>>>(g) : k_heads<true, false, false><<<grid, block, 0, s>>>(g);
-    else
-      vec ? k_heads<false, true, false><<<grid, block, 0, s>>>(g) : k_heads<false, false, false><<<grid, block, 0, s>>>(g);
-  }
+  const dim3 grid = wide_grid((p.waves + kWaves - 1) / kWaves);
+  if (cache) g.group_bits = group_lane_bits(g.dim, g.group, p.lane_bits);
+  if (cache)
+    f32 ? run<true, true>(g, mode, grid, s) : run<false, true>(g, mode, grid, s);
+  else
+    f32 ? run<true, false>(g, mode, grid, s) : run<false, false>(g, mode, grid, s);
   return hipGetLastError();
 }
 

@@ -1,9 +1,10 @@
 // heads_plan.h -- how the per-head kernels spread over waves (host code alone).
 //
-// A head of dim elements lies on 2^lane_bits lanes, a chunk of 8 elements in
-// each; a wave takes 2^slot_bits heads of a token side by side, and, where a
+// A head of dim elements lies on 2^lane_bits lanes, one or two chunks of 8
+// elements in each; a wave takes 2^slot_bits heads of a token side by side, and, where a
 // token has fewer heads than fit, 64 >> (lane_bits + slot_bits) tokens.  A
-// token's heads are walked in `steps` steps by each of `slices` waves.
+// token's heads are walked in `steps` steps by each of `slices` waves, each
+// step within one tensor (queries, keys or values).
 #pragma once
 
 #include <stdint.h>
@@ -15,7 +16,8 @@ constexpr int64_t kHeadMaxHeads = 1 << 20;  // of one call
 
 struct HeadPlan {
   int lane_bits, slot_bits;
-  int steps, slices;
+  int step_end[3];    // steps of the first tensor, of the first two, of all: a step is one tensor's
+  int steps, slices;  // a wave's steps, the waves of a token (or group of tokens)
   int64_t waves;
 };
 
@@ -30,14 +32,26 @@ inline int bits_for(int64_t n) {  // smallest b with 2^b >= n
 // hide latency.
 constexpr int64_t kHeadWaves = 2048;
 
-inline HeadPlan plan_heads(int64_t tokens, int64_t heads, int dim) {
+// log2 of the lanes a group's maximum is taken over: all of a head's when the
+// group is the head, else a chunk of 8 in each.
+inline int group_lane_bits(int dim, int group, int lane_bits) { return group == dim ? lane_bits : bits_for(group / 8); }
+
+// Tensors of h0, h1 and h2 heads (0: not there), 8 or 16 elements a lane.
+inline HeadPlan plan_heads(int64_t tokens, int64_t h0, int64_t h1, int64_t h2, int dim, int per_lane = 8) {
   HeadPlan p;
-  p.lane_bits = bits_for((dim + 7) / 8);
+  const int64_t h[3] = {h0, h1, h2};
+  int64_t most = h0 > h1 ? h0 : h1;
+  if (h2 > most) most = h2;
+  p.lane_bits = bits_for((dim + per_lane - 1) / per_lane);
   const int fit = 6 - p.lane_bits;
-  p.slot_bits = heads >= (int64_t(1) << fit) ? fit : bits_for(heads);
+  p.slot_bits = most >= (int64_t(1) << fit) ? fit : bits_for(most);
   const int64_t per_wave = int64_t(1) << (6 - p.lane_bits - p.slot_bits);
   const int64_t groups = (tokens + per_wave - 1) / per_wave;
-  const int64_t total = (heads + (int64_t(1) << p.slot_bits) - 1) >> p.slot_bits;
+  int64_t total = 0;
+  for (int t = 0; t < 3; ++t) {
+    total += (h[t] + (int64_t(1) << p.slot_bits) - 1) >> p.slot_bits;
+    p.step_end[t] = (int)total;
+  }
   int64_t slices = (kHeadWaves + groups - 1) / groups;
   if (slices > total) slices = total;
   p.steps = (int)((total + slices - 1) / slices);
