@@ -163,7 +163,13 @@ int hdq_w4_quantize(const void* w, const hdq_w4_tensor* out, void* stream) {
                                        W4Out{out->codes, out->scale, out->zero}, static_cast<hipStream_t>(stream)));
 }
 
-int hdq_w4_linear(const void* x, int64_t M, const hdq_w4_tensor* w, void* y, int32_t y_dtype, void* stream) {
+size_t hdq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || M > HDQ_W4_MAX_TOKENS || !w4_shape_ok(N, K, 32)) return 0;
+  return w4_workspace(M, N, K);
+}
+
+int hdq_w4_linear(const void* x, int64_t M, const hdq_w4_tensor* w, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                  void* stream) {
   if (w == nullptr || ((x == nullptr || y == nullptr) && M != 0)) return HDQ_ERR_INVALID;
   if (!valid_dtype(y_dtype)) return HDQ_ERR_UNSUPPORTED;
   if (M < 0 || M > HDQ_W4_MAX_TOKENS) return HDQ_ERR_SHAPE;
@@ -171,8 +177,11 @@ int hdq_w4_linear(const void* x, int64_t M, const hdq_w4_tensor* w, void* y, int
   if (st != HDQ_OK) return st;
   if (M == 0) return HDQ_OK;
   if (!aligned(x, 16) || !aligned(y, y_dtype == HDQ_DTYPE_F32 ? 4 : 2)) return HDQ_ERR_SHAPE;
+  const size_t need = w4_workspace(M, w->N, w->K);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return HDQ_ERR_WORKSPACE;
+  if (need > 0 && !aligned(ws, 16)) return HDQ_ERR_SHAPE;
   return hip_status(launch_w4(static_cast<const uint16_t*>(x), M, W4Weights{w->codes, w->scale, w->zero, w->N, w->K, w->group},
-                              y, y_dtype == HDQ_DTYPE_F32, static_cast<hipStream_t>(stream)));
+                              y, y_dtype == HDQ_DTYPE_F32, ws, static_cast<hipStream_t>(stream)));
 }
 
 int hdq_rope_turns(int32_t dim, double base, int32_t scaling, double factor, double length, double slow, double fast,

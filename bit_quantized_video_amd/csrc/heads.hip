@@ -473,6 +473,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   char* y_base = nullptr;
   const int64_t slot = CACHE && in ? g.slots[tok] : -1;
   const bool in_cache = slot >= 0 && slot < g.n_slots;
+  // the groups of the lane's chunks, and whether the lane is their first
+  const bool whole = g.group == g.dim;
+  const int group1 = CACHE && !whole ? c * 8 / g.group : 0, group2 = CACHE && !whole ? (c + far) * 8 / g.group : 0;
+  const bool heads_group = CACHE && (whole ? c == 0 : group1 * g.group == c * 8);
 
   auto process = [&](const Pair& raw, int s) {
     const int t = tensor(s), h = block(t, s) + hslot;
@@ -581,7 +585,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
         a = __builtin_elementwise_maximum(a, fabsf(x[e]));
         b = __builtin_elementwise_maximum(b, fabsf(y[e]));
       }
-      const bool whole = g.group == g.dim;
       if (whole) a = __builtin_elementwise_maximum(a, b);
       float scale, inv, scale2, inv2;
       code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
@@ -594,12 +597,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
         store_codes(g.codes[t - 1], row * g.dim + c * 8, x, inv, g.fmt);
         store_codes(g.codes[t - 1], row * g.dim + (c + far) * 8, y, inv2, g.fmt);
         float* to = g.scales[t - 1] + row * g.groups;
-        if (whole) {
-          if (c == 0) to[0] = scale;
-        } else if ((c * 8) % g.group == 0) {
-          to[c * 8 / g.group] = scale;
-          to[(c + far) * 8 / g.group] = scale2;
-        }
+        if (heads_group) to[group1] = scale;
+        if (heads_group && !whole) to[group2] = scale2;
       }
     } else {
       if (y_of != t) {

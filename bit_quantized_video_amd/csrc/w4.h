@@ -20,8 +20,8 @@ struct W4Out {
   uint8_t* zero;  // null: without zero points
 };
 
-// y [M, N] (float32 or bf16) from bf16 x [M, K].
-hipError_t launch_w4(const uint16_t* x, int64_t M, const W4Weights& w, void* y, bool f32, hipStream_t s);
+// y [M, N] (float32 or bf16) from bf16 x [M, K]; ws: w4_workspace bytes.
+hipError_t launch_w4(const uint16_t* x, int64_t M, const W4Weights& w, void* y, bool f32, void* ws, hipStream_t s);
 hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scale, const uint8_t* zero, int64_t N, int64_t K,
                           int group, const W4Out& out, hipStream_t s);
 hipError_t launch_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, const W4Out& out, hipStream_t s);

@@ -13,6 +13,8 @@
 #include "hdq_internal.h"
 #include "w4.h"
 
+#include <type_traits>
+
 namespace hdq {
 
 namespace {
@@ -25,186 +27,270 @@ struct W4Args {
   void* y;
   int64_t M, N, K;
   int64_t tiles_n, tiles_k;
-  int wn, wk;
+  int wn, wk, per;  // k_w4: waves along rows and K, tiles of rows of a wave
+  int split;      // workgroups along K; above 1 each writes float32 sums to y + its number * slice
+  int64_t slice;
 };
 
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
-// Codes to bf16 16 + u: eight columns of a word.
+// Codes to bf16 16 + u: eight columns of a word, which is kept rotated left by 3
+// bits, so that the first pair lies in place.
 __device__ __forceinline__ v8bf decode(uint32_t w) {
+  const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
   v4u r;
-  r.x = ((w << 3) & 0x00780078u) | 0x41804180u;
-  r.y = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  r.z = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  r.w = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  r.x = (w & mask) | sixteen;
+  r.y = ((w >> 4) & mask) | sixteen;
+  r.z = ((w >> 8) & mask) | sixteen;
+  r.w = (__builtin_rotateright32(w, 12) & mask) | sixteen;
   return __builtin_bit_cast(v8bf, r);
 }
 
-// One tile's operands as loaded: NT x 16 rows, MT x 16 tokens, 128 columns.
-template <int MT, int NT, int GROUPS, bool ZERO>
+// One tile of a row tile's weights as loaded: a lane's 32 codes, and the scales
+// (bf16) and zero points (bytes) of its row, l % 16.
+template <int GROUPS, bool ZERO>
 struct Tile {
-  v4u codes[NT];
-  v4u x[MT][4];
-  v2u scale[NT][GROUPS];
-  uint32_t zero[ZERO ? NT : 1][GROUPS];
+  v4u codes;
+  uint16_t scale[GROUPS];
+  uint8_t zero[ZERO ? GROUPS : 1];
+  __device__ __forceinline__ void load(const uint8_t* c, const uint16_t* s, const uint8_t* z, int64_t at) {
+    codes = *reinterpret_cast<const v4u*>(c + at * 1024);
+    __builtin_memcpy(scale, __builtin_assume_aligned(s + at * (16 * GROUPS), 2 * GROUPS), 2 * GROUPS);
+    if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z + at * (16 * GROUPS), GROUPS), GROUPS);
+  }
 };
 
-template <int MT, int NT, int GROUPS, bool ZERO, bool F32>
+// y += the tile's product; x(m, s): tokens 16 m .. + 15, columns 32 s .. + 31.  Of
+// the lane's four results of an instruction, tokens 4 quad + r, the first R are
+// wanted.
+template <int MT, int NT, int R, int GROUPS, bool ZERO, typename X>
+__device__ __forceinline__ void multiply(const Tile<GROUPS, ZERO> (&t)[NT], const X& x, float (&y)[NT][MT][R]) {
+  constexpr int STEPS = 4 / GROUPS;
+  const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int q = 0; q < GROUPS; ++q) {
+    v4f d[NT][MT], sum[MT];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      v8bf a[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        a[m] = x(m, q * STEPS + s);
+        sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m], ones, s == 0 ? none : sum[m], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const v8bf b = decode(t[i].codes[q * STEPS + s]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) d[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m], b, s == 0 ? none : d[i][m], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float sc = __uint_as_float((uint32_t)t[i].scale[q] << 16);
+      const float off = ZERO ? 16.0f + (float)t[i].zero[ZERO ? q : 0] : 24.0f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < R; ++r) y[i][m][r] = fmaf(sc, fmaf(-off, sum[m][r], d[i][m][r]), y[i][m][r]);
+    }
+    // one group's products at a time: with all of a tile's the compiler runs out of registers
+    if (MT > 1) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// An output: token m, row n.
+template <bool F32>
+__device__ __forceinline__ void store(const W4Args& g, void* y, int64_t m, int64_t n, float v) {
+  if (m >= g.M || n >= g.N) return;
+  if (F32)
+    static_cast<float*>(y)[m * g.N + n] = v;
+  else
+    static_cast<uint16_t*>(y)[m * g.N + n] = (uint16_t)pack_bf16x2(v, 0.0f);
+}
+
+// Up to 16 tokens whose columns fit LDS.  The workgroup keeps the tokens there
+// (a row's pitch is 16 bytes past a multiple of 256: a fragment's 16 rows fall on
+// all banks), and its waves stream weights, kDepth tiles in flight each:
+//   wk = 1: a wave takes `per` tiles of rows, one after the other -- their
+//           codes and scales are contiguous;
+//   wk > 1: wk waves share a tile of rows, each taking every wk-th tile of K,
+//           and their sums meet in LDS, in order.
+// Token 4 r + q is row 4 q + r of the product, so that R results a lane hold up
+// to 4 R tokens.
+constexpr int kDepth = 4;
+
+template <int R, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
-  extern __shared__ float s_sum[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  extern __shared__ __align__(16) uint8_t s_lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / g.wk, wk = wave - wn * g.wk;
   const int col = lane & 15, quad = lane >> 4;
-  const int64_t tn0 = ((int64_t)blockIdx.x * g.wn + wn) * NT;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int tiles_k = (int)g.tiles_k;
-  typedef Tile<MT, NT, GROUPS, ZERO> T;
+  const int tiles_k = (int)g.tiles_k, pitch = tiles_k * 256 + 16;
+  const int64_t tn0 = ((int64_t)blockIdx.x * g.wn + wn) * g.per;
+  const int rows_here = (int)max((int64_t)0, min((int64_t)g.per, g.tiles_n - tn0));
+  const int first = g.wk > 1 ? wk : 0, step = g.wk;
+  const int count = rows_here == 0 ? 0 : g.wk > 1 ? (tiles_k - wk + step - 1) / step : rows_here * tiles_k;
 
+  // item i is tile first + i step of the wave's contiguous ones
+  const int64_t base = tn0 * tiles_k + first;
+  const uint8_t* codes = g.codes + base * 1024 + lane * 16;
+  const uint16_t* scale = g.scale + (base * 16 + col) * GROUPS;
+  const uint8_t* zero = ZERO ? g.zero + (base * 16 + col) * GROUPS : nullptr;
+  typedef Tile<GROUPS, ZERO> T;
+  T ring[kDepth][1];
+  auto load = [&](T& t, int i) { t.load(codes, scale, zero, (int64_t)i * step); };
+#pragma unroll
+  for (int u = 0; u < kDepth; ++u)
+    if (u < count) load(ring[u][0], u);
+
+  // the tokens, zeros past the last column
+  const int pieces = tiles_k * 16, filled = (int)(g.K / 8);
+  for (int m = 0; m < (int)g.M; ++m)
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+      v4u v = {0u, 0u, 0u, 0u};
+      if (i < filled) v = *reinterpret_cast<const v4u*>(g.x + m * g.K + i * 8);
+      *reinterpret_cast<v4u*>(s_lds + m * pitch + i * 16) = v;
+    }
+  __syncthreads();
+  // rows of tokens that are not there repeat the first's, and are not stored
+  const int token = (col & 3) * 4 + (col >> 2);
+  const uint8_t* xr = s_lds + (token < g.M ? token : 0) * pitch + quad * 16;
+
+  float y[1][1][R] = {};
+  int kt = first;
+  int64_t tn = tn0;
+  auto work = [&](const T (&t)[1]) {
+    multiply<1, 1, R>(t, [&](int, int s) { return *reinterpret_cast<const v8bf*>(xr + kt * 256 + s * 64); }, y);
+    kt += step;
+    if (g.wk == 1 && kt == tiles_k) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        store<F32>(g, g.y, 4 * r + quad, tn * 16 + col, y[0][0][r]);
+        y[0][0][r] = 0.0f;
+      }
+      kt = 0;
+      ++tn;
+    }
+  };
+  for (int i = 0; i < count; i += kDepth) {
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+      if (i + u < count) {
+        work(ring[u]);
+        if (i + u + kDepth < count) load(ring[u][0], i + u + kDepth);
+      }
+  }
+  if (g.wk == 1) return;
+  __syncthreads();  // the tokens are done with
+  float* sums = reinterpret_cast<float*>(s_lds);  // [wn][wk][R][64]
+#pragma unroll
+  for (int r = 0; r < R; ++r) sums[(wave * R + r) * 64 + lane] = y[0][0][r];
+  __syncthreads();
+  if (wk != 0 || rows_here == 0) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v = y[0][0][r];
+    for (int k = 1; k < g.wk; ++k) v += sums[((wave + k) * R + r) * 64 + lane];
+    store<F32>(g, g.y, 4 * r + quad, tn0 * 16 + col, v);
+  }
+}
+
+// More tokens, or longer ones.  A workgroup of four waves takes 16 MT tokens x 128 rows
+// (two tiles each); the tokens' 128 columns of a stage lie in LDS, shared by
+// the waves, in rows of 16 pieces of 16 bytes, piece p of row r at p ^ (r % 16),
+// so that a fragment's 16 rows fall on all banks.  They are loaded straight to
+// LDS, a stage ahead.
+template <int MT, int GROUPS, bool ZERO, bool F32>
+__global__ __launch_bounds__(256, 2) void k_w4_shared(const W4Args g) {
+  constexpr int NT = 2;
+  __shared__ __align__(1024) uint8_t s_x[2][MT * 4096];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int64_t tn0 = ((int64_t)blockIdx.x * 4 + wave) * NT, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int each = (int)((g.tiles_k + g.split - 1) / g.split);
+  const int k0 = (int)blockIdx.z * each, k1 = min(k0 + each, (int)g.tiles_k);
   const uint8_t* codes[NT];
   const uint16_t* scale[NT];
   const uint8_t* zero[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int64_t tile = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * tiles_k;  // a row tile past the end repeats the last
+    const int64_t tile = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * g.tiles_k;  // past the end: the last again
     codes[i] = g.codes + tile * 1024 + lane * 16;
-    scale[i] = g.scale + tile * (16 * GROUPS) + quad * (4 * GROUPS);
-    zero[i] = ZERO ? g.zero + tile * (16 * GROUPS) + quad * (4 * GROUPS) : nullptr;
+    scale[i] = g.scale + (tile * 16 + col) * GROUPS;
+    zero[i] = ZERO ? g.zero + (tile * 16 + col) * GROUPS : nullptr;
   }
-  const uint16_t* xr[MT];
-  bool token[MT];
+  typedef Tile<GROUPS, ZERO> T;
+  auto load = [&](T (&t)[NT], int kt) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    token[m] = m0 + m * 16 + col < g.M;
-    xr[m] = g.x + (token[m] ? m0 + m * 16 + col : 0) * g.K + quad * 8;
-  }
-
-  auto load = [&](T& t, int kt) {
+    for (int i = 0; i < NT; ++i) t[i].load(codes[i], scale[i], zero[i], kt);
+  };
+  // the workgroup's tokens; pieces past the last token or column read zeros
+  const int64_t here = g.M - m0 < 16 * MT ? g.M - m0 : 16 * MT;
+  const uint32_t bytes = (uint32_t)(here * g.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.K, bytes);
+  auto fetch = [&](int buf, int kt) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      t.codes[i] = *reinterpret_cast<const v4u*>(codes[i] + (int64_t)kt * 1024);
-#pragma unroll
-      for (int q = 0; q < GROUPS; ++q) {
-        t.scale[i][q] = *reinterpret_cast<const v2u*>(scale[i] + (int64_t)kt * (16 * GROUPS) + 4 * q);
-        if (ZERO) t.zero[i][q] = *reinterpret_cast<const uint32_t*>(zero[i] + (int64_t)kt * (16 * GROUPS) + 4 * q);
-      }
+    for (int j = 0; j < MT; ++j) {
+      const int piece = (wave * MT + j) * 64 + lane, row = piece >> 4, c = (piece & 15) ^ (row & 15);
+      const bool in = row < here && (int64_t)kt * 128 + c * 8 < g.K;
+      const uint32_t at = in ? (uint32_t)((int64_t)row * g.K + (int64_t)kt * 128 + c * 8) * 2 : bytes;
+      lds_dma16(xr, &s_x[buf][(wave * MT + j) * 1024], at, 0);
     }
-    const int left = (int)(g.K - (int64_t)kt * 128) - quad * 8;  // columns from the lane's first on
+  };
+  float y[NT][MT][4] = {};
+  T w[2][NT];
+  fetch(0, k0);
+  load(w[0], k0);
+  auto stage = [&](auto half, int kt) {
+    constexpr int H = decltype(half)::value;
+    stage_barrier();  // this stage has arrived, and the last one's reads are done
+    if (kt + 1 < k1) {
+      fetch(H ^ 1, kt + 1);
+      load(w[H ^ 1], kt + 1);
+    }
+    multiply<MT, NT, 4>(w[H], [&](int m, int s) {
+      return *reinterpret_cast<const v8bf*>(&s_x[H][(m * 16 + col) * 256 + (((4 * s + quad) ^ col) * 16)]);
+    }, y);
+  };
+  for (int kt = k0; kt < k1; kt += 2) {
+    stage(std::integral_constant<int, 0>(), kt);
+    if (kt + 1 < k1) stage(std::integral_constant<int, 1>(), kt + 1);
+  }
+  void* out = g.split > 1 ? static_cast<float*>(g.y) + blockIdx.z * g.slice : g.y;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        t.x[m][s] = v4u{0u, 0u, 0u, 0u};
-        if (token[m] && 32 * s < left) t.x[m][s] = *reinterpret_cast<const v4u*>(xr[m] + (int64_t)kt * 128 + 32 * s);
-      }
-  };
+      for (int r = 0; r < 4; ++r) store<F32>(g, out, m0 + m * 16 + quad * 4 + r, (tn0 + i) * 16 + col, y[i][m][r]);
+}
 
-  v4f y[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) y[i][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-
-  auto multiply = [&](const T& t) {
-    constexpr int STEPS = 4 / GROUPS;
-#pragma unroll
-    for (int q = 0; q < GROUPS; ++q) {
-      v4f d[NT][MT], sum[MT];
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        v8bf b[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          b[m] = __builtin_bit_cast(v8bf, t.x[m][q * STEPS + s]);
-          const v4f c = s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : sum[m];
-          sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, b[m], c, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const v8bf a = decode(t.codes[i][q * STEPS + s]);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const v4f c = s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : d[i][m];
-            d[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[m], c, 0, 0, 0);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t w = t.scale[i][q][r >> 1];
-          const float sc = (r & 1) ? bf16_hi(w) : bf16_lo(w);
-          const float off = ZERO ? 16.0f + (float)((t.zero[ZERO ? i : 0][q] >> (8 * r)) & 255u) : 24.0f;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) y[i][m][r] = fmaf(sc, fmaf(-off, sum[m][r], d[i][m][r]), y[i][m][r]);
-        }
-    }
-  };
-
-  // two tiles in flight
-  T a, b;
-  int kt = wk;
-  if (kt < tiles_k) load(a, kt);
-  while (kt < tiles_k) {
-    if (kt + g.wk < tiles_k) load(b, kt + g.wk);
-    multiply(a);
-    kt += g.wk;
-    if (kt >= tiles_k) break;
-    if (kt + g.wk < tiles_k) load(a, kt + g.wk);
-    multiply(b);
-    kt += g.wk;
-  }
-
-  auto store = [&](int64_t tn, int64_t m, const v4f v) {
-    const int64_t n = tn * 16 + quad * 4;
-    if (m >= g.M || tn >= g.tiles_n || n >= g.N) return;
-    const int count = (int)(g.N - n < 4 ? g.N - n : 4);
-    if (F32) {
-      float* p = static_cast<float*>(g.y) + m * g.N + n;
-      if (count == 4) {
-        __builtin_memcpy(p, &v, 16);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 3; ++r)
-          if (r < count) p[r] = v[r];
-      }
-    } else {
-      uint16_t* p = static_cast<uint16_t*>(g.y) + m * g.N + n;
-      const v2u w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      if (count == 4) {
-        __builtin_memcpy(p, &w, 8);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 3; ++r)
-          if (r < count) p[r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
-      }
-    }
-  };
-
-  if (g.wk == 1) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) store(tn0 + i, m0 + m * 16 + col, y[i][m]);
+// Sums of the splits, in order: 4 outputs a thread.
+template <bool F32>
+__global__ __launch_bounds__(256) void k_w4_join(const float* __restrict__ sums, int split, int64_t slice, int64_t count,
+                                                 void* __restrict__ y) {
+  const int64_t i = ((int64_t)wide_block() * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  v4f v = *reinterpret_cast<const v4f*>(sums + i);
+  for (int k = 1; k < split; ++k) v += *reinterpret_cast<const v4f*>(sums + k * slice + i);
+  const v2u w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  if (i + 4 <= count) {
+    if (F32)
+      __builtin_memcpy(static_cast<float*>(y) + i, &v, 16);
+    else
+      __builtin_memcpy(static_cast<uint16_t*>(y) + i, &w, 8);
     return;
   }
-  // the waves along K join their sums, in order: tile t of the workgroup's
-  // wn x NT x MT by wave t, t + waves, ...
-  constexpr int TILES = NT * MT;
-  v4f* sums = reinterpret_cast<v4f*>(s_sum);  // [wn][TILES][wk][64]
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) sums[((wn * TILES + i * MT + m) * g.wk + wk) * 64 + lane] = y[i][m];
-  __syncthreads();
-  for (int t = wave; t < g.wn * TILES; t += g.wn * g.wk) {
-    const int tw = t / TILES, ti = t - tw * TILES;
-    v4f v = sums[t * g.wk * 64 + lane];
-    for (int k = 1; k < g.wk; ++k) v += sums[(t * g.wk + k) * 64 + lane];
-    store(((int64_t)blockIdx.x * g.wn + tw) * NT + ti / MT, m0 + (ti % MT) * 16 + col, v);
-  }
+  for (int r = 0; r < 3; ++r)
+    if (i + r < count) {
+      if (F32)
+        static_cast<float*>(y)[i + r] = v[r];
+      else
+        static_cast<uint16_t*>(y)[i + r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
+    }
 }
 
 // ---- weights ----------------------------------------------------------------
@@ -230,12 +316,13 @@ __global__ __launch_bounds__(256) void k_w4_pack(const uint8_t* __restrict__ src
       const uint32_t v = *reinterpret_cast<const uint32_t*>(src + (row * K + k) / 2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[s] |= ((v >> (4 * e)) & 15u) << (4 * nibble(e));
+      w[s] = __builtin_rotateleft32(w[s], 3);
     }
   }
   reinterpret_cast<uint4*>(out.codes)[tile * 64 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
   const int groups = 128 / group;
-  if (lane < 16 * groups) {  // [4 quads][groups][4 rows]
-    const int64_t r = tn * 16 + (lane / (4 * groups)) * 4 + lane % 4, kg = tk * groups + lane / 4 % groups, kgs = K / group;
+  if (lane < 16 * groups) {  // [16 rows][groups]
+    const int64_t r = tn * 16 + lane / groups, kg = tk * groups + lane % groups, kgs = K / group;
     const bool in = r < N && kg < kgs;
     out.scale[tile * 16 * groups + lane] = in ? scale[r * kgs + kg] : (uint16_t)0;
     if (out.zero != nullptr) out.zero[tile * 16 * groups + lane] = in ? zero[r * kgs + kg] : (uint8_t)0;
@@ -275,7 +362,7 @@ __global__ __launch_bounds__(256) void k_w4_quantize(const uint16_t* __restrict_
   const float z = zp ? (s > 0.0f ? fminf(rintf(-lo / s), 15.0f) : 0.0f) : 8.0f;
   const int64_t tile = (row >> 4) * tiles_k + kg / groups;
   const int q = (int)(kg % groups), n = (int)(row & 15);
-  const int64_t at = (tile * 4 + (n >> 2)) * (groups * 4) + q * 4 + (n & 3);
+  const int64_t at = (tile * 16 + n) * groups + q;
   out.scale[at] = finite ? (s > 0.0f ? (uint16_t)bits : (uint16_t)0) : (uint16_t)0x7fc0;
   if (zp) out.zero[at] = in ? (uint8_t)z : (uint8_t)0;
   for (int i = 0; i < group / 8; ++i) {
@@ -290,39 +377,53 @@ __global__ __launch_bounds__(256) void k_w4_quantize(const uint16_t* __restrict_
       }
     }
     const int k = q * group + 8 * i;  // column of the tile
-    reinterpret_cast<uint32_t*>(out.codes)[(tile * 64 + ((k >> 3) & 3) * 16 + n) * 4 + (k >> 5)] = w;
+    reinterpret_cast<uint32_t*>(out.codes)[(tile * 64 + ((k >> 3) & 3) * 16 + n) * 4 + (k >> 5)] = __builtin_rotateleft32(w, 3);
   }
 }
 
-template <int MT, int NT, int GROUPS, bool ZERO>
-hipError_t run(const W4Args& a, const W4Plan& p, bool f32, hipStream_t s) {
-  const dim3 grid((unsigned)p.grid_x, (unsigned)p.grid_y), block((unsigned)(64 * p.wn * p.wk));
-  const size_t lds = p.wk > 1 ? (size_t)p.wn * p.wk * NT * MT * 1024 : 0;
-  if (f32)
-    k_w4<MT, NT, GROUPS, ZERO, true><<<grid, block, lds, s>>>(a);
+template <int GROUPS, bool ZERO, bool F32>
+void run(const W4Args& a, const W4Plan& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.grid_x, (unsigned)p.grid_y, (unsigned)p.split), block((unsigned)(64 * p.wn * p.wk));
+  if (p.per > 0 && a.M <= 4)
+    k_w4<1, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.per > 0 && a.M <= 8)
+    k_w4<2, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.per > 0)
+    k_w4<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.mt == 4)
+    k_w4_shared<4, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+  else if (p.mt == 2)
+    k_w4_shared<2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else
-    k_w4<MT, NT, GROUPS, ZERO, false><<<grid, block, lds, s>>>(a);
-  return hipGetLastError();
+    k_w4_shared<1, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
 }
 
-template <int MT, int NT>
-hipError_t run_tiles(const W4Args& a, const W4Plan& p, int group, bool f32, hipStream_t s) {
+template <bool F32>
+void run_group(const W4Args& a, const W4Plan& p, int group, hipStream_t s) {
   const bool z = a.zero != nullptr;
   switch (group) {
-    case 32: return z ? run<MT, NT, 4, true>(a, p, f32, s) : run<MT, NT, 4, false>(a, p, f32, s);
-    case 64: return z ? run<MT, NT, 2, true>(a, p, f32, s) : run<MT, NT, 2, false>(a, p, f32, s);
-    default: return z ? run<MT, NT, 1, true>(a, p, f32, s) : run<MT, NT, 1, false>(a, p, f32, s);
+    case 32: z ? run<4, true, F32>(a, p, s) : run<4, false, F32>(a, p, s); break;
+    case 64: z ? run<2, true, F32>(a, p, s) : run<2, false, F32>(a, p, s); break;
+    default: z ? run<1, true, F32>(a, p, s) : run<1, false, F32>(a, p, s); break;
   }
 }
 
 }  // namespace
 
-hipError_t launch_w4(const uint16_t* x, int64_t M, const W4Weights& w, void* y, bool f32, hipStream_t s) {
+hipError_t launch_w4(const uint16_t* x, int64_t M, const W4Weights& w, void* y, bool f32, void* ws, hipStream_t s) {
   const W4Plan p = plan_w4(M, w.N, w.K);
-  const W4Args a{x, w.codes, w.scale, w.zero, y, M, w.N, w.K, w4_tiles_n(w.N), w4_tiles_k(w.K), p.wn, p.wk};
-  if (p.mt == 1) return run_tiles<1, 1>(a, p, w.group, f32, s);
-  if (p.mt == 2) return run_tiles<2, 2>(a, p, w.group, f32, s);
-  return run_tiles<4, 2>(a, p, w.group, f32, s);
+  const bool join = p.split > 1;
+  const int64_t slice = w4_slice(M, w.N), count = M * w.N;
+  const W4Args a{x, w.codes, w.scale, w.zero, join ? ws : y, M, w.N, w.K, w4_tiles_n(w.N), w4_tiles_k(w.K), p.wn, p.wk, p.per, p.split, slice};
+  f32 || join ? run_group<true>(a, p, w.group, s) : run_group<false>(a, p, w.group, s);
+  if (join) {
+    const dim3 grid = wide_grid((count + 1023) / 1024);
+    if (f32)
+      k_w4_join<true><<<grid, dim3(256), 0, s>>>(static_cast<const float*>(ws), p.split, slice, count, y);
+    else
+      k_w4_join<false><<<grid, dim3(256), 0, s>>>(static_cast<const float*>(ws), p.split, slice, count, y);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scale, const uint8_t* zero, int64_t N, int64_t K,

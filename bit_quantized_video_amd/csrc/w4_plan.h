@@ -4,9 +4,9 @@
 // Rows go in tiles of 16 and columns in tiles of 128, both rounded up:
 //   codes [N / 16][K / 128][64 lanes][16 bytes]: lane l holds row l % 16 and, in
 //         32-bit word s, columns 32 s + 8 (l / 16) .. + 7 of the tile, in nibbles
-//         0 4 1 5 2 6 3 7 (columns 0, 1 are nibbles 0 and 4, ...);
-//   scale [N / 16][K / 128][4][128 / group][4] bf16: rows 4 q + i (q, i the
-//         first and last index); zero the same in bytes.
+//         0 4 1 5 2 6 3 7 (columns 0, 1 are nibbles 0 and 4, ...), the word
+//         rotated left by 3 bits;
+//   scale [N / 16][K / 128][16][128 / group] bf16, zero the same in bytes.
 // Padding holds zeros (scale 0).
 #pragma once
 
@@ -24,32 +24,67 @@ inline size_t w4_scale_count(int64_t N, int64_t K, int group) {
   return (size_t)(w4_tiles_n(N) * w4_tiles_k(K)) * (size_t)(16 * (kW4TileK / group));
 }
 
+// Up to 16 tokens that fit LDS: a workgroup keeps them there and streams
+// weights (k_w4).  Else a workgroup of four waves shares 64 tokens (16 or 32
+// where there are no more) a stage at a time among 128 rows, and K is split
+// over workgroups, whose sums a second launch adds, where there are too few
+// (k_w4_shared).
 struct W4Plan {
-  int mt, nt;       // tiles of 16 tokens, of 16 rows, that a wave multiplies
-  int wn, wk;       // waves of a workgroup along the rows, and along K
+  int per;      // k_w4: tiles of rows of a wave, 0: k_w4_shared
+  int wn, wk;   // waves of a workgroup along the rows, and along K
+  size_t lds;
+  int mt;       // k_w4_shared: tiles of 16 tokens
+  int split;    // workgroups along K
   int64_t grid_x, grid_y;
 };
 
-// Waves wanted: eight for each CU.
-constexpr int64_t kW4Waves = 2048;
+#ifndef WW
+#define WW 8192
+#endif
+constexpr int64_t kW4Waves = WW;       // waves wanted of k_w4: 32 for each CU
+constexpr size_t kW4Lds = 64 << 10;    // LDS its tokens may take
+constexpr int64_t kW4Groups = 256;     // workgroups wanted of k_w4_shared
+constexpr int64_t kW4LeastTiles = 4;   // tiles of K that a split keeps at least
 
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
-  W4Plan p;
+  W4Plan p = {};
   const int64_t tm = (M + 15) / 16, tn = w4_tiles_n(N), tk = w4_tiles_k(K);
-  p.mt = tm == 1 ? 1 : tm == 2 ? 2 : 4;
-  p.nt = p.mt == 1 ? 1 : 2;
-  p.grid_y = (tm + p.mt - 1) / p.mt;
-  const int64_t gn = (tn + p.nt - 1) / p.nt, want = (kW4Waves + gn * p.grid_y - 1) / (gn * p.grid_y);
-  const int64_t most = p.mt == 4 ? 8 : 16;
-  int64_t wk = want < tk ? want : tk;
-  if (wk > most) wk = most;
-  // the same number of tiles for each wave, as far as that goes
-  const int64_t each = (tk + wk - 1) / wk;
-  wk = (tk + each - 1) / each;
-  p.wk = (int)wk;
-  p.wn = wk >= 4 ? 1 : (int)(4 / wk);
-  p.grid_x = (gn + p.wn - 1) / p.wn;
+  p.split = 1;
+  p.lds = (size_t)M * (size_t)(tk * 256 + 16);
+  if (tm == 1 && p.lds <= kW4Lds) {
+    p.grid_y = 1;
+    // waves of a tile of rows: as many as there are tiles to go round, two or more of K each
+    int64_t wk = kW4Waves / tn < tk / 2 ? kW4Waves / tn : tk / 2;
+    wk = wk > 16 ? 16 : wk < 1 ? 1 : wk;
+    const int64_t each = (tk + wk - 1) / wk;  // the same number of tiles for each, as far as that goes
+    wk = (tk + each - 1) / each;
+    p.wk = (int)wk;
+    p.wn = wk >= 4 ? 1 : (int)(8 / wk);
+    p.per = wk > 1 ? 1 : (int)((tn + kW4Waves - 1) / kW4Waves);
+    p.grid_x = (tn + p.wn * p.per - 1) / (p.wn * p.per);
+    if (wk > 1 && p.lds < (size_t)(p.wn * p.wk) * 1024) p.lds = (size_t)(p.wn * p.wk) * 1024;
+  } else {
+    p.mt = tm == 1 ? 1 : tm == 2 ? 2 : 4;
+    p.wn = 4;
+    p.wk = 1;
+    p.grid_x = (tn + 7) / 8;
+    p.grid_y = (tm + p.mt - 1) / p.mt;
+    const int64_t most = tk / kW4LeastTiles;
+    int64_t split = (kW4Groups + p.grid_x * p.grid_y - 1) / (p.grid_x * p.grid_y);
+    if (split > most) split = most;
+    if (split > 1) {
+      const int64_t each = (tk + split - 1) / split;
+      p.split = (int)((tk + each - 1) / each);
+    }
+  }
   return p;
+}
+
+// Scratch: the workgroups' float32 sums along K.
+inline int64_t w4_slice(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
+inline size_t w4_workspace(int64_t M, int64_t N, int64_t K) {
+  const W4Plan p = plan_w4(M, N, K);
+  return p.split > 1 ? (size_t)p.split * (size_t)w4_slice(M, N) * 4 : 0;
 }
 
 }  // namespace hdq

@@ -51,6 +51,7 @@ EXPORTS = ("hdq_select_precision", "hdq_delta_sums", "hdq_select_precision_sums"
            "hdq_fp8_quantize", "hdq_fp8_linear_workspace_bytes", "hdq_fp8_linear",
            "hdq_group_norm_workspace_bytes", "hdq_group_norm", "hdq_group_norm_fp8",
            "hdq_w4_bytes", "hdq_w4_pack", "hdq_w4_quantize", "hdq_w4_linear",
+           "hdq_w4_linear_workspace_bytes",
            "hdq_rope_turns", "hdq_qk_norm_rope", "hdq_qkv_to_cache", "hdq_cache_read",
            "hdq_linear", "hdq_workspace_bytes",
            "hdq_status_string", "hdq_version")
@@ -199,7 +200,9 @@ def _load():
     L.hdq_w4_quantize.restype = _c.c_int
     L.hdq_w4_quantize.argtypes = [_p, w4, _p]
     L.hdq_w4_linear.restype = _c.c_int
-    L.hdq_w4_linear.argtypes = [_p, _c.c_int64, w4, _p, _c.c_int32, _p]
+    L.hdq_w4_linear.argtypes = [_p, _c.c_int64, w4, _p, _c.c_int32, _p, _c.c_size_t, _p]
+    L.hdq_w4_linear_workspace_bytes.restype = _c.c_size_t
+    L.hdq_w4_linear_workspace_bytes.argtypes = [_c.c_int64, _c.c_int64, _c.c_int64]
     L.hdq_rope_turns.restype = _c.c_int
     L.hdq_rope_turns.argtypes = [_c.c_int32, _c.c_double, _c.c_int32, _c.c_double, _c.c_double, _c.c_double,
                                  _c.c_double, _c.POINTER(_c.c_double)]
@@ -875,7 +878,12 @@ def w4_quantize(w, group=128, zero_points=False, stream=None):
     return _launch(w.device, stream, call)
 
 
-def w4_linear(x, w, y=None, y_dtype=DTYPE_BF16, stream=None):
+def w4_linear_workspace_bytes(M, N, K):
+    """hdq_w4_linear_workspace_bytes: the scratch w4_linear needs."""
+    return lib.hdq_w4_linear_workspace_bytes(M, N, K)
+
+
+def w4_linear(x, w, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
     """hdq_w4_linear: Y[M, N] = X[M, K] @ W[N, K]^T, x bf16, w W4Weights."""
     x = _bf16(x, "x")
     (M, K), dev = x.shape, x.device
@@ -887,7 +895,8 @@ def w4_linear(x, w, y=None, y_dtype=DTYPE_BF16, stream=None):
 
     def call(s):
         out = torch.empty(M, w.N, dtype=dt, device=dev) if y is None else y
-        _check("hdq_w4_linear", lib.hdq_w4_linear(x.data_ptr(), M, w.desc(), out.data_ptr(), y_dtype, s))
+        _keep, wp, wn = _scratch(ws, lib.hdq_w4_linear_workspace_bytes(M, w.N, K), dev)
+        _check("hdq_w4_linear", lib.hdq_w4_linear(x.data_ptr(), M, w.desc(), out.data_ptr(), y_dtype, wp, wn, s))
         return out
     return _launch(dev, stream, call)
 

@@ -698,9 +698,17 @@ int hdq_w4_quantize(const void *w, const hdq_w4_tensor *out, void *stream);
  * A group's sum is taken in float32 on the matrix instructions, as
  * sum (16 + u) x - (16 + z) sum x with exact products, and scaled and added in
  * float32; the error is that of a float32 sum over terms (32 + z) / |u - z| times
- * as large.  No workspace.
+ * as large.
+ *   ws, ws_bytes : device scratch, 256-byte aligned, >=
+ *       hdq_w4_linear_workspace_bytes(M, N, K) (NULL where that is 0, as for one
+ *       token of up to 32640 columns).  Nothing in it needs a value before the call; calls that
+ *       may overlap need their own.
  */
-int hdq_w4_linear(const void *x, int64_t M, const hdq_w4_tensor *w, void *y, int32_t y_dtype, void *stream);
+int hdq_w4_linear(const void *x, int64_t M, const hdq_w4_tensor *w, void *y, int32_t y_dtype, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* Scratch bytes hdq_w4_linear needs; 0 on bad arguments. */
+size_t hdq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* ---- heads: norms, rotary positions, a quantized key-value cache ---------------
  * What lies between a QKV projection and the attention.  A tensor of heads is

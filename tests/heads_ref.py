@@ -168,12 +168,13 @@ def w4_pack(codes, scale, zero, group):
     v = u.view(tn, 16, tk, 4, 4, 8).permute(0, 2, 4, 1, 3, 5)
     place = torch.tensor([4 * ((e >> 1) + 4 * (e & 1)) for e in range(8)])
     words = (v << place).sum(-1)
+    words = ((words << 3) & 0xffffffff) | (words >> 29)
     packed = torch.stack([(words >> (8 * i)) & 255 for i in range(4)], -1).to(torch.uint8).flatten()
 
     def per_group(t):
         full = torch.zeros(tn * 16, tk * groups, dtype=t.dtype)
         full[:N, :K // group] = t
-        return full.view(tn, 4, 4, tk, groups).permute(0, 3, 1, 4, 2).contiguous().flatten()
+        return full.view(tn, 16, tk, groups).transpose(1, 2).contiguous().flatten()
     return packed, per_group(scale), per_group(zero) if zero is not None else None
 
 

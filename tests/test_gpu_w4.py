@@ -104,11 +104,10 @@ def test_weights_past_32_bits():
     w.codes[-tail:] = torch.randint(0, 256, (tail,), device=DEV, dtype=torch.uint8)
     x = make((1, K), BF, 10)
     y = hdq.w4_linear(x.to(DEV), w, y_dtype=hdq.DTYPE_F32).cpu()
-    t = w.codes[-tail:].cpu().view(1100, 4, 16, 4, 4)[:, :, :3]    # [tile k][quarter][row][word][byte], the last tile's three rows
-    u = torch.empty(1100, 4, 3, 4, 8, dtype=torch.uint8)
-    for e in range(8):
-        n = (e >> 1) + 4 * (e & 1)
-        u[..., e] = (t[..., n // 2] >> (4 * (n % 2))) & 15
+    t = w.codes[-tail:].cpu().view(1100, 4, 16, 4, 4)[:, :, :3].long()    # [tile k][quarter][row][word][byte], the last tile's three rows
+    t = sum(t[..., i] << (8 * i) for i in range(4))
+    t = (t >> 3) | ((t & 7) << 29)
+    u = torch.stack([(t >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15 for e in range(8)], -1).to(torch.uint8)
     u = u.permute(2, 0, 3, 1, 4).reshape(3, K)
     codes, scale = u[:, 0::2] | (u[:, 1::2] << 4), torch.full((3, K // group), 0.01, dtype=BF)
     check(y[:, -3:], x, codes, scale, None, group)

@@ -65,21 +65,29 @@ def test_w4_pack_reference_is_a_bijection():
     """The reference packing keeps every code (all nibbles present once)."""
     codes, scale, zero = R.w4_random(33, 160, 32, True, 1)
     p, s, z = R.w4_pack(codes, scale, zero, 32)
-    u = torch.bincount(torch.cat((p & 15, p >> 4)).long(), minlength=16)
+    w = sum(p.view(-1, 4)[:, i].long() << (8 * i) for i in range(4))
+    w = (w >> 3) | ((w & 7) << 29)                # the words are kept rotated
+    u = torch.bincount(torch.stack([(w >> (4 * i)) & 15 for i in range(8)]).flatten(), minlength=16)
     want = torch.bincount(R.w4_values(codes).flatten().long(), minlength=16)
     want[0] += p.numel() * 2 - want.sum()
     assert torch.equal(u, want)
     # row 17, column 43: tile row 1, lane 17 % 16 + 16 * (43 / 8 % 4), word 43 / 32, nibble of 43 % 8 = 3
     lane, word, nib = 1 + 16 * (43 // 8 % 4), 43 // 32, (3 >> 1) + 4 * (3 & 1)
-    byte = p[((1 * 2 + 0) * 64 + lane) * 16 + word * 4 + nib // 2]
-    assert (int(byte) >> (4 * (nib % 2))) & 15 == int(R.w4_values(codes)[17, 43])
+    assert (int(w[((1 * 2 + 0) * 64 + lane) * 4 + word]) >> (4 * nib)) & 15 == int(R.w4_values(codes)[17, 43])
+    assert s[((1 * 2 + 1) * 16 + 1) * 4 + 0] == scale[17, 4] and z[((1 * 2 + 0) * 16 + 1) * 4 + 1] == zero[17, 1]
     assert s.numel() == 3 * 2 * 64 and z.numel() == 3 * 2 * 64
 
 
 def test_w4_refusals(hdq):
     L, T = hdq.lib, hdq.W4TensorDesc
     ok = T(100, 128, 64, FAKE, FAKE, None)
-    lin = lambda w=ok, x=FAKE, M=3, y=FAKE, t=1: L.hdq_w4_linear(x, M, w, y, t, None)
+    lin = lambda w=ok, x=FAKE, M=3, y=FAKE, t=1, ws=None, n=0: L.hdq_w4_linear(x, M, w, y, t, ws, n, None)
+    need, big = L.hdq_w4_linear_workspace_bytes(64, 100, 4096), T(100, 4096, 64, FAKE, FAKE, None)
+    assert need >= 2 * 64 * 100 * 4 and L.hdq_w4_linear_workspace_bytes(1, 100, 32640) == 0
+    assert lin(big, M=64) == hdq.ERR_WORKSPACE and lin(big, M=64, ws=FAKE, n=need - 1) == hdq.ERR_WORKSPACE
+    assert lin(big, M=64, ws=FAKE + 8, n=need) == hdq.ERR_SHAPE
+    for bad in ((0, 100, 4096), (64, 0, 4096), (64, 100, 40), ((1 << 20) + 1, 100, 64)):
+        assert L.hdq_w4_linear_workspace_bytes(*bad) == 0, bad
     assert lin(x=None) == hdq.ERR_INVALID and lin(y=None) == hdq.ERR_INVALID and lin(w=None) == hdq.ERR_INVALID
     assert lin(t=2) == hdq.ERR_UNSUPPORTED
     assert lin(M=-1) == hdq.ERR_SHAPE and lin(M=(1 << 20) + 1) == hdq.ERR_SHAPE
