@@ -47,25 +47,23 @@ __device__ __forceinline__ v8bf decode(uint32_t w) {
   return __builtin_bit_cast(v8bf, r);
 }
 
-// One tile of a row tile's weights as loaded: a lane's 32 codes, and the scales
-// (bf16) and zero points (bytes) of its row, l % 16.
-template <int GROUPS, bool ZERO>
-struct Tile {
-  v4u codes;
-  uint16_t scale[GROUPS];
-  uint8_t zero[ZERO ? GROUPS : 1];
-  __device__ __forceinline__ void load(const uint8_t* c, const uint16_t* s, const uint8_t* z, int64_t at) {
-    codes = *reinterpret_cast<const v4u*>(c + at * 1024);
-    __builtin_memcpy(scale, __builtin_assume_aligned(s + at * (16 * GROUPS), 2 * GROUPS), 2 * GROUPS);
-    if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z + at * (16 * GROUPS), GROUPS), GROUPS);
+// Scales (bf16) and zero points (bytes) of a lane's row, l % 16, in COUNT groups.
+template <int COUNT, bool ZERO>
+struct Groups {
+  uint16_t scale[COUNT];
+  uint8_t zero[ZERO ? COUNT : 1];
+  __device__ __forceinline__ void load(const uint16_t* s, const uint8_t* z) {
+    __builtin_memcpy(scale, __builtin_assume_aligned(s, 2 * COUNT), 2 * COUNT);
+    if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z, COUNT), COUNT);
   }
 };
 
 // y += the tile's product; x(m, s): tokens 16 m .. + 15, columns 32 s .. + 31.  Of
 // the lane's four results of an instruction, tokens 4 quad + r, the first R are
-// wanted.
-template <int MT, int NT, int R, int GROUPS, bool ZERO, typename X>
-__device__ __forceinline__ void multiply(const Tile<GROUPS, ZERO> (&t)[NT], const X& x, float (&y)[NT][MT][R]) {
+// wanted.  The tile's groups begin at group `at` of those loaded.
+template <int MT, int NT, int R, int GROUPS, int COUNT, bool ZERO, typename X>
+__device__ __forceinline__ void multiply(const v4u (&codes)[NT], const Groups<COUNT, ZERO> (&of)[NT], int at, const X& x,
+                                         float (&y)[NT][MT][R]) {
   constexpr int STEPS = 4 / GROUPS;
   const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
   const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -82,15 +80,15 @@ __device__ __forceinline__ void multiply(const Tile<GROUPS, ZERO> (&t)[NT], cons
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const v8bf b = decode(t[i].codes[q * STEPS + s]);
+        const v8bf b = decode(codes[i][q * STEPS + s]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) d[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m], b, s == 0 ? none : d[i][m], 0, 0, 0);
       }
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const float sc = __uint_as_float((uint32_t)t[i].scale[q] << 16);
-      const float off = ZERO ? 16.0f + (float)t[i].zero[ZERO ? q : 0] : 24.0f;
+      const float sc = __uint_as_float((uint32_t)of[i].scale[at + q] << 16);
+      const float off = ZERO ? 16.0f + (float)of[i].zero[ZERO ? at + q : 0] : 24.0f;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -113,38 +111,46 @@ __device__ __forceinline__ void store(const W4Args& g, void* y, int64_t m, int64
 
 // Up to 16 tokens whose columns fit LDS.  The workgroup keeps the tokens there
 // (a row's pitch is 16 bytes past a multiple of 256: a fragment's 16 rows fall on
-// all banks), and its waves stream weights, kDepth tiles in flight each:
-//   wk = 1: a wave takes `per` tiles of rows, one after the other -- their
-//           codes and scales are contiguous;
-//   wk > 1: wk waves share a tile of rows, each taking every wk-th tile of K,
+// all banks), and its waves stream weights in blocks of four tiles, 512
+// columns of 16 rows, whose scales are one load; the next block is in flight.
+//   wk = 1: a wave takes `per` tiles of rows, one after the other;
+//   wk > 1: wk waves share a tile of rows, each taking every wk-th block of K,
 //           and their sums meet in LDS, in order.
 // Token 4 r + q is row 4 q + r of the product, so that R results a lane hold up
 // to 4 R tokens.
-constexpr int kDepth = 4;
-
 template <int R, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
   extern __shared__ __align__(16) uint8_t s_lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / g.wk, wk = wave - wn * g.wk;
   const int col = lane & 15, quad = lane >> 4;
-  const int tiles_k = (int)g.tiles_k, pitch = tiles_k * 256 + 16;
+  const int tiles_k = (int)g.tiles_k, blocks = (tiles_k + 3) >> 2, pitch = tiles_k * 256 + 16;
   const int64_t tn0 = ((int64_t)blockIdx.x * g.wn + wn) * g.per;
   const int rows_here = (int)max((int64_t)0, min((int64_t)g.per, g.tiles_n - tn0));
-  const int first = g.wk > 1 ? wk : 0, step = g.wk;
-  const int count = rows_here == 0 ? 0 : g.wk > 1 ? (tiles_k - wk + step - 1) / step : rows_here * tiles_k;
 
-  // item i is tile first + i step of the wave's contiguous ones
-  const int64_t base = tn0 * tiles_k + first;
-  const uint8_t* codes = g.codes + base * 1024 + lane * 16;
-  const uint16_t* scale = g.scale + (base * 16 + col) * GROUPS;
-  const uint8_t* zero = ZERO ? g.zero + (base * 16 + col) * GROUPS : nullptr;
-  typedef Tile<GROUPS, ZERO> T;
-  T ring[kDepth][1];
-  auto load = [&](T& t, int i) { t.load(codes, scale, zero, (int64_t)i * step); };
+  struct Block {
+    v4u codes[4][1];
+    Groups<4 * GROUPS, ZERO> of[1];
+  };
+  auto load = [&](Block& t, int64_t tn, int b) {
+    const int64_t tile = tn * tiles_k + 4 * b, group = ((tn * blocks + b) * 16 + col) * (4 * GROUPS);
+    t.of[0].load(g.scale + group, ZERO ? g.zero + group : nullptr);
 #pragma unroll
-  for (int u = 0; u < kDepth; ++u)
-    if (u < count) load(ring[u][0], u);
+    for (int j = 0; j < 4; ++j)
+      if (4 * b + j < tiles_k) t.codes[j][0] = *reinterpret_cast<const v4u*>(g.codes + (tile + j) * 1024 + lane * 16);
+  };
+  // the wave's blocks: b = wk, wk + g.wk, ... of row tile tn, then of the next
+  int64_t tn = tn0;
+  int b = wk;
+  int count = rows_here * ((blocks - wk + g.wk - 1) / g.wk);
+  int64_t next_tn = tn0;
+  int next_b = wk;
+  auto advance = [&](int64_t& t, int& k) {
+    k += g.wk;
+    if (k >= blocks) k = wk, ++t;
+  };
+  Block ring[2];
+  if (count > 0) load(ring[0], next_tn, next_b);
 
   // the tokens, zeros past the last column
   const int pieces = tiles_k * 16, filled = (int)(g.K / 8);
@@ -160,28 +166,30 @@ __global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
   const uint8_t* xr = s_lds + (token < g.M ? token : 0) * pitch + quad * 16;
 
   float y[1][1][R] = {};
-  int kt = first;
-  int64_t tn = tn0;
-  auto work = [&](const T (&t)[1]) {
-    multiply<1, 1, R>(t, [&](int, int s) { return *reinterpret_cast<const v8bf*>(xr + kt * 256 + s * 64); }, y);
-    kt += step;
-    if (g.wk == 1 && kt == tiles_k) {
+  auto work = [&](const Block& t) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * b + j < tiles_k)
+        multiply<1, 1, R, GROUPS>(t.codes[j], t.of, j * GROUPS, [&](int, int s) {
+          return *reinterpret_cast<const v8bf*>(xr + (4 * b + j) * 256 + s * 64);
+        }, y);
+    const int64_t done = tn;
+    advance(tn, b);
+    if (g.wk == 1 && tn != done) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        store<F32>(g, g.y, 4 * r + quad, tn * 16 + col, y[0][0][r]);
+        store<F32>(g, g.y, 4 * r + quad, done * 16 + col, y[0][0][r]);
         y[0][0][r] = 0.0f;
       }
-      kt = 0;
-      ++tn;
     }
   };
-  for (int i = 0; i < count; i += kDepth) {
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u)
-      if (i + u < count) {
-        work(ring[u]);
-        if (i + u + kDepth < count) load(ring[u][0], i + u + kDepth);
-      }
+  for (; count > 0; count -= 2) {
+    if (count > 1) advance(next_tn, next_b), load(ring[1], next_tn, next_b);
+    work(ring[0]);
+    if (count > 1) {
+      if (count > 2) advance(next_tn, next_b), load(ring[0], next_tn, next_b);
+      work(ring[1]);
+    }
   }
   if (g.wk == 1) return;
   __syncthreads();  // the tokens are done with
@@ -218,14 +226,22 @@ __global__ __launch_bounds__(256, 2) void k_w4_shared(const W4Args g) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int64_t tile = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * g.tiles_k;  // past the end: the last again
+    const int64_t block = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * ((g.tiles_k + 3) >> 2);
     codes[i] = g.codes + tile * 1024 + lane * 16;
-    scale[i] = g.scale + (tile * 16 + col) * GROUPS;
-    zero[i] = ZERO ? g.zero + (tile * 16 + col) * GROUPS : nullptr;
+    scale[i] = g.scale + (block * 16 + col) * (4 * GROUPS);
+    zero[i] = ZERO ? g.zero + (block * 16 + col) * (4 * GROUPS) : nullptr;
   }
-  typedef Tile<GROUPS, ZERO> T;
-  auto load = [&](T (&t)[NT], int kt) {
+  struct Stage {
+    v4u codes[NT];
+    Groups<GROUPS, ZERO> of[NT];
+  };
+  auto load = [&](Stage& t, int kt) {
+    const int64_t at = (int64_t)(kt >> 2) * (64 * GROUPS) + (kt & 3) * GROUPS;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) t[i].load(codes[i], scale[i], zero[i], kt);
+    for (int i = 0; i < NT; ++i) {
+      t.codes[i] = *reinterpret_cast<const v4u*>(codes[i] + (int64_t)kt * 1024);
+      t.of[i].load(scale[i] + at, ZERO ? zero[i] + at : nullptr);
+    }
   };
   // the workgroup's tokens; pieces past the last token or column read zeros
   const int64_t here = g.M - m0 < 16 * MT ? g.M - m0 : 16 * MT;
@@ -241,7 +257,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_shared(const W4Args g) {
     }
   };
   float y[NT][MT][4] = {};
-  T w[2][NT];
+  Stage w[2];
   fetch(0, k0);
   load(w[0], k0);
   auto stage = [&](auto half, int kt) {
@@ -251,7 +267,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_shared(const W4Args g) {
       fetch(H ^ 1, kt + 1);
       load(w[H ^ 1], kt + 1);
     }
-    multiply<MT, NT, 4>(w[H], [&](int m, int s) {
+    multiply<MT, NT, 4, GROUPS>(w[H].codes, w[H].of, 0, [&](int m, int s) {
       return *reinterpret_cast<const v8bf*>(&s_x[H][(m * 16 + col) * 256 + (((4 * s + quad) ^ col) * 16)]);
     }, y);
   };
@@ -321,11 +337,15 @@ __global__ __launch_bounds__(256) void k_w4_pack(const uint8_t* __restrict__ src
   }
   reinterpret_cast<uint4*>(out.codes)[tile * 64 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
   const int groups = 128 / group;
-  if (lane < 16 * groups) {  // [16 rows][groups]
-    const int64_t r = tn * 16 + lane / groups, kg = tk * groups + lane % groups, kgs = K / group;
+  // the row tile's last wave also clears the rest of its block of four tiles
+  const int64_t end = tk + 1 == tiles_k ? (tiles_k + 3) / 4 * 4 : tk + 1;
+  for (int64_t k = tk; k < end; ++k) {
+    if (lane >= 16 * groups) break;
+    const int64_t n = lane / groups, r = tn * 16 + n, kg = k * groups + lane % groups, kgs = K / group;
+    const int64_t at = w4_group_at(tn, n, kg, tiles_k, groups);
     const bool in = r < N && kg < kgs;
-    out.scale[tile * 16 * groups + lane] = in ? scale[r * kgs + kg] : (uint16_t)0;
-    if (out.zero != nullptr) out.zero[tile * 16 * groups + lane] = in ? zero[r * kgs + kg] : (uint8_t)0;
+    out.scale[at] = in ? scale[r * kgs + kg] : (uint16_t)0;
+    if (out.zero != nullptr) out.zero[at] = in ? zero[r * kgs + kg] : (uint8_t)0;
   }
 }
 
@@ -337,7 +357,7 @@ __global__ __launch_bounds__(256) void k_w4_pack(const uint8_t* __restrict__ src
 __global__ __launch_bounds__(256) void k_w4_quantize(const uint16_t* __restrict__ src, int64_t N, int64_t K, int group,
                                                      int64_t tiles_n, int64_t tiles_k, W4Out out) {
   const int groups = 128 / group;
-  const int64_t kgs = tiles_k * groups, id = (int64_t)wide_block() * 256 + threadIdx.x;
+  const int64_t kgs = (tiles_k + 3) / 4 * 4 * groups, id = (int64_t)wide_block() * 256 + threadIdx.x;
   const int64_t row = id / kgs, kg = id - row * kgs;
   if (row >= tiles_n * 16) return;
   const bool in = row < N && kg * group < K;
@@ -362,9 +382,10 @@ __global__ __launch_bounds__(256) void k_w4_quantize(const uint16_t* __restrict_
   const float z = zp ? (s > 0.0f ? fminf(rintf(-lo / s), 15.0f) : 0.0f) : 8.0f;
   const int64_t tile = (row >> 4) * tiles_k + kg / groups;
   const int q = (int)(kg % groups), n = (int)(row & 15);
-  const int64_t at = (tile * 16 + n) * groups + q;
+  const int64_t at = w4_group_at(row >> 4, n, kg, tiles_k, groups);
   out.scale[at] = finite ? (s > 0.0f ? (uint16_t)bits : (uint16_t)0) : (uint16_t)0x7fc0;
   if (zp) out.zero[at] = in ? (uint8_t)z : (uint8_t)0;
+  if (kg >= tiles_k * groups) return;
   for (int i = 0; i < group / 8; ++i) {
     uint32_t w = 0;
     if (in) {
@@ -434,7 +455,7 @@ hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scale, const uin
 }
 
 hipError_t launch_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, const W4Out& out, hipStream_t s) {
-  const int64_t tn = w4_tiles_n(N), tk = w4_tiles_k(K), threads = tn * 16 * tk * (128 / group);
+  const int64_t tn = w4_tiles_n(N), tk = w4_tiles_k(K), threads = tn * 16 * ((tk + 3) / 4 * 4) * (128 / group);
   k_w4_quantize<<<wide_grid((threads + 255) / 256), dim3(256), 0, s>>>(w, N, K, group, tn, tk, out);
   return hipGetLastError();
 }

@@ -1,13 +1,14 @@
 // w4_plan.h -- sizes of packed 4-bit weights and how the few-token product
-// spreads over waves (host code alone).
+// spreads over waves (no HIP types).
 //
 // Rows go in tiles of 16 and columns in tiles of 128, both rounded up:
 //   codes [N / 16][K / 128][64 lanes][16 bytes]: lane l holds row l % 16 and, in
 //         32-bit word s, columns 32 s + 8 (l / 16) .. + 7 of the tile, in nibbles
 //         0 4 1 5 2 6 3 7 (columns 0, 1 are nibbles 0 and 4, ...), the word
 //         rotated left by 3 bits;
-//   scale [N / 16][K / 128][16][128 / group] bf16, zero the same in bytes.
-// Padding holds zeros (scale 0).
+//   scale [N / 16][K / 512][16][512 / group] bf16 (four tiles of a row in one
+//         load), zero the same in bytes.
+// Padding holds zeros.
 #pragma once
 
 #include <stddef.h>
@@ -21,7 +22,14 @@ inline int64_t w4_tiles_n(int64_t N) { return (N + kW4TileN - 1) / kW4TileN; }
 inline int64_t w4_tiles_k(int64_t K) { return (K + kW4TileK - 1) / kW4TileK; }
 inline size_t w4_code_bytes(int64_t N, int64_t K) { return (size_t)(w4_tiles_n(N) * w4_tiles_k(K)) * 1024; }
 inline size_t w4_scale_count(int64_t N, int64_t K, int group) {
-  return (size_t)(w4_tiles_n(N) * w4_tiles_k(K)) * (size_t)(16 * (kW4TileK / group));
+  return (size_t)(w4_tiles_n(N) * ((w4_tiles_k(K) + 3) / 4)) * (size_t)(64 * (kW4TileK / group));
+}
+// Index of group kg of row n of row tile tn; groups: of a tile.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline int64_t w4_group_at(int64_t tn, int64_t n, int64_t kg, int64_t tiles_k, int groups) {
+  return ((tn * ((tiles_k + 3) / 4) + kg / (4 * groups)) * 16 + n) * (4 * groups) + kg % (4 * groups);
 }
 
 // Up to 16 tokens that fit LDS: a workgroup keeps them there and streams
@@ -39,9 +47,9 @@ struct W4Plan {
 };
 
 #ifndef WW
-#define WW 8192
+#define WW 4096
 #endif
-constexpr int64_t kW4Waves = WW;       // waves wanted of k_w4: 32 for each CU
+constexpr int64_t kW4Waves = WW;       // waves wanted of k_w4: 16 for each CU
 constexpr size_t kW4Lds = 64 << 10;    // LDS its tokens may take
 constexpr int64_t kW4Groups = 256;     // workgroups wanted of k_w4_shared
 constexpr int64_t kW4LeastTiles = 4;   // tiles of K that a split keeps at least
@@ -53,11 +61,12 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
   p.lds = (size_t)M * (size_t)(tk * 256 + 16);
   if (tm == 1 && p.lds <= kW4Lds) {
     p.grid_y = 1;
-    // waves of a tile of rows: as many as there are tiles to go round, two or more of K each
-    int64_t wk = kW4Waves / tn < tk / 2 ? kW4Waves / tn : tk / 2;
+    // waves of a tile of rows: as many as there are blocks of four tiles of K, and tiles of rows to go round
+    const int64_t blocks = (tk + 3) / 4;
+    int64_t wk = kW4Waves / tn < blocks ? kW4Waves / tn : blocks;
     wk = wk > 16 ? 16 : wk < 1 ? 1 : wk;
-    const int64_t each = (tk + wk - 1) / wk;  // the same number of tiles for each, as far as that goes
-    wk = (tk + each - 1) / each;
+    const int64_t each = (blocks + wk - 1) / wk;  // the same number of blocks for each, as far as that goes
+    wk = (blocks + each - 1) / each;
     p.wk = (int)wk;
     p.wn = wk >= 4 ? 1 : (int)(8 / wk);
     p.per = wk > 1 ? 1 : (int)((tn + kW4Waves - 1) / kW4Waves);

@@ -172,9 +172,9 @@ def w4_pack(codes, scale, zero, group):
     packed = torch.stack([(words >> (8 * i)) & 255 for i in range(4)], -1).to(torch.uint8).flatten()
 
     def per_group(t):
-        full = torch.zeros(tn * 16, tk * groups, dtype=t.dtype)
+        full = torch.zeros(tn * 16, -(-tk // 4) * 4 * groups, dtype=t.dtype)
         full[:N, :K // group] = t
-        return full.view(tn, 16, tk, groups).transpose(1, 2).contiguous().flatten()
+        return full.view(tn, 16, -1, 4 * groups).transpose(1, 2).contiguous().flatten()
     return packed, per_group(scale), per_group(zero) if zero is not None else None
 
 

@@ -53,7 +53,7 @@ def test_constants_match_the_header(hdq):
 
 def test_w4_bytes(hdq):
     assert hdq.lib.hdq_w4_bytes(1, 32, 32, 0) == 1024 and hdq.lib.hdq_w4_bytes(17, 160, 32, 0) == 4 * 1024
-    assert hdq.lib.hdq_w4_bytes(17, 160, 32, 1) == 4 * 128 and hdq.lib.hdq_w4_bytes(17, 160, 32, 2) == 4 * 64
+    assert hdq.lib.hdq_w4_bytes(17, 160, 32, 1) == 2 * 512 and hdq.lib.hdq_w4_bytes(17, 160, 32, 2) == 2 * 256
     assert hdq.lib.hdq_w4_bytes(5760, 1920, 128, 0) == 5760 * 1920 // 2
     assert hdq.lib.hdq_w4_bytes(1 << 27, 1 << 22, 64, 0) == 1 << 48
     for bad in ((0, 32, 32, 0), (1, 0, 32, 0), (1, 48, 32, 0), (1, 64, 16, 0), (1, 160, 64, 0), (1, 64, 64, 3),
@@ -74,8 +74,8 @@ def test_w4_pack_reference_is_a_bijection():
     # row 17, column 43: tile row 1, lane 17 % 16 + 16 * (43 / 8 % 4), word 43 / 32, nibble of 43 % 8 = 3
     lane, word, nib = 1 + 16 * (43 // 8 % 4), 43 // 32, (3 >> 1) + 4 * (3 & 1)
     assert (int(w[((1 * 2 + 0) * 64 + lane) * 4 + word]) >> (4 * nib)) & 15 == int(R.w4_values(codes)[17, 43])
-    assert s[((1 * 2 + 1) * 16 + 1) * 4 + 0] == scale[17, 4] and z[((1 * 2 + 0) * 16 + 1) * 4 + 1] == zero[17, 1]
-    assert s.numel() == 3 * 2 * 64 and z.numel() == 3 * 2 * 64
+    assert s[(1 * 16 + 1) * 16 + 4] == scale[17, 4] and z[(1 * 16 + 1) * 16 + 1] == zero[17, 1]
+    assert s.numel() == 3 * 256 and z.numel() == 3 * 256
 
 
 def test_w4_refusals(hdq):
