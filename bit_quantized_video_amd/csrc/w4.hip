@@ -52,9 +52,10 @@ template <int COUNT, bool ZERO>
 struct Groups {
   uint16_t scale[COUNT];
   uint8_t zero[ZERO ? COUNT : 1];
-  __device__ __forceinline__ void load(const uint16_t* s, const uint8_t* z) {
-    __builtin_memcpy(scale, __builtin_assume_aligned(s, 2 * COUNT), 2 * COUNT);
-    if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z, COUNT), COUNT);
+  // from scalar bases on
+  __device__ __forceinline__ void load(const uint16_t* s, const uint8_t* z, uint32_t at) {
+    __builtin_memcpy(scale, __builtin_assume_aligned(s + at, 2 * COUNT), 2 * COUNT);
+    if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z + at, COUNT), COUNT);
   }
 };
 
@@ -117,9 +118,9 @@ __device__ __forceinline__ void store(const W4Args& g, void* y, int64_t m, int64
 //   wk > 1: wk waves share a tile of rows, each taking every wk-th block of K,
 //           and their sums meet in LDS, in order.
 // Token 4 r + q is row 4 q + r of the product, so that R results a lane hold up
-// to 4 R tokens.
+// to 4 R tokens (R = 4: at most 8 waves, more than 8 tokens' 28 tiles have no more blocks).
 template <int R, int GROUPS, bool ZERO, bool F32>
-__global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
+__global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
   extern __shared__ __align__(16) uint8_t s_lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / g.wk, wk = wave - wn * g.wk;
@@ -133,11 +134,11 @@ __global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
     Groups<4 * GROUPS, ZERO> of[1];
   };
   auto load = [&](Block& t, int64_t tn, int b) {
-    const int64_t tile = tn * tiles_k + 4 * b, group = ((tn * blocks + b) * 16 + col) * (4 * GROUPS);
-    t.of[0].load(g.scale + group, ZERO ? g.zero + group : nullptr);
+    const int64_t tile = tn * tiles_k + 4 * b, group = (tn * blocks + b) * (64 * GROUPS);
+    t.of[0].load(g.scale + group, ZERO ? g.zero + group : nullptr, col * (4 * GROUPS));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (4 * b + j < tiles_k) t.codes[j][0] = *reinterpret_cast<const v4u*>(g.codes + (tile + j) * 1024 + lane * 16);
+      if (4 * b + j < tiles_k) t.codes[j][0] = reinterpret_cast<const v4u*>(g.codes + (tile + j) * 1024)[lane];
   };
   // the wave's blocks: b = wk, wk + g.wk, ... of row tile tn, then of the next
   int64_t tn = tn0;
@@ -206,82 +207,109 @@ __global__ __launch_bounds__(1024) void k_w4(const W4Args g) {
   }
 }
 
-// More tokens, or longer ones.  A workgroup of four waves takes 16 MT tokens x 128 rows
-// (two tiles each); the tokens' 128 columns of a stage lie in LDS, shared by
-// the waves, in rows of 16 pieces of 16 bytes, piece p of row r at p ^ (r % 16),
-// so that a fragment's 16 rows fall on all banks.  They are loaded straight to
-// LDS, a stage ahead.
-template <int MT, int GROUPS, bool ZERO, bool F32>
-__global__ __launch_bounds__(256, 2) void k_w4_shared(const W4Args g) {
-  constexpr int NT = 2;
-  __shared__ __align__(1024) uint8_t s_x[2][MT * 4096];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quad = lane >> 4;
-  const int64_t tn0 = ((int64_t)blockIdx.x * 4 + wave) * NT, m0 = (int64_t)blockIdx.y * (16 * MT);
+// More tokens, or longer ones.  A workgroup of eight waves takes 16 MT MW tokens
+// x 128 rows, 128 columns a stage; a wave multiplies MT tiles of tokens and NT
+// of rows, MW waves sharing the rows.  The tokens lie in LDS in rows of 16
+// pieces of 16 bytes, piece p of row r at p ^ (r % 16), so that a fragment's 16
+// rows fall on all banks.  Loads run two stages ahead in registers (memory
+// takes longer than a stage), none of them under a condition: the waits then
+// count the ones that may still be in flight.
+template <int MW, int MT, int NT, int GROUPS, bool ZERO, bool F32>
+__global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
+  static_assert(NT * (8 / MW) == 8, "128 rows a workgroup");
+  constexpr int TILES = MT * MW;            // of 16 tokens
+  constexpr int PIECES = (TILES + 1) / 2;   // of the tokens a thread brings
+  __shared__ __align__(16) uint8_t s_x[2][TILES * 4096];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, quad = lane >> 4, wm = wave % MW;
+  const int64_t tn0 = (int64_t)blockIdx.x * 8 + wave / MW * NT, m0 = (int64_t)blockIdx.y * (16 * TILES);
   const int each = (int)((g.tiles_k + g.split - 1) / g.split);
   const int k0 = (int)blockIdx.z * each, k1 = min(k0 + each, (int)g.tiles_k);
+  // scalar bases; the lane's part of an address is the same in every stage
   const uint8_t* codes[NT];
   const uint16_t* scale[NT];
   const uint8_t* zero[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int64_t tile = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * g.tiles_k;  // past the end: the last again
-    const int64_t block = (tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1) * ((g.tiles_k + 3) >> 2);
-    codes[i] = g.codes + tile * 1024 + lane * 16;
-    scale[i] = g.scale + (block * 16 + col) * (4 * GROUPS);
-    zero[i] = ZERO ? g.zero + (block * 16 + col) * (4 * GROUPS) : nullptr;
+    const int64_t tile = tn0 + i < g.tiles_n ? tn0 + i : g.tiles_n - 1;  // past the end: the last again
+    const int64_t block = tile * ((g.tiles_k + 3) >> 2);
+    codes[i] = g.codes + tile * g.tiles_k * 1024;
+    scale[i] = g.scale + block * (64 * GROUPS);
+    zero[i] = ZERO ? g.zero + block * (64 * GROUPS) : nullptr;
   }
+  // the workgroup's tokens: the thread's rows are tid / 16 + 32 j; pieces past the last token or column read zeros
+  const int64_t here = g.M - m0 < 16 * TILES ? g.M - m0 : 16 * TILES;
+  const uint32_t bytes = (uint32_t)(here * g.K * 2), k_bytes = (uint32_t)(g.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.K, bytes);
+  const int row = tid >> 4, piece = tid & 15;
+  uint32_t from[PIECES];
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) from[j] = row + 32 * j < here ? (row + 32 * j) * k_bytes + piece * 16 : bytes;
+  const int last = (int)g.tiles_k - 1;
+  const bool past = (uint32_t)last * 256 + piece * 16 >= k_bytes;  // of the last tile
   struct Stage {
     v4u codes[NT];
     Groups<GROUPS, ZERO> of[NT];
+    uint4 x[PIECES];
   };
   auto load = [&](Stage& t, int kt) {
+    kt = min(kt, k1 - 1);  // past the end: the last again
     const int64_t at = (int64_t)(kt >> 2) * (64 * GROUPS) + (kt & 3) * GROUPS;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      t.codes[i] = *reinterpret_cast<const v4u*>(codes[i] + (int64_t)kt * 1024);
-      t.of[i].load(scale[i] + at, ZERO ? zero[i] + at : nullptr);
+      t.codes[i] = reinterpret_cast<const v4u*>(codes[i] + (int64_t)kt * 1024)[lane];
+      t.of[i].load(scale[i] + at, ZERO ? zero[i] + at : nullptr, col * (4 * GROUPS));
     }
-  };
-  // the workgroup's tokens; pieces past the last token or column read zeros
-  const int64_t here = g.M - m0 < 16 * MT ? g.M - m0 : 16 * MT;
-  const uint32_t bytes = (uint32_t)(here * g.K * 2);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.K, bytes);
-  auto fetch = [&](int buf, int kt) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int piece = (wave * MT + j) * 64 + lane, row = piece >> 4, c = (piece & 15) ^ (row & 15);
-      const bool in = row < here && (int64_t)kt * 128 + c * 8 < g.K;
-      const uint32_t at = in ? (uint32_t)((int64_t)row * g.K + (int64_t)kt * 128 + c * 8) * 2 : bytes;
-      lds_dma16(xr, &s_x[buf][(wave * MT + j) * 1024], at, 0);
-    }
+    for (int j = 0; j < PIECES; ++j) t.x[j] = buf_load16(xr, past && kt == last ? bytes : from[j], kt * 256);
+  };
+  auto place = [&](const Stage& t, int kt) {
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
+      if (TILES % 2 == 0 || row < 16)
+        *reinterpret_cast<uint4*>(&s_x[kt & 1][(row + 32 * j) * 256 + ((piece ^ (row & 15)) * 16)]) = t.x[j];
   };
   float y[NT][MT][4] = {};
-  Stage w[2];
-  fetch(0, k0);
+  Stage w[3];
   load(w[0], k0);
-  auto stage = [&](auto half, int kt) {
-    constexpr int H = decltype(half)::value;
-    stage_barrier();  // this stage has arrived, and the last one's reads are done
-    if (kt + 1 < k1) {
-      fetch(H ^ 1, kt + 1);
-      load(w[H ^ 1], kt + 1);
-    }
+  load(w[1], k0 + 1);
+  place(w[0], k0);
+  auto stage = [&](auto slot, int kt) {
+    constexpr int H = decltype(slot)::value;
+    lds_only_barrier();  // the stage's tokens are there, and the other half is read
+    load(w[(H + 2) % 3], kt + 2);
+    const uint8_t* xs = s_x[kt & 1] + wm * (MT * 4096) + col * 256;
     multiply<MT, NT, 4, GROUPS>(w[H].codes, w[H].of, 0, [&](int m, int s) {
-      return *reinterpret_cast<const v8bf*>(&s_x[H][(m * 16 + col) * 256 + (((4 * s + quad) ^ col) * 16)]);
+      return *reinterpret_cast<const v8bf*>(xs + m * 4096 + (((4 * s + quad) ^ col) * 16));
     }, y);
+    place(w[(H + 1) % 3], kt + 1);
   };
-  for (int kt = k0; kt < k1; kt += 2) {
+  int kt = k0;
+  for (; kt + 2 < k1; kt += 3) {
     stage(std::integral_constant<int, 0>(), kt);
-    if (kt + 1 < k1) stage(std::integral_constant<int, 1>(), kt + 1);
+    stage(std::integral_constant<int, 1>(), kt + 1);
+    stage(std::integral_constant<int, 2>(), kt + 2);
   }
-  void* out = g.split > 1 ? static_cast<float*>(g.y) + blockIdx.z * g.slice : g.y;
+  if (kt < k1) stage(std::integral_constant<int, 0>(), kt);
+  if (kt + 1 < k1) stage(std::integral_constant<int, 1>(), kt + 1);
+  constexpr int kOut = F32 ? 4 : 2;
+  const int64_t pitch = g.N * kOut, first = m0 + wm * (MT * 16) + quad * 4;
+  char* out = static_cast<char*>(g.y) + (g.split > 1 ? blockIdx.z * g.slice * 4 : 0) + first * pitch + (tn0 * 16 + col) * kOut;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int r = 0; r < 4; ++r) {
+      char* p = out + (m * 16 + r) * pitch;
+      if (first + m * 16 + r >= g.M) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) store<F32>(g, out, m0 + m * 16 + quad * 4 + r, (tn0 + i) * 16 + col, y[i][m][r]);
+      for (int i = 0; i < NT; ++i)
+        if ((tn0 + i) * 16 + col < g.N) {
+          if (F32)
+            reinterpret_cast<float*>(p)[i * 16] = y[i][m][r];
+          else
+            reinterpret_cast<uint16_t*>(p)[i * 16] = (uint16_t)pack_bf16x2(y[i][m][r], 0.0f);
+        }
+    }
 }
 
 // Sums of the splits, in order: 4 outputs a thread.
@@ -290,8 +318,15 @@ __global__ __launch_bounds__(256) void k_w4_join(const float* __restrict__ sums,
                                                  void* __restrict__ y) {
   const int64_t i = ((int64_t)wide_block() * 256 + threadIdx.x) * 4;
   if (i >= count) return;
-  v4f v = *reinterpret_cast<const v4f*>(sums + i);
-  for (int k = 1; k < split; ++k) v += *reinterpret_cast<const v4f*>(sums + k * slice + i);
+  v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < split; k += 8) {  // eight loads in flight
+    v4f part[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      part[u] = k + u < split ? *reinterpret_cast<const v4f*>(sums + (k + u) * slice + i) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += part[u];
+  }
   const v2u w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   if (i + 4 <= count) {
     if (F32)
@@ -412,20 +447,20 @@ void run(const W4Args& a, const W4Plan& p, hipStream_t s) {
   else if (p.per > 0)
     k_w4<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.mt == 4)
-    k_w4_shared<4, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<2, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 2)
-    k_w4_shared<2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<2, 1, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else
-    k_w4_shared<1, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<1, 1, 1, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
 }
 
 template <bool F32>
 void run_group(const W4Args& a, const W4Plan& p, int group, hipStream_t s) {
   const bool z = a.zero != nullptr;
   switch (group) {
-    case 32: z ? run<4, true, F32>(a, p, s) : run<4, false, F32>(a, p, s); break;
-    case 64: z ? run<2, true, F32>(a, p, s) : run<2, false, F32>(a, p, s); break;
-    default: z ? run<1, true, F32>(a, p, s) : run<1, false, F32>(a, p, s); break;
+    case 32: return z ? run<4, true, F32>(a, p, s) : run<4, false, F32>(a, p, s);
+    case 64: return z ? run<2, true, F32>(a, p, s) : run<2, false, F32>(a, p, s);
+    default: return z ? run<1, true, F32>(a, p, s) : run<1, false, F32>(a, p, s);
   }
 }
 

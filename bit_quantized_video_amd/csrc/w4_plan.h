@@ -46,12 +46,12 @@ struct W4Plan {
   int64_t grid_x, grid_y;
 };
 
-#ifndef WW
-#define WW 4096
-#endif
-constexpr int64_t kW4Waves = WW;       // waves wanted of k_w4: 16 for each CU
+constexpr int64_t kW4Waves = 4096;       // waves wanted of k_w4: 16 for each CU
 constexpr size_t kW4Lds = 64 << 10;    // LDS its tokens may take
-constexpr int64_t kW4Groups = 256;     // workgroups wanted of k_w4_shared
+#ifndef WG
+#define WG 256
+#endif
+constexpr int64_t kW4Groups = WG;     // workgroups wanted of k_w4_shared
 constexpr int64_t kW4LeastTiles = 4;   // tiles of K that a split keeps at least
 
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
@@ -74,7 +74,7 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
     if (wk > 1 && p.lds < (size_t)(p.wn * p.wk) * 1024) p.lds = (size_t)(p.wn * p.wk) * 1024;
   } else {
     p.mt = tm == 1 ? 1 : tm == 2 ? 2 : 4;
-    p.wn = 4;
+    p.wn = 8;
     p.wk = 1;
     p.grid_x = (tn + 7) / 8;
     p.grid_y = (tm + p.mt - 1) / p.mt;
