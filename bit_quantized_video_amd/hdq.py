@@ -9,6 +9,7 @@ is no CPU fallback.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -838,9 +839,10 @@ class W4Weights:
         self.zero = torch.empty(sizes[2], dtype=torch.uint8, device=device) if zero_points else None
         self._desc = W4TensorDesc(N, K, group, self.codes.data_ptr(), self.scale.data_ptr(),
                                   self.zero.data_ptr() if zero_points else None)
+        self._ref = _c.byref(self._desc)
 
     def desc(self):
-        return self._desc
+        return self._ref
 
 
 def w4_pack(codes, scale, zero=None, stream=None):
@@ -894,8 +896,10 @@ def w4_linear(x, w, y=None, y_dtype=DTYPE_BF16, ws=None, stream=None):
         _operand(y, "y", dt, (M, w.N), dev)
 
     def call(s):
-        out = torch.empty(M, w.N, dtype=dt, device=dev) if y is None else y
-        _keep, wp, wn = _scratch(ws, lib.hdq_w4_linear_workspace_bytes(M, w.N, K), dev)
+        out = x.new_empty((M, w.N), dtype=dt) if y is None else y
+        # few tokens in short rows need none
+        need = 0 if M <= 16 and M * K <= 24576 else lib.hdq_w4_linear_workspace_bytes(M, w.N, K)
+        _keep, wp, wn = _scratch(ws, need, dev)
         _check("hdq_w4_linear", lib.hdq_w4_linear(x.data_ptr(), M, w.desc(), out.data_ptr(), y_dtype, wp, wn, s))
         return out
     return _launch(dev, stream, call)
@@ -930,67 +934,96 @@ class Rope:
             turns = torch.cat([rope_turns(d, base, scaling, factor, length, ramp) for d in dims]).to(device or "cuda")
         _operand(turns, "turns", torch.float64, (sum(dims) // 2,), turns.device)
         self.dims, self.dim, self.axes, self.layout, self.scale, self.turns = dims, sum(dims), len(dims), layout, scale, turns
-        self._dims = (_c.c_int32 * 3)(*dims)
-        self._turns = turns.data_ptr()
+        self._device = turns.device
+        self._fixed = (layout, self.dim, self.axes, *dims, *(0,) * (3 - len(dims)), scale, turns.data_ptr())
 
     def desc(self, positions, batch, length, dev):
-        """RopeDesc with positions int64 [axes, batch, length]; [batch, length] or
+        """hdq_rope with positions int64 [axes, batch, length]; [batch, length] or
         [length] for one axis and [axes, length], the same in every sequence."""
-        if positions.dtype != torch.int64 or positions.device != dev or self.turns.device != dev:
+        if positions.dtype is not _I64 or positions.device != dev or self._device != dev:
             raise ValueError(f"positions: expected int64 on {dev}, got {positions.dtype} on {positions.device}; "
-                             f"turns on {self.turns.device}")
-        shape, st, axes = tuple(positions.shape), positions.stride(), self.axes
+                             f"turns on {self._device}")
+        shape, st, axes = positions.shape, positions.stride(), self.axes
         if shape == (axes, batch, length):
-            st = st
+            a, b, t = st
         elif axes == 1 and shape == (batch, length):
-            st = (0, *st)
+            a, (b, t) = 0, st
         elif axes == 1 and shape == (length,):
-            st = (0, 0, *st)
+            a, b, t = 0, 0, st[0]
         elif shape == (axes, length):
-            st = (st[0], 0, st[1])
+            a, b, t = st[0], 0, st[1]
         else:
-            raise ValueError(f"positions {shape} for {axes} axes, {batch} sequences of {length}")
-        return RopeDesc(self.layout, self.dim, axes, self._dims, self.scale, self._turns, positions.data_ptr(), *st)
+            raise ValueError(f"positions {tuple(shape)} for {axes} axes, {batch} sequences of {length}")
+        return _ROPE.pack(*self._fixed, positions.data_ptr(), a, b, t)
 
 
-_ROW_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_F32, _BF16, _I64 = torch.float32, torch.bfloat16, torch.int64
+# hdq_heads, hdq_head_norm and hdq_rope as bytes, in C's layout (see HeadsDesc, HeadNormDesc, RopeDesc): several
+# of them are made for every call, and packing takes a fraction of a ctypes structure's time
+_HEADS, _NORM, _ROPE = struct.Struct("Piiqqq"), struct.Struct("ifPPPP"), struct.Struct("iii3ifPPqqq")
+
+
+def _entry(name, pointers):
+    """lib's function `name` with these arguments taken as addresses or bytes."""
+    f = lib[name]
+    f.restype, types = _c.c_int, list(getattr(lib, name).argtypes)
+    for i in pointers:
+        types[i] = _c.c_char_p
+    f.argtypes = types
+    return f
+
+
+_qk_norm_rope = _entry("hdq_qk_norm_rope", (0, 1, 5, 6, 7, 8))
+_qkv_to_cache = _entry("hdq_qkv_to_cache", (0, 1, 2, 5, 6, 7))
 
 
 def _head_shape(x, name):
     """(batch, length, heads, dim) of a view [batch, length, heads, dim] or [length, heads, dim]."""
     shape = x.shape
-    if len(shape) == 3:
-        shape = (1, *shape)
-    if len(shape) != 4:
-        raise ValueError(f"{name}: expected [batch, length, heads, dim] or [length, heads, dim], got {tuple(x.shape)}")
-    return shape
+    if len(shape) == 4:
+        return shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: expected [batch, length, heads, dim] or [length, heads, dim], got {tuple(shape)}")
+    return (1, *shape)
 
 
-def _heads(x, name, dev):
-    """hdq_heads of a view whose last dimension is contiguous."""
-    st, dt = x.stride(), _ROW_DTYPES.get(x.dtype)
-    if dt is None or x.device != dev or (st[-1] != 1 and x.shape[-1] != 1):
+def _row_dtype(dtype):
+    return DTYPE_BF16 if dtype is _BF16 else DTYPE_F32 if dtype is _F32 else -1
+
+
+def _heads(x, name, heads, dim, dev):
+    """hdq_heads of a view of `heads` heads whose last dimension is contiguous."""
+    st, dt = x.stride(), _row_dtype(x.dtype)
+    if dt < 0 or x.device != dev or (st[-1] != 1 and dim != 1):
         raise ValueError(f"{name}: expected bfloat16 or float32 on {dev} with contiguous heads, got {x.dtype} on "
                          f"{x.device}, strides {st}")
-    return HeadsDesc(x.data_ptr(), dt, x.shape[-2], st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    if len(st) == 4:
+        b, t, h, _ = st
+    else:
+        b, (t, h, _) = 0, st
+    return _HEADS.pack(x.data_ptr(), dt, heads, b, t, h)
 
 
-def _head_norm(norm, eps, dim, dev, *weights):
-    if norm == HEAD_NORM_NONE:
+def _head_norm(kind, eps, dim, dev, qw, qb, kw, kb):
+    if kind == HEAD_NORM_NONE:
         return None
-    ptrs = [_operand(w, "norm weight or bias", torch.float32, (dim,), dev).data_ptr() if w is not None else None
-            for w in weights]
-    return HeadNormDesc(norm, eps, *ptrs)
+    shape = (dim,)
+    return _NORM.pack(kind, eps, 0 if qw is None else _operand(qw, "q_weight", _F32, shape, dev).data_ptr(),
+                      0 if qb is None else _operand(qb, "q_bias", _F32, shape, dev).data_ptr(),
+                      0 if kw is None else _operand(kw, "k_weight", _F32, shape, dev).data_ptr(),
+                      0 if kb is None else _operand(kb, "k_bias", _F32, shape, dev).data_ptr())
 
 
-def _new_heads(out, x, dtype):
-    """out, checked against x's shape, or a new contiguous tensor (dtype None: x's)."""
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype if dtype is None else torch.float32 if dtype == DTYPE_F32 else torch.bfloat16,
-                           device=x.device)
-    if out.shape != x.shape:
-        raise ValueError(f"output {tuple(out.shape)} for an input {tuple(x.shape)}")
-    return out
+def _out_heads(out, x, shape, y_dtype, name, dev):
+    """(out or a new contiguous tensor of y_dtype (None: x's), its hdq_heads)."""
+    B, T, H, D = shape
+    if out is not None:
+        if out.shape != x.shape:
+            raise ValueError(f"{name} {tuple(out.shape)} for an input {tuple(x.shape)}")
+        return out, _heads(out, name, H, D, dev)
+    sizes = (B, T, H, D) if x.dim() == 4 else (T, H, D)
+    out = x.new_empty(sizes) if y_dtype is None else x.new_empty(sizes, dtype=_F32 if y_dtype == DTYPE_F32 else _BF16)
+    return out, _HEADS.pack(out.data_ptr(), _row_dtype(out.dtype), H, T * H * D, H * D, D)
 
 
 def _rope_desc(rope, positions, batch, length, dev):
@@ -1008,23 +1041,24 @@ def qk_norm_rope(q, k=None, norm=HEAD_NORM_NONE, q_weight=None, k_weight=None, q
     rotated.  Any strides but the last; outputs are new contiguous tensors (of
     y_dtype, None: the input's) or q_out and k_out (which may be q and k).
     Returns (q_out, k_out), or q_out alone without k."""
-    B, T, _, D = _head_shape(q, "q")
-    dev = q.device
+    shape, dev = _head_shape(q, "q"), q.device
+    B, T, H, D = shape
     if k is not None:
-        kb, kt, _, kd = _head_shape(k, "k")
-        if (kb, kt, kd) != (B, T, D):
+        kshape = _head_shape(k, "k")
+        if (kshape[0], kshape[1], kshape[3]) != (B, T, D):
             raise ValueError(f"queries {tuple(q.shape)}, keys {tuple(k.shape)}")
 
     def call(s):
-        qo = _new_heads(q_out, q, y_dtype)
-        ko = _new_heads(k_out, k, y_dtype) if k is not None else None
-        if B * T == 0:
-            return qo if k is None else (qo, ko)
-        st = lib.hdq_qk_norm_rope(_heads(q, "q", dev), _heads(k, "k", dev) if k is not None else None, B, T, D,
-                                  _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias),
-                                  _rope_desc(rope, positions, B, T, dev), _heads(qo, "q_out", dev),
-                                  _heads(ko, "k_out", dev) if k is not None else None, s)
-        _check("hdq_qk_norm_rope", st)
+        qd = _heads(q, "q", H, D, dev)
+        qo, qod = _out_heads(q_out, q, shape, y_dtype, "q_out", dev)
+        ko = kd = kod = None
+        if k is not None:
+            kd = _heads(k, "k", kshape[2], D, dev)
+            ko, kod = _out_heads(k_out, k, kshape, y_dtype, "k_out", dev)
+        nd = _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias)
+        rd = _rope_desc(rope, positions, B, T, dev)
+        if B * T:
+            _check("hdq_qk_norm_rope", _qk_norm_rope(qd, kd, B, T, D, nd, rd, qod, kod, s))
         return qo if k is None else (qo, ko)
     return _launch(dev, stream, call)
 
@@ -1064,13 +1098,14 @@ class KvCache:
         self.v_scale = buffer(v_scale, "v_scale", torch.float32, sshape)
         self._desc = KvCacheDesc(fmt, group, had_block, heads, dim, slots, self.k_codes.data_ptr(), self.k_scale.data_ptr(),
                                  self.v_codes.data_ptr(), self.v_scale.data_ptr())
+        self._ref = _c.byref(self._desc)
 
     def desc(self):
-        return self._desc
+        return self._ref
 
 
 def _slots(slots, n, dev):
-    if slots.dtype != torch.int64 or slots.numel() != n or not slots.is_contiguous() or slots.device != dev:
+    if slots.dtype is not _I64 or slots.numel() != n or not slots.is_contiguous() or slots.device != dev:
         raise ValueError(f"slots: expected {n} contiguous int64 on {dev}, got {slots.dtype} {tuple(slots.shape)} on {slots.device}")
     return slots.data_ptr()
 
@@ -1082,26 +1117,28 @@ def qkv_to_cache(cache, q, k, v, slots, norm=HEAD_NORM_NONE, q_weight=None, k_we
     as they are.  Views as qk_norm_rope's.  Returns q_out (None without q)."""
     B, T, Hk, D = _head_shape(k, "k")
     dev = k.device
-    for t, name in ((v, "v"), (q, "q")):
-        if t is None:
-            if name == "v":
-                raise ValueError("v is missing")
-            continue
-        b, n, h, d = _head_shape(t, name)
-        if (b, n, d) != (B, T, D) or (name == "v" and h != Hk):
-            raise ValueError(f"{name} {tuple(t.shape)}, keys {tuple(k.shape)}")
-    if (Hk, D) != (cache.heads, cache.dim) or cache.device != dev:
+    if v is None:
+        raise ValueError("v is missing")
+    if v.shape != k.shape:
+        raise ValueError(f"values {tuple(v.shape)}, keys {tuple(k.shape)}")
+    if q is not None:
+        shape = _head_shape(q, "q")
+        if (shape[0], shape[1], shape[3]) != (B, T, D):
+            raise ValueError(f"queries {tuple(q.shape)}, keys {tuple(k.shape)}")
+    if Hk != cache.heads or D != cache.dim or cache.device != dev:
         raise ValueError(f"keys {tuple(k.shape)} on {dev}, a cache of {cache.heads} heads of {cache.dim} on {cache.device}")
 
     def call(s):
-        qo = _new_heads(q_out, q, y_dtype) if q is not None else None
-        if B * T == 0:
-            return qo
-        st = lib.hdq_qkv_to_cache(_heads(q, "q", dev) if q is not None else None, _heads(k, "k", dev), _heads(v, "v", dev),
-                                  B, T, _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias),
-                                  _rope_desc(rope, positions, B, T, dev), _heads(qo, "q_out", dev) if q is not None else None,
-                                  _slots(slots, B * T, dev), cache.desc(), s)
-        _check("hdq_qkv_to_cache", st)
+        qo = qd = qod = None
+        if q is not None:
+            qd = _heads(q, "q", shape[2], D, dev)
+            qo, qod = _out_heads(q_out, q, shape, y_dtype, "q_out", dev)
+        kd, vd = _heads(k, "k", Hk, D, dev), _heads(v, "v", Hk, D, dev)
+        nd = _head_norm(norm, eps, D, dev, q_weight, q_bias, k_weight, k_bias)
+        rd = _rope_desc(rope, positions, B, T, dev)
+        sp = _slots(slots, B * T, dev)
+        if B * T:
+            _check("hdq_qkv_to_cache", _qkv_to_cache(qd, kd, vd, B, T, nd, rd, qod, sp, cache.desc(), s))
         return qo
     return _launch(dev, stream, call)
 
@@ -1123,8 +1160,8 @@ def cache_read(cache, slots, k_out=None, v_out=None, y_dtype=DTYPE_BF16, stream=
             _operand(t, name, dt, shape, dev)
 
     def call(s):
-        ko = torch.empty(shape, dtype=dt, device=dev) if k_out is None else k_out
-        vo = torch.empty(shape, dtype=dt, device=dev) if v_out is None else v_out
+        ko = slots.new_empty(shape, dtype=dt) if k_out is None else k_out
+        vo = slots.new_empty(shape, dtype=dt) if v_out is None else v_out
         if n:
             _check("hdq_cache_read", lib.hdq_cache_read(cache.desc(), sp, n, ko.data_ptr(), vo.data_ptr(), y_dtype, s))
         return ko, vo

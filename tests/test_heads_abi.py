@@ -236,11 +236,20 @@ def test_binding_refusals(hdq):
         hdq.Rope(64, turns=torch.zeros(32))
     dev = torch.device("cpu")
     r3 = hdq.Rope((16, 24, 24), turns=torch.cat([hdq.rope_turns(d) for d in (16, 24, 24)]))
-    assert list(r3.desc(torch.zeros(3, 2, 5, dtype=torch.int64), 2, 5, dev).axis_dim) == [16, 24, 24]
-    d = r3.desc(torch.zeros(3, 5, dtype=torch.int64), 2, 5, dev)
+    desc = lambda rope, p: hdq.RopeDesc.from_buffer_copy(rope.desc(p, 2, 5, dev))
+    d = desc(r3, torch.zeros(3, 2, 5, dtype=torch.int64))
+    assert list(d.axis_dim) == [16, 24, 24] and (d.layout, d.dim, d.axes, d.scale) == (hdq.ROPE_INTERLEAVED, 64, 3, 1.0)
+    assert d.turns == r3.turns.data_ptr()
+    d = desc(r3, torch.zeros(3, 5, dtype=torch.int64))
     assert (d.pos_axis_stride, d.pos_batch_stride, d.pos_token_stride) == (5, 0, 1)
-    d = r.desc(torch.zeros(5, 2, dtype=torch.int64).t(), 2, 5, dev)
+    d = desc(r, torch.zeros(5, 2, dtype=torch.int64).t())
     assert (d.pos_batch_stride, d.pos_token_stride) == (1, 2)
+    for packed, cls in ((hdq._HEADS, hdq.HeadsDesc), (hdq._NORM, hdq.HeadNormDesc), (hdq._ROPE, hdq.RopeDesc)):
+        assert packed.size == ctypes.sizeof(cls)
+    h = hdq.HeadsDesc.from_buffer_copy(hdq._heads(x[:, 1:3], "x", 2, 64, dev))
+    assert (h.data, h.dtype, h.heads, h.batch_stride, h.token_stride, h.head_stride) == (x[:, 1:].data_ptr(), 1, 2, 0, 256, 64)
+    n = hdq.HeadNormDesc.from_buffer_copy(hdq._head_norm(2, 0.5, 64, dev, None, r.turns[:0].new_zeros(64).float(), None, None))
+    assert (n.kind, n.eps, n.q_weight, n.k_bias) == (2, 0.5, None, None) and n.q_bias
     for p in (pos.int(), torch.zeros(4, dtype=torch.int64), torch.zeros(2, 5, 1, dtype=torch.int64)):
         with pytest.raises(ValueError):
             r.desc(p, 2, 5, dev)
