@@ -44,8 +44,8 @@ struct HeadArgs {
   int64_t n_slots;
   uint8_t* codes[2];
   float* scales[2];
-  // the plan's
-  int lane_bits, slot_bits, steps, slices, step_end[3];
+  // the plan's: the first `qk_slices` layers of the grid take the queries' and keys' steps
+  int lane_bits, slot_bits, steps, qk_slices, step_end[3];
 };
 
 // Reading slots back: token t's keys and values go to row t of the outputs.
@@ -58,12 +58,18 @@ struct CacheReadArgs {
   int heads, dim, fmt, group, groups, hb;
   float c_b;
   bool y_f32;
-  int lane_bits, slot_bits, steps, slices, step_end[3];
+  int lane_bits, slot_bits, steps;  // the plan's: layers z and z + half of the grid take step z * steps of keys and values
 };
 
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s);
 hipError_t launch_cache_read(CacheReadArgs g, hipStream_t s);
 
+// Whether two chunks, half a head apart, can lie in a lane: Hadamard blocks and
+// groups within half a head, or the whole.
+inline bool cache_pairs(int dim, int hb, int group) {
+  const int half = dim / 2;
+  return dim % 16 == 0 && (hb == dim || half % hb == 0) && (group == dim || half % group == 0);
+}
 inline float cache_top(int fmt) { return fmt == kCacheInt8 ? 127.0f : fmt == kCacheFp8 ? kFp8Max : 7.0f; }
 
 // Sum over the 2^bits lanes (aligned) that hold a head; the same in each.

@@ -186,6 +186,33 @@ __device__ __forceinline__ float2 pair_angle(const HeadArgs& g, int64_t p0, int6
   return make_float2(co * g.scale, s * g.scale);
 }
 
+// A token's sequence and place in it; one past the last stands in the first.
+struct Token {
+  bool in;
+  uint32_t batch, pos;
+};
+__device__ __forceinline__ Token token_of(const HeadArgs& g, int64_t token) {
+  Token t;
+  t.in = token < g.tokens;
+  const uint32_t i = t.in ? (uint32_t)token : 0u;
+  t.batch = g.length == g.tokens ? 0u : i / (uint32_t)g.length;
+  t.pos = i - t.batch * (uint32_t)g.length;
+  return t;
+}
+
+// Its positions on the axes; live: it is rotated.
+struct Positions {
+  int64_t p0, p1, p2;
+  bool live;
+  __device__ __forceinline__ Positions(const HeadArgs& g, const Token& t) {
+    const int64_t* p = g.positions + t.batch * g.pos_batch + t.pos * g.pos_token;
+    p0 = p[0];
+    p1 = g.axes > 1 ? p[g.pos_axis] : 0;
+    p2 = g.axes > 2 ? p[2 * g.pos_axis] : 0;
+    live = (p0 | p1 | p2) >= 0;
+  }
+};
+
 // Weights and biases of a lane's chunk (null: 1 and 0), aligned to an element.
 __device__ __forceinline__ void load_weights(const float* p, int at, float other, float (&w)[8]) {
   if (p != nullptr) {
@@ -196,29 +223,35 @@ __device__ __forceinline__ void load_weights(const float* p, int at, float other
   }
 }
 
+// The wave's steps, of the layer of the grid it is in.
+struct Steps {
+  int first, end;
+};
+__device__ __forceinline__ Steps wave_steps(const HeadArgs& g) {
+  const int z = (int)blockIdx.z, qk = g.qk_slices;
+  const int first = z < qk ? z * g.steps : g.step_end[1] + (z - qk) * g.steps;
+  return Steps{first, min(first + g.steps, z < qk ? g.step_end[1] : g.step_end[2])};
+}
+
 template <bool F32, int MODE, bool CACHE>
 __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
   constexpr bool VEC = MODE != kElements;
   __shared__ __align__(16) float2 s_trig[kWaves][kMaxPairs];
   __shared__ __align__(16) float s_swap[kWaves][64 * 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // 32 bits hold the wave's number: one token a wave at most, and slices only with few tokens
-  const uint32_t work = wide_block() * kWaves + wave;
-  const uint32_t tgroup = work / (uint32_t)g.slices;
-  const int slice = (int)(work - tgroup * (uint32_t)g.slices);
   const int ll = g.lane_bits, sl = g.slot_bits;
   // lane l of a head holds chunk c (in an order that the Hadamard stages like)
   const int c = CACHE ? (int)fwht_src(lane & ((1 << ll) - 1), lane, g.hb) : lane & ((1 << ll) - 1);
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
-  const int64_t first = (int64_t)tgroup * (64 >> (ll + sl)), token = first + (lane >> (ll + sl));
-  if (first >= g.tokens) return;  // whole waves
-  const uint32_t tok = token < g.tokens ? (uint32_t)token : 0u, bi = tok / (uint32_t)g.length, ti = tok - bi * (uint32_t)g.length;
+  const int64_t group0 = ((int64_t)wide_block() * kWaves + wave) * (64 >> (ll + sl)), token = group0 + (lane >> (ll + sl));
+  if (group0 >= g.tokens) return;  // whole waves
+  const Token at = token_of(g, token);
   const int n = min(8, g.dim - c * 8);  // the lane's elements, <= 0 past the head
-  const bool in = token < g.tokens && n > 0;
+  const bool in = at.in && n > 0;
 
   // Steps: 2^sl heads of a tensor each, the queries' first.  A step's tensor is
   // the same for the whole wave.
-  const int step0 = slice * g.steps, step1 = min(step0 + g.steps, g.step_end[2]);
+  const Steps steps = wave_steps(g);
   auto tensor = [&](int s) { return s < g.step_end[0] ? 0 : !CACHE || s < g.step_end[1] ? 1 : 2; };
   auto block = [&](int t, int s) { return (s - (t == 0 ? 0 : t == 1 ? g.step_end[0] : g.step_end[1])) << sl; };
   auto rows = [&](int t) -> const HeadRows& { return t == 0 ? g.q : !CACHE || t == 1 ? g.k : g.v; };
@@ -228,36 +261,29 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
   int x_of = -1;  // whose lane base this is
   const char* x_base = nullptr;
   auto load = [&](Chunk<F32>& raw, int s) {
-    raw.zero();
-    if (s >= step1) return;
+    if (s >= steps.end) return;
     const int t = tensor(s), h0 = block(t, s);
     const HeadRows& r = rows(t);
     if (t != x_of) {
       x_of = t;
-      x_base = static_cast<const char*>(r.x) + (bi * r.xb + ti * r.xt + hslot * r.xh + c * 8) * kIn;
+      x_base = static_cast<const char*>(r.x) + (at.batch * r.xb + at.pos * r.xt + hslot * r.xh + c * 8) * kIn;
     }
     if (in && h0 + hslot < r.heads) raw.template load<VEC>(x_base + h0 * r.xh * kIn, n);
   };
 
-  Chunk<F32> raw[kUnroll];
+  Chunk<F32> raw[kUnroll];  // lanes past a head's end keep zeros
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) load(raw[u], step0 + u);
+  for (int u = 0; u < kUnroll; ++u) raw[u].zero(), load(raw[u], steps.first + u);
 
   // angles of the wave's tokens: pair j of a token by lane j, j + lanes, ... of it
   float cs[8], sn[8];
   bool live = false;
-  if (g.half > 0) {
-    const int64_t* pp = g.positions + bi * g.pos_batch + ti * g.pos_token;
-    int64_t pos[3];
-    live = true;
-#pragma unroll
-    for (int a = 0; a < 3; ++a) {
-      pos[a] = a < g.axes ? pp[a * g.pos_axis] : 0;
-      live = live && pos[a] >= 0;
-    }
+  if (g.half > 0 && steps.first < g.step_end[1]) {
+    const Positions pos(g, at);
+    live = pos.live;
     const int per = 1 << (ll + sl);
     float2* trig = s_trig[wave] + (lane >> (ll + sl)) * g.half;
-    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos[0], pos[1], pos[2], j);
+    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos.p0, pos.p1, pos.p2, j);
     wave_lds_fence();
     if (g.split) {  // element i of pair i or i - half, the sine negative for the first
 #pragma unroll
@@ -282,7 +308,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
   float wt[8], bs[8];
   int w_of = -1, y_of = -1;  // whose weights, whose lane base
   char* y_base = nullptr;
-  const int64_t slot = CACHE && in ? g.slots[tok] : -1;
+  const int64_t slot = CACHE && in ? g.slots[token] : -1;
   const bool in_cache = slot >= 0 && slot < g.n_slots;
 
   auto process = [&](const Chunk<F32>& raw, int s) {
@@ -365,21 +391,19 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
     } else {
       if (y_of != t) {
         y_of = t;
-        y_base = static_cast<char*>(r.y) + (bi * r.yb + ti * r.yt + hslot * r.yh + c * 8) * out_size;
+        y_base = static_cast<char*>(r.y) + (at.batch * r.yb + at.pos * r.yt + hslot * r.yh + c * 8) * out_size;
       }
       if (ok) store_chunk<VEC>(y_base + (h - hslot) * r.yh * out_size, g.y_f32, x, n);
     }
   };
 
-  for (int s = step0; s < step1; s += kUnroll) {
-    Chunk<F32> now[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) load(raw[u], s + kUnroll + u);
+  for (int s = steps.first; s < steps.end; s += kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (s + u < step1) process(now[u], s + u);
+      if (s + u < steps.end) {
+        process(raw[u], s + u);
+        load(raw[u], s + kUnroll + u);
+      }
   }
 }
 
@@ -394,20 +418,17 @@ template <bool F32, int LL, bool CACHE>
 __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   __shared__ __align__(16) float2 s_trig[kWaves][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t work = wide_block() * kWaves + wave;
-  const uint32_t tgroup = work / (uint32_t)g.slices;
-  const int slice = (int)(work - tgroup * (uint32_t)g.slices);
   const int ll = LL < 0 ? g.lane_bits : LL, sl = g.slot_bits;
   const int far = g.dim >> 4;  // chunks from a lane's first to its second
   const int hb1 = CACHE ? min(g.hb, g.dim >> 1) : 1;
   const int c = CACHE ? (int)fwht_src(lane & ((1 << ll) - 1), lane, hb1) : lane & ((1 << ll) - 1);
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
-  const int64_t first = (int64_t)tgroup * (64 >> (ll + sl)), token = first + (lane >> (ll + sl));
-  if (first >= g.tokens) return;  // whole waves
-  const uint32_t tok = token < g.tokens ? (uint32_t)token : 0u, bi = tok / (uint32_t)g.length, ti = tok - bi * (uint32_t)g.length;
-  const bool in = token < g.tokens && c < far;
+  const int64_t group0 = ((int64_t)wide_block() * kWaves + wave) * (64 >> (ll + sl)), token = group0 + (lane >> (ll + sl));
+  if (group0 >= g.tokens) return;  // whole waves
+  const Token at = token_of(g, token);
+  const bool in = at.in && c < far;
 
-  const int step0 = slice * g.steps, step1 = min(step0 + g.steps, g.step_end[2]);
+  const Steps steps = wave_steps(g);
   auto tensor = [&](int s) { return s < g.step_end[0] ? 0 : !CACHE || s < g.step_end[1] ? 1 : 2; };
   auto block = [&](int t, int s) { return (s - (t == 0 ? 0 : t == 1 ? g.step_end[0] : g.step_end[1])) << sl; };
   auto rows = [&](int t) -> const HeadRows& { return t == 0 ? g.q : !CACHE || t == 1 ? g.k : g.v; };
@@ -420,14 +441,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   int x_of = -1;  // whose lane base this is
   const char* x_base = nullptr;
   auto load = [&](Pair& raw, int s) {
-    raw.a.zero();
-    raw.b.zero();
-    if (s >= step1) return;
+    if (s >= steps.end) return;
     const int t = tensor(s), h0 = block(t, s);
     const HeadRows& r = rows(t);
     if (t != x_of) {
       x_of = t;
-      x_base = static_cast<const char*>(r.x) + (bi * r.xb + ti * r.xt + hslot * r.xh + c * 8) * kIn;
+      x_base = static_cast<const char*>(r.x) + (at.batch * r.xb + at.pos * r.xt + hslot * r.xh + c * 8) * kIn;
     }
     if (in && h0 + hslot < r.heads) {
       const char* p = x_base + h0 * r.xh * kIn;
@@ -436,42 +455,35 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
     }
   };
 
-  Pair raw[kUnroll];
+  Pair raw[kUnroll];  // lanes past a head's end keep zeros
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) load(raw[u], step0 + u);
+  for (int u = 0; u < kUnroll; ++u) raw[u].a.zero(), raw[u].b.zero(), load(raw[u], steps.first + u);
 
   // angles of the wave's tokens, as above; cs, sn: of the lane's eight pairs
+  // (what lies past the rotated ones is not used)
   float cs[8], sn[8];
   bool live = false, live2 = false;
-  if (g.half > 0) {
-    const int64_t* pp = g.positions + bi * g.pos_batch + ti * g.pos_token;
-    int64_t pos[3];
-    live = true;
-#pragma unroll
-    for (int a = 0; a < 3; ++a) {
-      pos[a] = a < g.axes ? pp[a * g.pos_axis] : 0;
-      live = live && pos[a] >= 0;
-    }
+  if (g.half > 0 && steps.first < g.step_end[1]) {
+    const Positions pos(g, at);
     const int per = 1 << (ll + sl);
-    float2* trig = s_trig[wave] + (lane >> (ll + sl)) * g.half;
-    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos[0], pos[1], pos[2], j);
+    float2* trig = s_trig[wave] + (lane >> (ll + sl)) * (8 << ll);
+    for (int j = lane & (per - 1); j < g.half; j += per) trig[j] = pair_angle(g, pos.p0, pos.p1, pos.p2, j);
     wave_lds_fence();
     const int j0 = g.split ? c * 8 : c * 4, j1 = g.split ? c * 8 + 4 : (c + far) * 4;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 v = j0 + e < g.half ? trig[j0 + e] : make_float2(1.0f, 0.0f);
-      const float2 w = j1 + e < g.half ? trig[j1 + e] : make_float2(1.0f, 0.0f);
+      const float2 v = trig[j0 + e], w = trig[j1 + e];
       cs[e] = v.x, sn[e] = v.y;
       cs[4 + e] = w.x, sn[4 + e] = w.y;
     }
-    live2 = live && (c + far) * 8 < 2 * g.half;  // interleaved: each chunk is turned or not
-    live = live && c * 8 < 2 * g.half;
+    live2 = pos.live && (c + far) * 8 < 2 * g.half;  // interleaved: each chunk is turned or not
+    live = pos.live && c * 8 < 2 * g.half;
   }
 
   float wt[2][8], bs[2][8];
   int w_of = -1, y_of = -1;  // whose weights, whose lane base
   char* y_base = nullptr;
-  const int64_t slot = CACHE && in ? g.slots[tok] : -1;
+  const int64_t slot = CACHE && in ? g.slots[token] : -1;
   const bool in_cache = slot >= 0 && slot < g.n_slots;
   // the groups of the lane's chunks, and whether the lane is their first
   const bool whole = g.group == g.dim;
@@ -603,7 +615,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
     } else {
       if (y_of != t) {
         y_of = t;
-        y_base = static_cast<char*>(r.y) + (bi * r.yb + ti * r.yt + hslot * r.yh + c * 8) * out_size;
+        y_base = static_cast<char*>(r.y) + (at.batch * r.yb + at.pos * r.yt + hslot * r.yh + c * 8) * out_size;
       }
       if (ok) {
         char* p = y_base + (h - hslot) * r.yh * out_size;
@@ -613,15 +625,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
     }
   };
 
-  for (int s = step0; s < step1; s += kUnroll) {
-    Pair now[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) load(raw[u], s + kUnroll + u);
+  for (int s = steps.first; s < steps.end; s += kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (s + u < step1) process(now[u], s + u);
+      if (s + u < steps.end) {
+        process(raw[u], s + u);
+        load(raw[u], s + kUnroll + u);
+      }
   }
 }
 
@@ -648,10 +658,8 @@ void run(const HeadArgs& g, int mode, dim3 grid, hipStream_t s) {
 int mode_of(const HeadArgs& g, bool vec, bool cache) {
   if (!vec) return kElements;
   const bool chunks = g.half % (g.split ? 8 : 4) == 0;
-  const int whole = g.dim, part = g.dim / 2;
-  const auto within = [&](int v) { return v == whole || part % v == 0; };
-  if (g.dim % 16 == 0 && chunks && (!g.split || g.half == 0 || g.half == part) && (!cache || (within(g.hb) && within(g.group))))
-    return kPairs;
+  const bool pairs = cache ? cache_pairs(g.dim, g.hb, g.group) : g.dim % 16 == 0;
+  if (pairs && chunks && (!g.split || g.half == 0 || 2 * g.half == g.dim)) return kPairs;
   return chunks ? kChunks : kVectors;
 }
 
@@ -659,15 +667,16 @@ int mode_of(const HeadArgs& g, bool vec, bool cache) {
 
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s) {
   const int mode = mode_of(g, vec, cache);
-  const HeadPlan p = plan_heads(g.tokens, g.q.heads, g.k.heads, g.v.heads, g.dim, mode == kPairs ? 16 : 8);
+  const HeadPlan p = plan_heads(g.tokens, g.q.heads, g.k.heads, g.v.heads, g.dim, mode == kPairs ? 16 : 8, kHeadWaves);
   g.lane_bits = p.lane_bits;
   g.slot_bits = p.slot_bits;
   g.steps = p.steps;
-  g.slices = p.slices;
+  g.qk_slices = p.slices[0];
   for (int i = 0; i < 3; ++i) g.step_end[i] = p.step_end[i];
   g.inv_dim = 1.0f / (float)g.dim;
-  const dim3 grid = wide_grid((p.waves + kWaves - 1) / kWaves);
   if (cache) g.group_bits = group_lane_bits(g.dim, g.group, p.lane_bits);
+  dim3 grid = wide_grid((p.groups + kWaves - 1) / kWaves);
+  grid.z = (unsigned)(p.slices[0] + p.slices[1]);
   if (cache)
     f32 ? run<true, true>(g, mode, grid, s) : run<false, true>(g, mode, grid, s);
   else

@@ -9,107 +9,169 @@ namespace hdq {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kUnroll = 4;  // head steps whose loads are in flight together
+constexpr int kUnroll = 2;  // head steps whose loads are in flight together
 
-struct Coded {
+// A chunk of eight codes as loaded.
+template <int FMT>
+struct Codes {
   uint2 w;
-  float scale;
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if (FMT == kCacheInt4)
+      w.x = *reinterpret_cast<const uint32_t*>(p);
+    else
+      w = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void to_f32(float scale, float (&x)[8]) const {
+    if (FMT == kCacheFp8) {
+      e4m3x4_to_f32(w.x, x);
+      e4m3x4_to_f32(w.y, x + 4);
+    } else if (FMT == kCacheInt8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)((int)(w.x << (28 - 4 * e)) >> 28);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * scale;
+  }
 };
 
-__device__ __forceinline__ void decode8(const Coded& v, int fmt, float (&x)[8]) {
-  if (fmt == kCacheFp8) {
-    e4m3x4_to_f32(v.w.x, x);
-    e4m3x4_to_f32(v.w.y, x + 4);
-  } else if (fmt == kCacheInt8) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? v.w.x : v.w.y) >> (8 * (e & 3)));
+__device__ __forceinline__ void store8(void* y, bool f32, int64_t at, const float (&x)[8]) {
+  if (f32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)((int)(v.w.x << (28 - 4 * e)) >> 28);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = x[e] * v.scale;
 }
 
+// A layer of the grid takes `steps` steps of the keys' heads, or of the
+// values'.  A lane holds one chunk of a head, or (PAIRS) chunks c and
+// c + dim / 16, as the kernels that write the cache; LL: log2 of a head's
+// lanes, or -1 for g.lane_bits.
+template <int FMT, int LL, bool PAIRS>
 __global__ __launch_bounds__(64 * kWaves) void k_cache_read(const CacheReadArgs g) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t work = wide_block() * kWaves + wave;
-  const uint32_t tgroup = work / (uint32_t)g.slices;
-  const int slice = (int)(work - tgroup * (uint32_t)g.slices);
-  const int ll = g.lane_bits, sl = g.slot_bits;
-  const int c = (int)fwht_src(lane & ((1 << ll) - 1), lane, g.hb);
+  const int ll = LL < 0 ? g.lane_bits : LL, sl = g.slot_bits;
+  const int far = PAIRS ? g.dim >> 4 : 0, hb1 = PAIRS ? min(g.hb, g.dim >> 1) : g.hb;
+  const int c = (int)fwht_src(lane & ((1 << ll) - 1), lane, hb1);
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
-  const int64_t first = (int64_t)tgroup * (64 >> (ll + sl)), token = first + (lane >> (ll + sl));
-  if (first >= g.tokens) return;  // whole waves
-  const bool in = token < g.tokens && c * 8 < g.dim;
+  const int64_t group0 = ((int64_t)wide_block() * kWaves + wave) * (64 >> (ll + sl)), token = group0 + (lane >> (ll + sl));
+  if (group0 >= g.tokens) return;  // whole waves
+  const bool in = token < g.tokens && (PAIRS ? c < far : c * 8 < g.dim);
   const int64_t slot = in ? g.slots[token] : -1;
   const bool cached = slot >= 0 && slot < g.n_slots;
-  // the lane's element of head hslot, and its scale, in the cache and in the output
-  const int64_t row = (cached ? slot : 0) * g.heads + hslot;
-  const int64_t from = row * g.dim + c * 8, scale_from = row * g.groups + c * 8 / g.group;
-  const int64_t to = (token * g.heads + hslot) * g.dim + c * 8;
-  const int step0 = slice * g.steps, step1 = min(step0 + g.steps, g.step_end[2]);
+  const int layers = (int)gridDim.z >> 1, z = (int)blockIdx.z, t = z >= layers;
+  const int heads = ((g.heads - 1) >> sl) + 1;  // steps of a tensor
+  const int step0 = (t ? z - layers : z) * g.steps, step1 = min(step0 + g.steps, heads);
 
-  auto load = [&](Coded& v, int s) {
-    v = Coded{make_uint2(0u, 0u), 0.0f};  // slots that are not there read zeros
+  // the lane's element of head hslot, and its scales, in the cache and in the output
+  constexpr int kBits = FMT == kCacheInt4 ? 4 : 8;
+  const int64_t row = (cached ? slot : 0) * g.heads + hslot;
+  const uint8_t* from = g.codes[t] + (row * g.dim + c * 8) * kBits / 8;
+  const float* scale_from = g.scales[t] + row * g.groups;
+  const int group1 = c * 8 / g.group, group2 = (c + far) * 8 / g.group;
+  const int64_t to = (token * g.heads + hslot) * g.dim + c * 8;
+  void* y = g.y[t];
+
+  struct Head {
+    Codes<FMT> a, b;
+    float scale, scale2;
+  };
+  auto load = [&](Head& v, int s) {
     if (s >= step1) return;
-    const int t = s < g.step_end[0] ? 0 : 1, h0 = (s - (t ? g.step_end[0] : 0)) << sl;
+    const int h0 = s << sl;
     if (cached && h0 + hslot < g.heads) {
-      const int64_t at = from + (int64_t)h0 * g.dim;
-      if (g.fmt == kCacheInt4)
-        v.w.x = *reinterpret_cast<const uint32_t*>(g.codes[t] + at / 2);
-      else
-        v.w = *reinterpret_cast<const uint2*>(g.codes[t] + at);
-      v.scale = g.scales[t][scale_from + (int64_t)h0 * g.groups];
+      const int64_t at = (int64_t)h0 * g.dim * kBits / 8;
+      v.a.load(from + at);
+      if (PAIRS) v.b.load(from + at + far * kBits);
+      const float* p = scale_from + (int64_t)h0 * g.groups;
+      v.scale = p[group1];
+      if (PAIRS) v.scale2 = p[group2];
     }
   };
-  auto process = [&](const Coded& v, int s) {
-    const int t = s < g.step_end[0] ? 0 : 1, h0 = (s - (t ? g.step_end[0] : 0)) << sl;
-    float x[8];
-    decode8(v, g.fmt, x);
-    const float sc = fwht8(x, lane, g.hb) * g.c_b;
+  auto process = [&](const Head& v, int s) {
+    float x[8], w[8];
+    v.a.to_f32(v.scale, x);
+    if (PAIRS) v.b.to_f32(v.scale2, w);
     if (g.hb > 1) {
+      const float sc = fwht8(x, lane, hb1) * g.c_b;
+      if (PAIRS) {
+        fwht8(w, lane, hb1);
+        if (g.hb != hb1) {  // the last stage, half a head apart
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = w[e];
+            x[e] = a + b;
+            w[e] = a - b;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = w[e] * sc;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = x[e] * sc;
     }
+    const int h0 = s << sl;
     if (in && h0 + hslot < g.heads) {
       const int64_t at = to + (int64_t)h0 * g.dim;
-      if (g.y_f32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(g.y[t]) + at);
-        d[0] = make_float4(x[0], x[1], x[2], x[3]);
-        d[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.y[t]) + at) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-      }
+      store8(y, g.y_f32, at, x);
+      if (PAIRS) store8(y, g.y_f32, at + far * 8, w);
     }
   };
 
-  Coded raw[kUnroll];
+  Head raw[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) load(raw[u], step0 + u);
+  for (int u = 0; u < kUnroll; ++u) {
+    raw[u].a.w = raw[u].b.w = make_uint2(0u, 0u);  // slots that are not there read zeros
+    raw[u].scale = raw[u].scale2 = 0.0f;
+    load(raw[u], step0 + u);
+  }
   for (int s = step0; s < step1; s += kUnroll) {
-    Coded now[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) load(raw[u], s + kUnroll + u);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (s + u < step1) process(now[u], s + u);
+      if (s + u < step1) {
+        process(raw[u], s + u);
+        load(raw[u], s + kUnroll + u);
+      }
   }
+}
+
+template <int FMT>
+void run(const CacheReadArgs& g, bool pairs, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kWaves);
+  if (!pairs)
+    k_cache_read<FMT, -1, false><<<grid, block, 0, s>>>(g);
+  else if (g.dim == 64)
+    k_cache_read<FMT, 2, true><<<grid, block, 0, s>>>(g);
+  else if (g.dim == 128)
+    k_cache_read<FMT, 3, true><<<grid, block, 0, s>>>(g);
+  else
+    k_cache_read<FMT, -1, true><<<grid, block, 0, s>>>(g);
 }
 
 }  // namespace
 
 hipError_t launch_cache_read(CacheReadArgs g, hipStream_t s) {
-  const HeadPlan p = plan_heads(g.tokens, g.heads, g.heads, 0, g.dim);
+  const bool pairs = cache_pairs(g.dim, g.hb, g.group);
+  // keys and values by waves of their own: the plan of one of them
+  const HeadPlan p = plan_heads(2 * g.tokens, g.heads, 0, 0, g.dim, pairs ? 16 : 8, kReadWaves);
   g.lane_bits = p.lane_bits;
   g.slot_bits = p.slot_bits;
   g.steps = p.steps;
-  g.slices = p.slices;
-  for (int i = 0; i < 3; ++i) g.step_end[i] = p.step_end[i];
-  k_cache_read<<<wide_grid((p.waves + kWaves - 1) / kWaves), dim3(64 * kWaves), 0, s>>>(g);
+  const int64_t per_wave = int64_t(1) << (6 - p.lane_bits - p.slot_bits);
+  const int64_t groups = (g.tokens + per_wave - 1) / per_wave;
+  dim3 grid = wide_grid((groups + kWaves - 1) / kWaves);
+  grid.z = (unsigned)(2 * p.slices[0]);
+  if (g.fmt == kCacheFp8)
+    run<kCacheFp8>(g, pairs, grid, s);
+  else if (g.fmt == kCacheInt8)
+    run<kCacheInt8>(g, pairs, grid, s);
+  else
+    run<kCacheInt4>(g, pairs, grid, s);
   return hipGetLastError();
 }
 
