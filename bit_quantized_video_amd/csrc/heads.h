@@ -61,6 +61,10 @@ struct CacheReadArgs {
   int lane_bits, slot_bits, steps;  // the plan's: layers z and z + half of the grid take step z * steps of keys and values
 };
 
+// heads16*.hip, for launch_heads
+void run_heads16(const HeadArgs& g, dim3 grid, hipStream_t s);
+void run_heads16_cache(const HeadArgs& g, dim3 grid, hipStream_t s);
+void run_heads16_f32(const HeadArgs& g, bool cache, dim3 grid, hipStream_t s);
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s);
 hipError_t launch_cache_read(CacheReadArgs g, hipStream_t s);
 
@@ -104,28 +108,53 @@ __device__ __forceinline__ void code_scales(float a, float top, float& scale, fl
   inv = live ? top / a : 0.0f;
 }
 
-// Codes the lane's chunk at element `at` (a multiple of 8) of a cache's codes,
-// rounded to even; inv 0 gives zeros whatever y holds.  Integers: adding
-// 1.5 2^23 leaves the rounded value in the sum's low bits, two's complement;
-// |y * inv| passes top by less than half.
-__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t at, const float (&y)[8], float inv, int fmt) {
-  if (fmt == kCacheFp8) {
-    *reinterpret_cast<uint2*>(codes + at) = fp8_encode8(y, inv);
-    return;
-  }
-  uint32_t q[8];
+// Integer codes of eight values, rounded to even, in the low bytes of words:
+// adding 1.5 2^23 leaves the rounded value in the sum's low bits, two's
+// complement; |y * inv| passes top by less than half.
+__device__ __forceinline__ void int_codes(const float (&y)[8], float inv, uint32_t (&q)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(y[e] * inv + 12582912.0f);
-  // bytes of four elements: v_perm takes byte 0 of each
-  const auto bytes = [&](int a, int b, int c, int d) {
-    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[d], q[c], 0x0c0c0400u), __builtin_amdgcn_perm(q[b], q[a], 0x0c0c0400u), 0x05040100u);
-  };
-  if (fmt == kCacheInt8) {
-    const uint32_t lo = bytes(0, 1, 2, 3), hi = bytes(4, 5, 6, 7);
-    *reinterpret_cast<uint2*>(codes + at) = inv != 0.0f ? make_uint2(lo, hi) : make_uint2(0u, 0u);
+}
+// Byte 0 of each of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
+}
+__device__ __forceinline__ uint2 int8_word(const float (&y)[8], float inv) {
+  uint32_t q[8];
+  int_codes(y, inv, q);
+  const uint2 w = make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+  return inv != 0.0f ? w : make_uint2(0u, 0u);
+}
+__device__ __forceinline__ uint32_t int4_word(const float (&y)[8], float inv) {
+  uint32_t q[8];
+  int_codes(y, inv, q);
+  const uint32_t w = (low_bytes(q[0], q[2], q[4], q[6]) & 0x0f0f0f0fu) | (low_bytes(q[1], q[3], q[5], q[7]) & 0x0f0f0f0fu) << 4;
+  return inv != 0.0f ? w : 0u;
+}
+
+// Codes the lane's chunk at element `at` (a multiple of 8) of a cache's codes;
+// inv 0 gives zeros whatever y holds.
+__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t at, const float (&y)[8], float inv, int fmt) {
+  if (fmt == kCacheFp8)
+    *reinterpret_cast<uint2*>(codes + at) = fp8_encode8(y, inv);
+  else if (fmt == kCacheInt8)
+    *reinterpret_cast<uint2*>(codes + at) = int8_word(y, inv);
+  else
+    *reinterpret_cast<uint32_t*>(codes + at / 2) = int4_word(y, inv);
+}
+
+// The same for chunks x at `at` and y at `at` + far.
+__device__ __forceinline__ void store_codes2(uint8_t* codes, int64_t at, int far, const float (&x)[8], const float (&y)[8],
+                                             float inv, float inv2, int fmt) {
+  if (fmt == kCacheFp8) {
+    *reinterpret_cast<uint2*>(codes + at) = fp8_encode8(x, inv);
+    *reinterpret_cast<uint2*>(codes + at + far) = fp8_encode8(y, inv2);
+  } else if (fmt == kCacheInt8) {
+    *reinterpret_cast<uint2*>(codes + at) = int8_word(x, inv);
+    *reinterpret_cast<uint2*>(codes + at + far) = int8_word(y, inv2);
   } else {
-    const uint32_t w = (bytes(0, 2, 4, 6) & 0x0f0f0f0fu) | (bytes(1, 3, 5, 7) & 0x0f0f0f0fu) << 4;
-    *reinterpret_cast<uint32_t*>(codes + at / 2) = inv != 0.0f ? w : 0u;
+    *reinterpret_cast<uint32_t*>(codes + at / 2) = int4_word(x, inv);
+    *reinterpret_cast<uint32_t*>(codes + at / 2 + far / 2) = int4_word(y, inv2);
   }
 }
 
