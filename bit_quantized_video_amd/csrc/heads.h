@@ -64,6 +64,8 @@ struct CacheReadArgs {
 // heads16*.hip, for launch_heads
 void run_heads16(const HeadArgs& g, dim3 grid, hipStream_t s);
 void run_heads16_cache(const HeadArgs& g, dim3 grid, hipStream_t s);
+void run_heads16_cache64(const HeadArgs& g, dim3 grid, hipStream_t s);
+void run_heads16_cache128(const HeadArgs& g, dim3 grid, hipStream_t s);
 void run_heads16_f32(const HeadArgs& g, bool cache, dim3 grid, hipStream_t s);
 hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t s);
 hipError_t launch_cache_read(CacheReadArgs g, hipStream_t s);
@@ -106,6 +108,16 @@ __device__ __forceinline__ void code_scales(float a, float top, float& scale, fl
   const bool live = finite && a >= kTiny;
   scale = live ? a / top : (finite ? 0.0f : __builtin_nanf(""));
   inv = live ? top / a : 0.0f;
+}
+
+// Stores 16 bytes.
+template <typename V>
+__device__ __forceinline__ void put16(void* p, const V& v) {
+#ifdef NTS
+  __builtin_nontemporal_store(__builtin_bit_cast(v4i, v), static_cast<v4i*>(p));
+#else
+  *static_cast<V*>(p) = v;
+#endif
 }
 
 // Integer codes of eight values, rounded to even, in the low bytes of words:

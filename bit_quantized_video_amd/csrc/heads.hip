@@ -231,7 +231,11 @@ hipError_t launch_heads(HeadArgs g, bool f32, bool vec, bool cache, hipStream_t 
   dim3 grid = wide_grid((p.groups + kWaves - 1) / kWaves);
   grid.z = (unsigned)(p.slices[0] + p.slices[1]);
   if (mode == kPairs)
-    f32 ? run_heads16_f32(g, cache, grid, s) : cache ? run_heads16_cache(g, grid, s) : run_heads16(g, grid, s);
+    f32 ? run_heads16_f32(g, cache, grid, s)
+    : !cache ? run_heads16(g, grid, s)
+    : g.dim == 64 ? run_heads16_cache64(g, grid, s)
+    : g.dim == 128 ? run_heads16_cache128(g, grid, s)
+                   : run_heads16_cache(g, grid, s);
   else if (cache)
     f32 ? run<true, true>(g, mode, grid, s) : run<false, true>(g, mode, grid, s);
   else

@@ -17,17 +17,20 @@
 namespace hdq {
 
 enum Rotation : int { kRotateNone = 0, kRotateSplit = 1, kRotatePairs = 2 };
+// The cache's Hadamard blocks: none, whole heads of 8 << (LL + 1) elements, or g.hb.
+enum Hadamard : int { kHadamardNone = 0, kHadamardWhole = 1, kHadamardAny = 2 };
 
 namespace {
 
 // LL: log2 of a head's lanes, or -1 for g.lane_bits.
-template <bool F32, int LL, bool CACHE, bool NORM, int ROTATE>
+template <bool F32, int LL, bool CACHE, bool NORM, int ROTATE, int HADAMARD>
 __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   __shared__ __align__(16) float2 s_trig[kWaves][ROTATE != kRotateNone ? 2 * kMaxPairs : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ll = LL < 0 ? g.lane_bits : LL, sl = g.slot_bits;
   const int far = g.dim >> 4;  // chunks from a lane's first to its second
-  const int hb1 = CACHE ? min(g.hb, g.dim >> 1) : 1;
+  const int hb = HADAMARD == kHadamardNone ? 1 : HADAMARD == kHadamardWhole ? 16 << LL : g.hb;
+  const int hb1 = HADAMARD == kHadamardWhole ? hb / 2 : HADAMARD == kHadamardNone ? 1 : min(hb, g.dim >> 1);
   const int c = CACHE ? (int)fwht_src(lane & ((1 << ll) - 1), lane, hb1) : lane & ((1 << ll) - 1);
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
   const int64_t group0 = ((int64_t)wide_block() * kWaves + wave) * (64 >> (ll + sl)), token = group0 + (lane >> (ll + sl));
@@ -180,10 +183,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
         for (int e = 0; e < 8; ++e) x[e] = a[e], y[e] = b[e];
       }
       if (CACHE && (VALUES || t != 0)) {
-        if (g.hb > 1) {
+        if (hb > 1) {
           const float sc = fwht8(x, lane, hb1) * g.c_b;
           fwht8(y, lane, hb1);
-          if (g.hb != hb1) {  // the last stage, half a head apart
+          if (hb != hb1) {  // the last stage, half a head apart
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float a = x[e], b = y[e];
@@ -246,24 +249,38 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
     walk(std::false_type());
 }
 
-template <bool F32, int LL, bool CACHE, bool NORM>
+template <bool F32, int LL, bool CACHE, bool NORM, int HADAMARD>
 void run16_rotate(const HeadArgs& g, int rotate, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kWaves);
   if (rotate == kRotateNone)
-    k_heads16<F32, LL, CACHE, NORM, kRotateNone><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotateNone, HADAMARD><<<grid, block, 0, s>>>(g);
   else if (rotate == kRotateSplit)
-    k_heads16<F32, LL, CACHE, NORM, kRotateSplit><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotateSplit, HADAMARD><<<grid, block, 0, s>>>(g);
   else
-    k_heads16<F32, LL, CACHE, NORM, kRotatePairs><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotatePairs, HADAMARD><<<grid, block, 0, s>>>(g);
+}
+
+template <bool F32, int LL, bool CACHE, int HADAMARD>
+void run16_norm(const HeadArgs& g, dim3 grid, hipStream_t s) {
+  const int rotate = g.half == 0 ? kRotateNone : g.split ? kRotateSplit : kRotatePairs;
+  if (g.norm != kHeadNormNone)
+    run16_rotate<F32, LL, CACHE, true, HADAMARD>(g, rotate, grid, s);
+  else
+    run16_rotate<F32, LL, CACHE, false, HADAMARD>(g, rotate, grid, s);
 }
 
 template <bool F32, int LL, bool CACHE>
 void run16(const HeadArgs& g, dim3 grid, hipStream_t s) {
-  const int rotate = g.half == 0 ? kRotateNone : g.split ? kRotateSplit : kRotatePairs;
-  if (g.norm != kHeadNormNone)
-    run16_rotate<F32, LL, CACHE, true>(g, rotate, grid, s);
+  if constexpr (!CACHE)
+    run16_norm<F32, LL, CACHE, kHadamardNone>(g, grid, s);
+  else if constexpr (LL < 0)
+    run16_norm<F32, LL, CACHE, kHadamardAny>(g, grid, s);
+  else if (g.hb == 1)
+    run16_norm<F32, LL, CACHE, kHadamardNone>(g, grid, s);
+  else if (g.hb == g.dim)
+    run16_norm<F32, LL, CACHE, kHadamardWhole>(g, grid, s);
   else
-    run16_rotate<F32, LL, CACHE, false>(g, rotate, grid, s);
+    run16_norm<F32, LL, CACHE, kHadamardAny>(g, grid, s);
 }
 
 }  // namespace

@@ -62,8 +62,8 @@ __device__ __forceinline__ void store_chunk(void* p, bool f32, const float (&y)[
   if (f32) {
     float* d = static_cast<float*>(p);
     if constexpr (VEC) {
-      reinterpret_cast<float4*>(d)[0] = make_float4(y[0], y[1], y[2], y[3]);
-      reinterpret_cast<float4*>(d)[1] = make_float4(y[4], y[5], y[6], y[7]);
+      put16(d, make_float4(y[0], y[1], y[2], y[3]));
+      put16(d + 4, make_float4(y[4], y[5], y[6], y[7]));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -72,7 +72,7 @@ __device__ __forceinline__ void store_chunk(void* p, bool f32, const float (&y)[
   } else {
     const uint4 w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
     if constexpr (VEC) {
-      *static_cast<uint4*>(p) = w;
+      put16(p, w);
     } else {
       const uint32_t v[4] = {w.x, w.y, w.z, w.w};
       uint16_t* d = static_cast<uint16_t*>(p);

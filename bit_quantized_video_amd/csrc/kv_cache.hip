@@ -39,12 +39,12 @@ struct Codes {
 
 __device__ __forceinline__ void store8(void* y, bool f32, int64_t at, const float (&x)[8]) {
   if (f32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+    float* d = static_cast<float*>(y) + at;
+    put16(d, make_float4(x[0], x[1], x[2], x[3]));
+    put16(d + 4, make_float4(x[4], x[5], x[6], x[7]));
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    put16(static_cast<uint16_t*>(y) + at,
+          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
   }
 }
 
