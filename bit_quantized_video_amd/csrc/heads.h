@@ -113,11 +113,7 @@ __device__ __forceinline__ void code_scales(float a, float top, float& scale, fl
 // Stores 16 bytes.
 template <typename V>
 __device__ __forceinline__ void put16(void* p, const V& v) {
-#ifdef NTS
-  __builtin_nontemporal_store(__builtin_bit_cast(v4i, v), static_cast<v4i*>(p));
-#else
   *static_cast<V*>(p) = v;
-#endif
 }
 
 // Integer codes of eight values, rounded to even, in the low bytes of words:

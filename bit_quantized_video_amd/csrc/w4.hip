@@ -36,9 +36,11 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
 // Codes to bf16 16 + u: eight columns of a word, which is kept rotated left by 3
-// bits, so that the first pair lies in place.
+// bits, so that the first pair lies in place.  The constants are kept in vector
+// registers: as literals they make two operations of each and-or.
 __device__ __forceinline__ v8bf decode(uint32_t w) {
-  const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+  uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+  asm("" : "+v"(mask), "+v"(sixteen));
   v4u r;
   r.x = (w & mask) | sixteen;
   r.y = ((w >> 4) & mask) | sixteen;
@@ -224,7 +226,12 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
   const int col = lane & 15, quad = lane >> 4, wm = wave % MW;
   const int64_t tn0 = (int64_t)blockIdx.x * 8 + wave / MW * NT, m0 = (int64_t)blockIdx.y * (16 * TILES);
   const int each = (int)((g.tiles_k + g.split - 1) / g.split);
-  const int k0 = (int)blockIdx.z * each, k1 = min(k0 + each, (int)g.tiles_k);
+  const int k0 = (int)blockIdx.z * each, n = min(each, (int)g.tiles_k - k0);
+  // The tiles of K go round from one that neighbours on the XCD do not start
+  // with: rows of tokens a multiple of 4 KB apart, and tiles of weights, put
+  // all that one tile reads on one or a few of L2's 16 channels.
+  const unsigned id = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  const int turn = (int)(((id >> 3) - (unsigned)k0) & 15u) % n;
   // scalar bases; the lane's part of an address is the same in every stage
   const uint8_t* codes[NT];
   const uint16_t* scale[NT];
@@ -252,8 +259,9 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
     Groups<GROUPS, ZERO> of[NT];
     uint4 x[PIECES];
   };
-  auto load = [&](Stage& t, int kt) {
-    kt = min(kt, k1 - 1);  // past the end: the last again
+  auto load = [&](Stage& t, int i_k) {
+    i_k = min(i_k, n - 1) + turn;  // past the end: the last again
+    const int kt = k0 + (i_k < n ? i_k : i_k - n);
     const int64_t at = (int64_t)(kt >> 2) * (64 * GROUPS) + (kt & 3) * GROUPS;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -271,9 +279,9 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
   };
   float y[NT][MT][4] = {};
   Stage w[3];
-  load(w[0], k0);
-  load(w[1], k0 + 1);
-  place(w[0], k0);
+  load(w[0], 0);
+  load(w[1], 1);
+  place(w[0], 0);
   auto stage = [&](auto slot, int kt) {
     constexpr int H = decltype(slot)::value;
     lds_only_barrier();  // the stage's tokens are there, and the other half is read
@@ -284,14 +292,14 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
     }, y);
     place(w[(H + 1) % 3], kt + 1);
   };
-  int kt = k0;
-  for (; kt + 2 < k1; kt += 3) {
+  int kt = 0;
+  for (; kt + 2 < n; kt += 3) {
     stage(std::integral_constant<int, 0>(), kt);
     stage(std::integral_constant<int, 1>(), kt + 1);
     stage(std::integral_constant<int, 2>(), kt + 2);
   }
-  if (kt < k1) stage(std::integral_constant<int, 0>(), kt);
-  if (kt + 1 < k1) stage(std::integral_constant<int, 1>(), kt + 1);
+  if (kt < n) stage(std::integral_constant<int, 0>(), kt);
+  if (kt + 1 < n) stage(std::integral_constant<int, 1>(), kt + 1);
   constexpr int kOut = F32 ? 4 : 2;
   const int64_t pitch = g.N * kOut, first = m0 + wm * (MT * 16) + quad * 4;
   char* out = static_cast<char*>(g.y) + (g.split > 1 ? blockIdx.z * g.slice * 4 : 0) + first * pitch + (tn0 * 16 + col) * kOut;

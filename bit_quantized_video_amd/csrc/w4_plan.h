@@ -48,10 +48,7 @@ struct W4Plan {
 
 constexpr int64_t kW4Waves = 4096;       // waves wanted of k_w4: 16 for each CU
 constexpr size_t kW4Lds = 64 << 10;    // LDS its tokens may take
-#ifndef WG
-#define WG 256
-#endif
-constexpr int64_t kW4Groups = WG;     // workgroups wanted of k_w4_shared
+constexpr int64_t kW4Groups = 256;     // workgroups wanted of k_w4_shared
 constexpr int64_t kW4LeastTiles = 4;   // tiles of K that a split keeps at least
 
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
