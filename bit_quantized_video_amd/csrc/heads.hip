@@ -171,6 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads(const HeadArgs g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) a = __builtin_elementwise_maximum(a, fabsf(x[e]));
       float scale, inv;
+      if (n <= 0) a = 0.0f;  // lanes past the head hold biases
       code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
       if (ok && in_cache) {
         const int64_t row = slot * r.heads + h;

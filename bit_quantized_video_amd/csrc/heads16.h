@@ -207,6 +207,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
           b = __builtin_elementwise_maximum(b, fabsf(y[e]));
         }
         if (whole) a = __builtin_elementwise_maximum(a, b);
+        if (LL < 0 && c >= far) a = 0.0f;  // lanes past the head hold biases, turned by any angle
         float scale, inv;
         code_scales(lanes_max(a, g.group_bits), g.top, scale, inv);
         float scale2 = scale, inv2 = inv;

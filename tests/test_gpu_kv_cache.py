@@ -110,6 +110,32 @@ def test_step_equals_its_parts():
         assert torch.equal(getattr(a, n), getattr(b, n)), n
 
 
+@pytest.mark.parametrize("dim,dims,split", [(96, (96,), True), (96, (48,), False), (72, (72,), True), (72, (32,), False),
+                                            (72, (36,), True), (40, (16,), True)])
+@pytest.mark.parametrize("dtype,odd", [(BF, 0), (F32, 0), (BF, 1)])
+@pytest.mark.parametrize("kind", ["layer", "none"])
+def test_scale_of_heads_that_leave_lanes(dim, dims, split, dtype, odd, kind):
+    """A head's scale is of its own elements: its lanes are more than it fills, and
+    the first elements' biases are larger than any of its results."""
+    T, H = 5, 3
+    flat = make((T * H * dim + odd,), dtype, 19).abs()
+    w, b = torch.ones(dim), torch.zeros(dim)
+    w[:8], b[:8] = -0.5, 64.0
+    x = flat[odd:].view(1, T, H, dim)
+    x[..., :8] += 4
+    pos = positions(1, 1, T, 20)
+    pos[0, 0, :2] = -1
+    turns, r = plan(dims, split)
+    c = hdq.KvCache(T, H, dim, hdq.CACHE_INT8, device=DEV)
+    dev = flat.to(DEV)[odd:].view(1, T, H, dim)
+    hdq.qkv_to_cache(c, None, dev, dev, torch.arange(T, device=DEV), KIND[kind], k_weight=w.to(DEV), k_bias=b.to(DEV),
+                     positions=pos.to(DEV), rope=r)
+    ref, tol = reference(x, kind, w, b, 1e-6, dims, split, turns, pos, 1.0)
+    want, off = ref.abs().amax(-1) / 127, tol.amax(-1) / 127
+    assert bool(((c.k_scale.cpu()[..., 0].double() - want).abs() <= off * (1 + R.U) + R.U * want).all())
+    assert torch.equal(c.v_scale.cpu()[..., 0], x.float().abs().amax(-1)[0] / 127)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "fp8", "int4"])
 @pytest.mark.parametrize("had", [1, 32])
 def test_values_outside_the_range(fmt, had):
