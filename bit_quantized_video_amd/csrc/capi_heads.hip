@@ -23,7 +23,7 @@ bool w4_shape_ok(int64_t N, int64_t K, int32_t group) {
 int check_w4(const hdq_w4_tensor& w) {
   if (!w4_shape_ok(w.N, w.K, w.group)) return HDQ_ERR_SHAPE;
   if (w.codes == nullptr || w.scale == nullptr) return HDQ_ERR_INVALID;
-  if (!aligned(w.codes, 16) || !aligned(w.scale, 8) || !aligned(w.zero, 4)) return HDQ_ERR_SHAPE;
+  if (!aligned(w.codes, 16) || !aligned(w.scale, 16) || !aligned(w.zero, 16)) return HDQ_ERR_SHAPE;
   return HDQ_OK;
 }
 

@@ -54,9 +54,9 @@ template <int COUNT, bool ZERO>
 struct Groups {
   uint16_t scale[COUNT];
   uint8_t zero[ZERO ? COUNT : 1];
-  // from scalar bases on
+  // from scalar bases on (buffers aligned to 16 bytes)
   __device__ __forceinline__ void load(const uint16_t* s, const uint8_t* z, uint32_t at) {
-    __builtin_memcpy(scale, __builtin_assume_aligned(s + at, 2 * COUNT), 2 * COUNT);
+    __builtin_memcpy(scale, __builtin_assume_aligned(s + at, COUNT < 8 ? 2 * COUNT : 16), 2 * COUNT);
     if (ZERO) __builtin_memcpy(zero, __builtin_assume_aligned(z + at, COUNT), COUNT);
   }
 };

@@ -854,7 +854,7 @@ def w4_pack(codes, scale, zero=None, stream=None):
     (N, half), dev = codes.shape, codes.device
     K, group = 2 * half, 2 * half // scale.shape[1]
     _operand(codes, "codes", torch.uint8, (N, half), dev)
-    if K % group:
+    if group == 0 or K % group:
         raise ValueError(f"{scale.shape[1]} scales a row do not divide {K} columns")
     _operand(scale, "scale", torch.bfloat16, (N, K // group), dev)
     if zero is not None:

@@ -651,8 +651,8 @@ int hdq_group_norm_fp8(const void *x, int32_t x_dtype, int64_t n, int64_t length
  * A tensor [N, K] is kept packed in tiles of 16 rows x 128 columns, both
  * rounded up (hdq_w4_pack and hdq_w4_quantize write it, padding included):
  *   codes : device, hdq_w4_bytes(..., HDQ_W4_CODES) bytes, 16-byte aligned;
- *   scale : device bf16, hdq_w4_bytes(..., HDQ_W4_SCALE) bytes, 8-byte aligned;
- *   zero  : NULL, or device, hdq_w4_bytes(..., HDQ_W4_ZERO) bytes, 4-byte aligned.
+ *   scale : device bf16, hdq_w4_bytes(..., HDQ_W4_SCALE) bytes, 16-byte aligned;
+ *   zero  : NULL, or device, hdq_w4_bytes(..., HDQ_W4_ZERO) bytes, 16-byte aligned.
  * N at most HDQ_W4_MAX_ROWS, K a multiple of 32 and of the group, at most
  * HDQ_FP8_MAX_COLS. */
 #define HDQ_W4_CODES 0
@@ -698,7 +698,8 @@ int hdq_w4_quantize(const void *w, const hdq_w4_tensor *out, void *stream);
  * A group's sum is taken in float32 on the matrix instructions, as
  * sum (16 + u) x - (16 + z) sum x with exact products, and scaled and added in
  * float32; the error is that of a float32 sum over terms (32 + z) / |u - z| times
- * as large.
+ * as large.  A token with a NaN or an infinity, or with such a sum past float32's
+ * range, gets NaN or infinities; the others' outputs are not touched by it.
  *   ws, ws_bytes : device scratch, 256-byte aligned, >=
  *       hdq_w4_linear_workspace_bytes(M, N, K) (NULL where that is 0, as for one
  *       token of up to 32640 columns).  Nothing in it needs a value before the call; calls that

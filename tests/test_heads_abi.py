@@ -94,7 +94,8 @@ def test_w4_refusals(hdq):
     assert lin(x=FAKE + 2) == hdq.ERR_SHAPE and lin(y=FAKE + 1) == hdq.ERR_SHAPE and lin(y=FAKE + 2, t=0) == hdq.ERR_SHAPE
     assert lin(M=0) == hdq.OK and lin(M=0, x=None, y=None) == hdq.OK
     for w in (T(0, 128, 64, FAKE, FAKE, None), T(100, 96, 64, FAKE, FAKE, None), T(100, 128, 16, FAKE, FAKE, None),
-              T(100, 128, 64, FAKE + 8, FAKE, None), T(100, 128, 64, FAKE, FAKE + 4, None), T(100, 128, 64, FAKE, FAKE, FAKE + 2)):
+              T(100, 128, 64, FAKE + 8, FAKE, None), T(100, 128, 64, FAKE, FAKE + 4, None), T(100, 128, 64, FAKE, FAKE, FAKE + 2),
+              T(100, 128, 64, FAKE, FAKE + 8, None), T(100, 128, 64, FAKE, FAKE, FAKE + 8)):
         assert lin(w=w) == hdq.ERR_SHAPE and L.hdq_w4_quantize(FAKE, w, None) == hdq.ERR_SHAPE
         zero = FAKE if w.zero else None
         assert L.hdq_w4_pack(FAKE, FAKE, zero, w, None) == hdq.ERR_SHAPE
@@ -109,7 +110,7 @@ def test_w4_refusals(hdq):
             hdq.W4Weights(*bad, device="cpu")
     codes, scale = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.bfloat16)
     for args in ((codes, scale), (codes.int(), scale), (codes, scale[:, :0]), (codes, scale.float()), (codes, scale[:3]),
-                 (codes, scale, scale)):
+                 (codes, scale, scale), (codes, scale.repeat(1, 100)), (codes[:, :0], scale)):
         with pytest.raises(ValueError):           # wrong operands, and (the first) not on a GPU
             hdq.w4_pack(*args)
 
