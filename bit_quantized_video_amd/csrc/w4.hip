@@ -7,8 +7,9 @@
 // its other columns unused, at no cost beside the loads.  A code becomes bf16
 // in one operation a pair: nibble u in bits 6..3 of a bf16 16.0 is 16 + u,
 // exact, so the product is sum (16 + u) x - (16 + z) sum x, and sum x comes from a
-// second product with ones.  Sums are float32: the difference costs at most
-// (31 + 31) / 8 times a float32 sum's rounding.
+// second product with ones; without zero points from one with -24, in whose
+// registers the codes' product goes on.  Sums are float32: the difference costs
+// at most (31 + 31) / 8 times a float32 sum's rounding.
 #include "hdq_device.h"
 #include "hdq_internal.h"
 #include "w4.h"
@@ -28,6 +29,7 @@ struct W4Args {
   int64_t M, N, K;
   int64_t tiles_n, tiles_k;
   int wn, wk, per;  // k_w4: waves along rows and K, tiles of rows of a wave
+  int step, part;   // its waves, in tokens of as many blocks and blocks
   int split;      // workgroups along K; above 1 each writes float32 sums to y + its number * slice
   int64_t slice;
 };
@@ -68,34 +70,38 @@ template <int MT, int NT, int R, int GROUPS, int COUNT, bool ZERO, typename X>
 __device__ __forceinline__ void multiply(const v4u (&codes)[NT], const Groups<COUNT, ZERO> (&of)[NT], int at, const X& x,
                                          float (&y)[NT][MT][R]) {
   constexpr int STEPS = 4 / GROUPS;
-  const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  // ones, or without zero points the -24 itself, whose product the codes' then begins with
+  constexpr uint32_t kSum = ZERO ? 0x3f803f80u : 0xc1c0c1c0u;
+  const v8bf ones = __builtin_bit_cast(v8bf, v4u{kSum, kSum, kSum, kSum});
   const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int q = 0; q < GROUPS; ++q) {
     v4f d[NT][MT], sum[MT];
+    v8bf a[STEPS][MT];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      v8bf a[MT];
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        a[m] = x(m, q * STEPS + s);
-        sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m], ones, s == 0 ? none : sum[m], 0, 0, 0);
+        a[s][m] = x(m, q * STEPS + s);
+        sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][m], ones, s == 0 ? none : sum[m], 0, 0, 0);
       }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const v8bf b = decode(codes[i][q * STEPS + s]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) d[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m], b, s == 0 ? none : d[i][m], 0, 0, 0);
+        for (int m = 0; m < MT; ++m)
+          d[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][m], b, s > 0 ? d[i][m] : ZERO ? none : sum[m], 0, 0, 0);
       }
-    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const float sc = __uint_as_float((uint32_t)of[i].scale[at + q] << 16);
-      const float off = ZERO ? 16.0f + (float)of[i].zero[ZERO ? at + q : 0] : 24.0f;
+      const float off = ZERO ? 16.0f + (float)of[i].zero[ZERO ? at + q : 0] : 0.0f;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < R; ++r) y[i][m][r] = fmaf(sc, fmaf(-off, sum[m][r], d[i][m][r]), y[i][m][r]);
+        for (int r = 0; r < R; ++r) y[i][m][r] = fmaf(sc, ZERO ? fmaf(-off, sum[m][r], d[i][m][r]) : d[i][m][r], y[i][m][r]);
     }
     // one group's products at a time: with all of a tile's the compiler runs out of registers
     if (MT > 1) __builtin_amdgcn_sched_barrier(0);
@@ -155,14 +161,30 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
   Block ring[2];
   if (count > 0) load(ring[0], next_tn, next_b);
 
-  // the tokens, zeros past the last column
-  const int pieces = tiles_k * 16, filled = (int)(g.K / 8);
-  for (int m = 0; m < (int)g.M; ++m)
-    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
-      v4u v = {0u, 0u, 0u, 0u};
-      if (i < filled) v = *reinterpret_cast<const v4u*>(g.x + m * g.K + i * 8);
-      *reinterpret_cast<v4u*>(s_lds + m * pitch + i * 16) = v;
+  // the tokens, zeros past the last column: 64 pieces of a token a wave at a time, four such loads in flight
+  const int pieces = tiles_k * 16, filled = (int)(g.K / 8), tokens = (int)g.M;
+  int m = 0, part = wave;
+  while (part >= blocks) part -= blocks, ++m;
+  while (m < tokens) {
+    v4u v[4];
+    int to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      to[j] = -1;
+      if (m < tokens) {
+        const int i = part * 64 + lane;
+        if (i < pieces) to[j] = m * pitch + i * 16;
+        v[j] = v4u{0u, 0u, 0u, 0u};
+        if (i < filled) v[j] = *reinterpret_cast<const v4u*>(g.x + m * g.K + i * 8);
+      }
+      m += g.step;
+      part += g.part;
+      if (part >= blocks) part -= blocks, ++m;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (to[j] >= 0) *reinterpret_cast<v4u*>(s_lds + to[j]) = v[j];
+  }
   __syncthreads();
   // rows of tokens that are not there repeat the first's, and are not stored
   const int token = (col & 3) * 4 + (col >> 2);
@@ -286,6 +308,7 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
     constexpr int H = decltype(slot)::value;
     lds_only_barrier();  // the stage's tokens are there, and the other half is read
     load(w[(H + 2) % 3], kt + 2);
+    __builtin_amdgcn_sched_barrier(0);  // first: two whole stages to arrive in
     const uint8_t* xs = s_x[kt & 1] + wm * (MT * 4096) + col * 256;
     multiply<MT, NT, 4, GROUPS>(w[H].codes, w[H].of, 0, [&](int m, int s) {
       return *reinterpret_cast<const v8bf*>(xs + m * 4096 + (((4 * s + quad) ^ col) * 16));
@@ -478,7 +501,8 @@ hipError_t launch_w4(const uint16_t* x, int64_t M, const W4Weights& w, void* y, 
   const W4Plan p = plan_w4(M, w.N, w.K);
   const bool join = p.split > 1;
   const int64_t slice = w4_slice(M, w.N), count = M * w.N;
-  const W4Args a{x, w.codes, w.scale, w.zero, join ? ws : y, M, w.N, w.K, w4_tiles_n(w.N), w4_tiles_k(w.K), p.wn, p.wk, p.per, p.split, slice};
+  const W4Args a{x, w.codes, w.scale, w.zero, join ? ws : y, M, w.N, w.K, w4_tiles_n(w.N), w4_tiles_k(w.K),
+                 p.wn, p.wk, p.per, p.step, p.part, p.split, slice};
   f32 || join ? run_group<true>(a, p, w.group, s) : run_group<false>(a, p, w.group, s);
   if (join) {
     const dim3 grid = wide_grid((count + 1023) / 1024);

@@ -40,6 +40,7 @@ inline int64_t w4_group_at(int64_t tn, int64_t n, int64_t kg, int64_t tiles_k, i
 struct W4Plan {
   int per;      // k_w4: tiles of rows of a wave, 0: k_w4_shared
   int wn, wk;   // waves of a workgroup along the rows, and along K
+  int step, part;  // k_w4: wn * wk waves in whole tokens of a block of K each, and the rest
   size_t lds;
   int mt;       // k_w4_shared: tiles of 16 tokens
   int split;    // workgroups along K
@@ -66,6 +67,8 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
     wk = (blocks + each - 1) / each;
     p.wk = (int)wk;
     p.wn = wk >= 4 ? 1 : (int)(8 / wk);
+    p.step = (int)(p.wn * p.wk / blocks);
+    p.part = (int)(p.wn * p.wk % blocks);
     p.per = wk > 1 ? 1 : (int)((tn + kW4Waves - 1) / kW4Waves);
     p.grid_x = (tn + p.wn * p.per - 1) / (p.wn * p.per);
     if (wk > 1 && p.lds < (size_t)(p.wn * p.wk) * 1024) p.lds = (size_t)(p.wn * p.wk) * 1024;

@@ -145,8 +145,9 @@ def w4_values(codes):
 
 
 def w4_linear(x, codes, scale, zero, group):
-    """(y float64, bound): a group's sums of (16 + u) x and (16 + z) x round at most
-    group + 8 times each, the scaled sums once a group and once a wave more."""
+    """(y float64, bound): a group's sums of (16 + u) x and (16 + z) x, beside each other
+    or one after the other, round at most group + 8 times (a matrix instruction adds
+    several products before it rounds), the scaled sums once a group and once a wave more."""
     N = codes.shape[0]
     u = w4_values(codes).double().view(N, -1, group)
     z = zero.double().unsqueeze(2) if zero is not None else torch.full((N, u.shape[1], 1), 8.0, dtype=torch.float64)
