@@ -239,7 +239,7 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
 // takes longer than a stage), none of them under a condition: the waits then
 // count the ones that may still be in flight.
 template <int MW, int MT, int NT, int GROUPS, bool ZERO, bool F32>
-__global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
+__global__ __launch_bounds__(512, MT > 1 && !ZERO ? 4 : 2) void k_w4_shared(const W4Args g) {
   static_assert(NT * (8 / MW) == 8, "128 rows a workgroup");
   constexpr int TILES = MT * MW;            // of 16 tokens
   constexpr int PIECES = (TILES + 1) / 2;   // of the tokens a thread brings
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(512) void k_w4_shared(const W4Args g) {
     constexpr int H = decltype(slot)::value;
     lds_only_barrier();  // the stage's tokens are there, and the other half is read
     load(w[(H + 2) % 3], kt + 2);
-    __builtin_amdgcn_sched_barrier(0);  // first: two whole stages to arrive in
+    if (MT == 1) __builtin_amdgcn_sched_barrier(0);  // first: two whole stages to arrive in
     const uint8_t* xs = s_x[kt & 1] + wm * (MT * 4096) + col * 256;
     multiply<MT, NT, 4, GROUPS>(w[H].codes, w[H].of, 0, [&](int m, int s) {
       return *reinterpret_cast<const v8bf*>(xs + m * 4096 + (((4 * s + quad) ^ col) * 16));

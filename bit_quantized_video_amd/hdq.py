@@ -1021,8 +1021,11 @@ def _out_heads(out, x, shape, y_dtype, name, dev):
         if out.shape != x.shape:
             raise ValueError(f"{name} {tuple(out.shape)} for an input {tuple(x.shape)}")
         return out, _heads(out, name, H, D, dev)
-    sizes = (B, T, H, D) if x.dim() == 4 else (T, H, D)
-    out = x.new_empty(sizes) if y_dtype is None else x.new_empty(sizes, dtype=_F32 if y_dtype == DTYPE_F32 else _BF16)
+    dtype = x.dtype if y_dtype is None else _F32 if y_dtype == DTYPE_F32 else _BF16
+    if dtype is not x.dtype:
+        out = x.new_empty((B, T, H, D) if x.dim() == 4 else (T, H, D), dtype=dtype)
+    else:                       # the quicker forms
+        out = x.new_empty(B, T, H, D) if x.dim() == 4 else x.new_empty(T, H, D)
     return out, _HEADS.pack(out.data_ptr(), _row_dtype(out.dtype), H, T * H * D, H * D, D)
 
 
