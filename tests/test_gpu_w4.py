@@ -163,3 +163,52 @@ def test_serving_step(T):
         # largest group's, a step at most the rotated maximum / 127, that at most the head's 2-norm
         err = (y[past:].cpu().double() - ref[0]).norm(dim=-1)
         assert bool((err <= ref[0].norm(dim=-1) * (math.sqrt(D) / 2 / 127 + 2.0 ** -18) + tol[0].norm(dim=-1)).all())
+
+
+@pytest.mark.parametrize("M,N,K,group", [
+    (1, 20, 32640, 128), (1, 20, 32672, 32),      # the last row of tokens that LDS takes, the first it does not
+    (9, 33, 3584, 64), (9, 33, 3616, 32), (16, 40, 1920, 64), (16, 40, 2048, 128), (8, 17, 4064, 32), (8, 17, 4096, 64),
+    (4, 70001, 128, 64), (13, 66000, 256, 32),    # several tiles of rows a wave
+    (2, 500, 20480, 64), (33, 16, 8192, 128), (64, 2050, 1920, 32), (200, 129, 512, 64)])
+@pytest.mark.parametrize("zero", [False, True])
+def test_edges_of_the_forms(M, N, K, group, zero):
+    codes, scale, z = R.w4_random(N, K, group, zero, 3 * M + N)
+    x = make((M, K), BF, 21)
+    w = hdq.w4_pack(codes.to(DEV), scale.to(DEV), z.to(DEV) if zero else None)
+    check(hdq.w4_linear(x.to(DEV), w, y_dtype=hdq.DTYPE_F32), x, codes, scale, z, group)
+
+
+def test_scratch_and_streams():
+    """The caller's scratch, whatever it held; calls that overlap on two streams."""
+    M, N, K = 40, 300, 8192
+    codes, scale, _ = R.w4_random(N, K, 64, False, 31)
+    w = hdq.w4_pack(codes.to(DEV), scale.to(DEV))
+    xs = [make((M, K), BF, 32 + i).to(DEV) for i in range(2)]
+    want = [hdq.w4_linear(x, w) for x in xs]
+    need = hdq.w4_linear_workspace_bytes(M, N, K)
+    assert need > 0
+    for size in (need, need + 4096, 16):          # too small: one of its own
+        ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+        assert all(torch.equal(hdq.w4_linear(x, w, ws=ws), y) for x, y in zip(xs, want))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for x, s, g in zip(xs, streams, got):
+            g.append(hdq.w4_linear(x, w, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    # two graphs that share the caller's scratch, replayed one after the other
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = hdq.w4_linear(x, w, ws=ws)
+        graphs.append((g, y))
+    for i in (0, 1, 1, 0):
+        ws.fill_(77)
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[i][1], want[i])
