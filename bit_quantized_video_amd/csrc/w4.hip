@@ -231,6 +231,48 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
   }
 }
 
+// Up to 16 tokens and few rows.  The workgroup has one tile of rows, so it wants
+// a fragment of the tokens once and LDS would serve no second reader; with a
+// block of K for each wave all its loads are in flight at once.
+template <int GROUPS, bool ZERO, bool F32>
+__global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
+  __shared__ float s_sums[16][4][64];
+  const int lane = threadIdx.x & 63, b = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int tiles_k = (int)g.tiles_k, blocks = (tiles_k + 3) >> 2;
+  const int64_t tn = blockIdx.x, group = (tn * blocks + b) * (64 * GROUPS);
+  const uint8_t* codes = g.codes + (tn * tiles_k + 4 * b) * 1024;
+  // rows of tokens that are not there repeat the first's, and are not stored; columns past the last read zeros
+  const uint32_t bytes = (uint32_t)(g.M * g.K * 2), k_bytes = (uint32_t)(g.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x, bytes);
+  const uint32_t from = (col < g.M ? col : 0) * k_bytes + quad * 16;
+  v4u w[4][1];
+  Groups<4 * GROUPS, ZERO> of[1];
+  uint4 x[16];
+  of[0].load(g.scale + group, ZERO ? g.zero + group : nullptr, col * (4 * GROUPS));
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (4 * b + j < tiles_k) w[j][0] = reinterpret_cast<const v4u*>(codes + j * 1024)[lane];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t at = b * 1024 + i * 64;  // bytes of a token before the fragment
+    x[i] = buf_load16(xr, at + quad * 16 < k_bytes ? from : bytes, at);
+  }
+  float y[1][1][4] = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (4 * b + j < tiles_k)
+      multiply<1, 1, 4, GROUPS>(w[j], of, j * GROUPS, [&](int, int s) { return __builtin_bit_cast(v8bf, x[4 * j + s]); }, y);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s_sums[b][r][lane] = y[0][0][r];
+  __syncthreads();
+  for (int r = b; r < 4; r += blocks) {
+    float v = s_sums[0][r][lane];
+    for (int k = 1; k < blocks; ++k) v += s_sums[k][r][lane];
+    store<F32>(g, g.y, 4 * quad + r, tn * 16 + col, v);
+  }
+}
+
 // More tokens, or longer ones.  A workgroup of eight waves takes 16 MT MW tokens
 // x 128 rows, 128 columns a stage; a wave multiplies MT tiles of tokens and NT
 // of rows, MW waves sharing the rows.  The tokens lie in LDS in rows of 16
@@ -477,6 +519,8 @@ void run(const W4Args& a, const W4Plan& p, hipStream_t s) {
     k_w4<2, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.per > 0)
     k_w4<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.direct)
+    k_w4_direct<GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 4)
     k_w4_shared<2, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 2)

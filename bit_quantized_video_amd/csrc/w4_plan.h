@@ -32,35 +32,56 @@ inline int64_t w4_group_at(int64_t tn, int64_t n, int64_t kg, int64_t tiles_k, i
   return ((tn * ((tiles_k + 3) / 4) + kg / (4 * groups)) * 16 + n) * (4 * groups) + kg % (4 * groups);
 }
 
-// Up to 16 tokens that fit LDS: a workgroup keeps them there and streams
-// weights (k_w4).  Else a workgroup of four waves shares 64 tokens (16 or 32
-// where there are no more) a stage at a time among 128 rows, and K is split
-// over workgroups, whose sums a second launch adds, where there are too few
-// (k_w4_shared).
+// How a product runs.
+//   k_w4_direct: up to 16 tokens and few rows.  A workgroup has one tile of
+//     rows and a wave for each block of four tiles of K (at most 16): every
+//     wave loads all it needs at once, the tokens straight from L2.
+//   k_w4: up to 16 tokens that fit LDS.  A workgroup keeps them there and
+//     streams weights.
+//   k_w4_shared: else.  A workgroup of eight waves shares 64 tokens (16 or 32
+//     where there are no more) a stage at a time among 128 rows, and K is split
+//     over workgroups, whose sums a second launch adds, where there are too few.
 struct W4Plan {
-  int per;      // k_w4: tiles of rows of a wave, 0: k_w4_shared
-  int wn, wk;   // waves of a workgroup along the rows, and along K
+  bool direct;     // k_w4_direct
+  int per;         // k_w4: tiles of rows of a wave; with neither k_w4_shared
+  int wn, wk;      // waves of a workgroup along the rows, and along K
   int step, part;  // k_w4: wn * wk waves in whole tokens of a block of K each, and the rest
   size_t lds;
-  int mt;       // k_w4_shared: tiles of 16 tokens
-  int split;    // workgroups along K
+  int mt;          // k_w4_shared: tiles of 16 tokens
+  int split;       // workgroups along K
   int64_t grid_x, grid_y;
 };
 
-constexpr int64_t kW4Waves = 4096;       // waves wanted of k_w4: 16 for each CU
-constexpr size_t kW4Lds = 64 << 10;    // LDS its tokens may take
-constexpr int64_t kW4Groups = 256;     // workgroups wanted of k_w4_shared
-constexpr int64_t kW4LeastTiles = 4;   // tiles of K that a split keeps at least
+// k_w4_direct: rows in tiles (three workgroups a CU), waves (as many as run at a
+// time) and bytes of tokens that a CU's workgroups read.  Within these it is the
+// faster one (us on the GPU; k_w4, or k_w4_shared and its second launch):
+//   16 x 1920 -> 1920 4.7 (6.8), -> 12288 9.1 (14.5); 1 x 4096 -> 4096 4.3 (4.6);
+//   13 x 4096 -> 4096 6.7 (5.0 + 2.4, and 7.2 for 11.1 a call).
+// Past them it is not: 4 x 512 -> 65536 8.6 (6.7; 4096 tiles of rows), 16 x 4096
+// -> 8192 11.6 (7.0 + 2.4; 256 KB), 16 x 8192 -> 4096 11.7 (7.2 + 2.4; 256 KB).
+constexpr int64_t kW4DirectTiles = 768, kW4DirectWaves = 4096, kW4DirectBytes = 192 << 10;
+constexpr int64_t kW4Waves = 4096;    // waves wanted of k_w4: 16 a CU, what its registers leave room for
+constexpr size_t kW4Lds = 64 << 10;   // LDS its tokens may take: 13 x 4096 -> 1921 in 106 KB took 8.2 us (5.4 + 2.5 shared)
+constexpr int64_t kW4Groups = 256;    // workgroups wanted of k_w4_shared, one a CU: with 512 its sums cost what it gains
+constexpr int64_t kW4LeastTiles = 4;  // tiles of K that a split keeps at least: a stage is a tile, and two are loaded ahead
 
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
   W4Plan p = {};
   const int64_t tm = (M + 15) / 16, tn = w4_tiles_n(N), tk = w4_tiles_k(K);
   p.split = 1;
   p.lds = (size_t)M * (size_t)(tk * 256 + 16);
-  if (tm == 1 && p.lds <= kW4Lds) {
+  const int64_t blocks = (tk + 3) / 4;
+  if (tm == 1 && blocks <= 16 && tn <= kW4DirectTiles && tn * blocks <= kW4DirectWaves &&
+      (tn + 255) / 256 * M * K * 2 <= kW4DirectBytes) {
+    p.direct = true;
+    p.wn = 1;
+    p.wk = (int)blocks;
+    p.lds = 0;
+    p.grid_x = tn;
+    p.grid_y = 1;
+  } else if (tm == 1 && p.lds <= kW4Lds) {
     p.grid_y = 1;
     // waves of a tile of rows: as many as there are blocks of four tiles of K, and tiles of rows to go round
-    const int64_t blocks = (tk + 3) / 4;
     int64_t wk = kW4Waves / tn < blocks ? kW4Waves / tn : blocks;
     wk = wk > 16 ? 16 : wk < 1 ? 1 : wk;
     const int64_t each = (blocks + wk - 1) / wk;  // the same number of blocks for each, as far as that goes

@@ -169,6 +169,8 @@ def test_serving_step(T):
     (1, 20, 32640, 128), (1, 20, 32672, 32),      # the last row of tokens that LDS takes, the first it does not
     (9, 33, 3584, 64), (9, 33, 3616, 32), (16, 40, 1920, 64), (16, 40, 2048, 128), (8, 17, 4064, 32), (8, 17, 4096, 64),
     (4, 70001, 128, 64), (13, 66000, 256, 32),    # several tiles of rows a wave
+    (7, 13000, 1920, 64), (16, 12300, 1920, 128), (3, 12305, 2080, 32), (2, 12289, 96, 32), (5, 26000, 640, 128),  # waves that share K
+    (16, 12288, 1920, 64), (1, 12288, 2560, 128), (1, 4096, 8192, 64), (12, 256, 8192, 128), (13, 256, 8192, 128),
     (2, 500, 20480, 64), (33, 16, 8192, 128), (64, 2050, 1920, 32), (200, 129, 512, 64)])
 @pytest.mark.parametrize("zero", [False, True])
 def test_edges_of_the_forms(M, N, K, group, zero):

@@ -24,7 +24,7 @@ int main() {
                   p.slices[0], p.slices[1], (long long)p.groups);
     } else {
       const W4Plan p = plan_w4(a, b, c);
-      std::printf("%d %d %d %lld %d %d %lld %lld %lld %lld\\n", p.per, p.wn, p.wk, (long long)p.lds, p.mt, p.split,
+      std::printf("%d %d %d %d %d %d %lld %d %d %lld %lld %lld %lld\\n", (int)p.direct, p.step, p.part, p.per, p.wn, p.wk, (long long)p.lds, p.mt, p.split,
                   (long long)p.grid_x, (long long)p.grid_y, (long long)w4_workspace(a, b, c), (long long)w4_slice(a, b));
     }
   }
@@ -100,14 +100,18 @@ def test_w4(plans):
     for _ in range(4000):
         sizes.append((log_size(g, 1, g.choice((16, 200, top_m))), log_size(g, 1, top_n), 32 * log_size(g, 1, g.choice((100, top_k // 32)))))
     forms = set()
-    for (m, n, k), (per, wn, wk, lds, mt, split, gx, gy, ws, piece) in zip(sizes, plans("w", sizes)):
+    for (m, n, k), (direct, step, part, per, wn, wk, lds, mt, split, gx, gy, ws, piece) in zip(sizes, plans("w", sizes)):
         s = (m, n, k)
         tn, tk = up(n, 16), up(k, 128)
         blocks = up(tk, 4)
         assert 0 < gy < 1 << 16 and 0 < split < 1 << 16 and gx * 64 * wn * wk < 1 << 32, s
         assert m * n <= piece < m * n + 4
-        if per:
+        if direct:
+            forms.add("direct")
+            assert m <= 16 and wn == 1 and wk == blocks <= 16 and gx == tn and gy == split == 1 and ws == 0 and per == 0, s
+        elif per:
             forms.add((per > 1, wk > 1, wn > 1))
+            assert step * blocks + part == wn * wk and 0 <= part < blocks, s
             assert m <= 16 and gy == split == 1 and ws == 0
             assert 64 * wn * wk <= (1024 if m <= 8 else 512), s          # the kernels' launch bounds
             assert lds <= 65536 and lds >= m * (tk * 256 + 16), s
@@ -126,4 +130,4 @@ def test_w4(plans):
         if m <= 16 and m * k <= 24576:                                     # what the binding takes to need no scratch
             assert ws == 0, s
     assert {(1, True), (1, False), (2, True), (2, False), (4, True), (4, False)} <= forms
-    assert {(False, True, False), (False, False, True), (True, False, True), (False, True, True)} <= forms
+    assert "direct" in forms and {(False, True, False), (False, False, True), (True, False, True), (False, True, True)} <= forms
