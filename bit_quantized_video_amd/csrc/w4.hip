@@ -231,45 +231,53 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
   }
 }
 
-// Up to 16 tokens and few rows.  The workgroup has one tile of rows, so it wants
-// a fragment of the tokens once and LDS would serve no second reader; with a
-// block of K for each wave all its loads are in flight at once.
-template <int GROUPS, bool ZERO, bool F32>
+// Few rows.  The workgroup has one tile of them, so it wants a fragment of the
+// tokens once and LDS would serve no second reader; with 4 / MT tiles of K for
+// each wave (16 fragments of the tokens, 64 registers) all its loads are in
+// flight at once.
+template <int MT, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
-  __shared__ float s_sums[16][4][64];
-  const int lane = threadIdx.x & 63, b = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int TILES = 4 / MT;  // of K, a wave's
+  extern __shared__ __align__(16) float s_sums[];  // [waves][MT][4][64]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int tiles_k = (int)g.tiles_k, blocks = (tiles_k + 3) >> 2;
-  const int64_t tn = blockIdx.x, group = (tn * blocks + b) * (64 * GROUPS);
-  const uint8_t* codes = g.codes + (tn * tiles_k + 4 * b) * 1024;
+  const int tiles_k = (int)g.tiles_k, k0 = wave * TILES;
+  const int64_t tn = blockIdx.x;
+  const int64_t group = tn * ((tiles_k + 3) >> 2) * (64 * GROUPS) + (k0 >> 2) * (64 * GROUPS) + (k0 & 3) * GROUPS;
+  const uint8_t* codes = g.codes + (tn * tiles_k + k0) * 1024;
   // rows of tokens that are not there repeat the first's, and are not stored; columns past the last read zeros
   const uint32_t bytes = (uint32_t)(g.M * g.K * 2), k_bytes = (uint32_t)(g.K * 2);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x, bytes);
-  const uint32_t from = (col < g.M ? col : 0) * k_bytes + quad * 16;
-  v4u w[4][1];
-  Groups<4 * GROUPS, ZERO> of[1];
-  uint4 x[16];
+  uint32_t from[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) from[m] = (16 * m + col < g.M ? 16 * m + col : 0) * k_bytes + quad * 16;
+  v4u w[TILES][1];
+  Groups<TILES * GROUPS, ZERO> of[1];
+  uint4 x[TILES * 4][MT];
   of[0].load(g.scale + group, ZERO ? g.zero + group : nullptr, col * (4 * GROUPS));
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * b + j < tiles_k) w[j][0] = reinterpret_cast<const v4u*>(codes + j * 1024)[lane];
+  for (int j = 0; j < TILES; ++j)
+    if (k0 + j < tiles_k) w[j][0] = reinterpret_cast<const v4u*>(codes + j * 1024)[lane];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t at = b * 1024 + i * 64;  // bytes of a token before the fragment
-    x[i] = buf_load16(xr, at + quad * 16 < k_bytes ? from : bytes, at);
+  for (int i = 0; i < TILES * 4; ++i) {
+    const uint32_t at = k0 * 256 + i * 64;  // bytes of a token before the fragment
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x[i][m] = buf_load16(xr, at + quad * 16 < k_bytes ? from[m] : bytes, at);
   }
-  float y[1][1][4] = {};
+  float y[1][MT][4] = {};
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * b + j < tiles_k)
-      multiply<1, 1, 4, GROUPS>(w[j], of, j * GROUPS, [&](int, int s) { return __builtin_bit_cast(v8bf, x[4 * j + s]); }, y);
+  for (int j = 0; j < TILES; ++j)
+    if (k0 + j < tiles_k)
+      multiply<MT, 1, 4, GROUPS>(w[j], of, j * GROUPS, [&](int m, int s) { return __builtin_bit_cast(v8bf, x[4 * j + s][m]); }, y);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) s_sums[b][r][lane] = y[0][0][r];
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s_sums[((wave * MT + m) * 4 + r) * 64 + lane] = y[0][m][r];
   __syncthreads();
-  for (int r = b; r < 4; r += blocks) {
-    float v = s_sums[0][r][lane];
-    for (int k = 1; k < blocks; ++k) v += s_sums[k][r][lane];
-    store<F32>(g, g.y, 4 * quad + r, tn * 16 + col, v);
+  for (int r = wave; r < 4 * MT; r += g.wk) {
+    float v = s_sums[r * 64 + lane];
+    for (int k = 1; k < g.wk; ++k) v += s_sums[(k * MT * 4 + r) * 64 + lane];
+    store<F32>(g, g.y, 16 * (r >> 2) + 4 * quad + (r & 3), tn * 16 + col, v);
   }
 }
 
@@ -519,8 +527,12 @@ void run(const W4Args& a, const W4Plan& p, hipStream_t s) {
     k_w4<2, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.per > 0)
     k_w4<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.direct && p.mt == 1)
+    k_w4_direct<1, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.direct && p.mt == 2)
+    k_w4_direct<2, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.direct)
-    k_w4_direct<GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_direct<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.mt == 4)
     k_w4_shared<2, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 2)

@@ -33,9 +33,10 @@ inline int64_t w4_group_at(int64_t tn, int64_t n, int64_t kg, int64_t tiles_k, i
 }
 
 // How a product runs.
-//   k_w4_direct: up to 16 tokens and few rows.  A workgroup has one tile of
-//     rows and a wave for each block of four tiles of K (at most 16): every
-//     wave loads all it needs at once, the tokens straight from L2.
+//   k_w4_direct: up to 64 tokens and few rows.  A workgroup has one tile of
+//     rows and a wave for every four tiles of K (two or one from 17 and 33 tokens
+//     on; at most 16 waves), which loads all it needs at once, the tokens
+//     straight from L2.
 //   k_w4: up to 16 tokens that fit LDS.  A workgroup keeps them there and
 //     streams weights.
 //   k_w4_shared: else.  A workgroup of eight waves shares 64 tokens (16 or 32
@@ -47,7 +48,7 @@ struct W4Plan {
   int wn, wk;      // waves of a workgroup along the rows, and along K
   int step, part;  // k_w4: wn * wk waves in whole tokens of a block of K each, and the rest
   size_t lds;
-  int mt;          // k_w4_shared: tiles of 16 tokens
+  int mt;          // k_w4_direct, k_w4_shared: tiles of 16 tokens of a workgroup
   int split;       // workgroups along K
   int64_t grid_x, grid_y;
 };
@@ -55,10 +56,11 @@ struct W4Plan {
 // k_w4_direct: rows in tiles (three workgroups a CU), waves (as many as run at a
 // time) and bytes of tokens that a CU's workgroups read.  Within these it is the
 // faster one (us on the GPU; k_w4, or k_w4_shared and its second launch):
-//   16 x 1920 -> 1920 4.7 (6.8), -> 12288 9.1 (14.5); 1 x 4096 -> 4096 4.3 (4.6);
-//   13 x 4096 -> 4096 6.7 (5.0 + 2.4, and 7.2 for 11.1 a call).
+//   1 x 4096 -> 4096 4.3 (4.6), 16 x 1920 -> 1920 4.7 (6.8), -> 12288 9.1 (14.5),
+//   13 x 4096 -> 4096 6.7 (5.0 + 2.4, and 7.2 for 11.1 a call), 32 x 1920 -> 1920
+//   6.3 (6.2 + 2.2), 64 x 1024 -> 4096 7.2 (7.6 + 2.5).
 // Past them it is not: 4 x 512 -> 65536 8.6 (6.7; 4096 tiles of rows), 16 x 4096
-// -> 8192 11.6 (7.0 + 2.4; 256 KB), 16 x 8192 -> 4096 11.7 (7.2 + 2.4; 256 KB).
+// -> 8192 11.6 (7.0 + 2.4; 256 KB), 32 x 4096 -> 4096 10.6 (7.3 + 3.0; 256 KB).
 constexpr int64_t kW4DirectTiles = 768, kW4DirectWaves = 4096, kW4DirectBytes = 192 << 10;
 constexpr int64_t kW4Waves = 4096;    // waves wanted of k_w4: 16 a CU, what its registers leave room for
 constexpr size_t kW4Lds = 64 << 10;   // LDS its tokens may take: 13 x 4096 -> 1921 in 106 KB took 8.2 us (5.4 + 2.5 shared)
@@ -71,12 +73,14 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
   p.split = 1;
   p.lds = (size_t)M * (size_t)(tk * 256 + 16);
   const int64_t blocks = (tk + 3) / 4;
-  if (tm == 1 && blocks <= 16 && tn <= kW4DirectTiles && tn * blocks <= kW4DirectWaves &&
+  p.mt = tm <= 2 ? (int)tm : 4;
+  const int64_t parts = (tk * p.mt + 3) / 4;  // waves of k_w4_direct
+  if (tm <= 4 && parts <= 16 && tn <= kW4DirectTiles && tn * parts <= kW4DirectWaves &&
       (tn + 255) / 256 * M * K * 2 <= kW4DirectBytes) {
     p.direct = true;
     p.wn = 1;
-    p.wk = (int)blocks;
-    p.lds = 0;
+    p.wk = (int)parts;
+    p.lds = (size_t)(parts * p.mt) * 1024;
     p.grid_x = tn;
     p.grid_y = 1;
   } else if (tm == 1 && p.lds <= kW4Lds) {
@@ -94,7 +98,6 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K) {
     p.grid_x = (tn + p.wn * p.per - 1) / (p.wn * p.per);
     if (wk > 1 && p.lds < (size_t)(p.wn * p.wk) * 1024) p.lds = (size_t)(p.wn * p.wk) * 1024;
   } else {
-    p.mt = tm == 1 ? 1 : tm == 2 ? 2 : 4;
     p.wn = 8;
     p.wk = 1;
     p.grid_x = (tn + 7) / 8;

@@ -170,6 +170,7 @@ def test_serving_step(T):
     (9, 33, 3584, 64), (9, 33, 3616, 32), (16, 40, 1920, 64), (16, 40, 2048, 128), (8, 17, 4064, 32), (8, 17, 4096, 64),
     (4, 70001, 128, 64), (13, 66000, 256, 32),    # several tiles of rows a wave
     (7, 13000, 1920, 64), (16, 12300, 1920, 128), (3, 12305, 2080, 32), (2, 12289, 96, 32), (5, 26000, 640, 128),  # waves that share K
+    (17, 100, 96, 32), (32, 1000, 2080, 32), (33, 70, 1920, 64), (64, 257, 1120, 32), (47, 4100, 640, 128),
     (16, 12288, 1920, 64), (1, 12288, 2560, 128), (1, 4096, 8192, 64), (12, 256, 8192, 128), (13, 256, 8192, 128),
     (2, 500, 20480, 64), (33, 16, 8192, 128), (64, 2050, 1920, 32), (200, 129, 512, 64)])
 @pytest.mark.parametrize("zero", [False, True])
@@ -182,7 +183,7 @@ def test_edges_of_the_forms(M, N, K, group, zero):
 
 def test_scratch_and_streams():
     """The caller's scratch, whatever it held; calls that overlap on two streams."""
-    M, N, K = 40, 300, 8192
+    M, N, K = 40, 300, 8192                       # K split over workgroups
     codes, scale, _ = R.w4_random(N, K, 64, False, 31)
     w = hdq.w4_pack(codes.to(DEV), scale.to(DEV))
     xs = [make((M, K), BF, 32 + i).to(DEV) for i in range(2)]

@@ -107,8 +107,10 @@ def test_w4(plans):
         assert 0 < gy < 1 << 16 and 0 < split < 1 << 16 and gx * 64 * wn * wk < 1 << 32, s
         assert m * n <= piece < m * n + 4
         if direct:
-            forms.add("direct")
-            assert m <= 16 and wn == 1 and wk == blocks <= 16 and gx == tn and gy == split == 1 and ws == 0 and per == 0, s
+            forms.add(("direct", mt))
+            tiles = 4 // mt                                                # of K, a wave's
+            assert m <= 16 * mt and wn == 1 and (wk - 1) * tiles < tk <= wk * tiles and wk <= 16, s
+            assert gx == tn and gy == split == 1 and ws == 0 and per == 0 and lds == wk * mt * 1024 <= 65536, s
         elif per:
             forms.add((per > 1, wk > 1, wn > 1))
             assert step * blocks + part == wn * wk and 0 <= part < blocks, s
@@ -130,4 +132,4 @@ def test_w4(plans):
         if m <= 16 and m * k <= 24576:                                     # what the binding takes to need no scratch
             assert ws == 0, s
     assert {(1, True), (1, False), (2, True), (2, False), (4, True), (4, False)} <= forms
-    assert "direct" in forms and {(False, True, False), (False, False, True), (True, False, True), (False, True, True)} <= forms
+    assert {("direct", 1), ("direct", 2), ("direct", 4)} <= forms and {(False, True, False), (False, False, True), (True, False, True), (False, True, True)} <= forms
