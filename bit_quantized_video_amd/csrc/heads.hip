@@ -10,7 +10,21 @@
 //            t = 2 pi frac(p * turns[j]), the product and its fraction in float64;
 //   cache    y = H_b x / sqrt(b) in blocks of b, code = rne(y * (top / a)) with
 //            a = max|y| of a group, scale a / top (top 127, 448 or 7).
-// Bound by HBM: every element is read and written once.
+// Bound by HBM: every element is read and written once.  Queries and keys of
+// 17776 tokens, 60 heads of 64, layer norm and rotation: 62 us, 4.4 TB/s (a copy
+// 4.9); rotation of 30 of them 27 us, 5.0 TB/s (part from the memory-side cache);
+// 4050 tokens of 90 heads, queries written back, keys and values to FP8 in
+// blocks of 64: 23 us, 3.4 TB/s (too short a launch to reach more: 2.6 rounds
+// of waves, each beginning with positions, angles and loads).  One token: 4.2
+// us, a chain of latencies (arguments, positions, angles, norm) of which an
+// empty launch is 1.5.
+//
+// Two forms: k_heads16 (heads16.h), 16 elements a lane, for heads of a multiple
+// of 16 in whole vectors, and k_heads here, 8 elements a lane, for the rest.
+// With one form of 8 elements the largest calls took 86 us (62) and 49 (23 to 32):
+// a step's addresses, lane sums and tests served half as many elements.
+// Rounding: everything is float32 until the output's type or the code; angles are
+// float64 up to the fraction of a turn.
 #include "heads_device.h"
 
 namespace hdq {

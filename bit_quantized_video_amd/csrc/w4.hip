@@ -10,6 +10,9 @@
 // second product with ones; without zero points from one with -24, in whose
 // registers the codes' product goes on.  Sums are float32: the difference costs
 // at most (31 + 31) / 8 times a float32 sum's rounding.
+// Measured: one token 512 -> 345600 with zero points 21.5 us, 4.5 TB/s of codes and
+// scales; 12288 -> 12288 17.5 us, 4.4 TB/s; 1920 -> 5760 4.2 us, 1.3 TB/s (an empty
+// launch is 1.5, the loads' latency another 1 to 1.5).
 #include "hdq_device.h"
 #include "hdq_internal.h"
 #include "w4.h"
@@ -234,7 +237,9 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
 // Few rows.  The workgroup has one tile of them, so it wants a fragment of the
 // tokens once and LDS would serve no second reader; with 4 / MT tiles of K for
 // each wave (16 fragments of the tokens, 64 registers) all its loads are in
-// flight at once.
+// flight at once.  One launch where k_w4_shared takes two.  13 x 4096 -> 1921 in
+// groups of 32 6.8 us (k_w4_shared 5.4 + 2.5), bound by the tokens' way from L2,
+// 106 KB a CU; 16 x 1920 -> 1920 4.7 (k_w4 6.8).
 template <int MT, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
   constexpr int TILES = 4 / MT;  // of K, a wave's
@@ -288,6 +293,18 @@ __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
 // rows fall on all banks.  Loads run two stages ahead in registers (memory
 // takes longer than a stage), none of them under a condition: the waits then
 // count the ones that may still be in flight.
+//
+// 64 x 12288 -> 4096: 15.2 to 16.8 us and 4 for the sums, 12 stages of 0.9 us and
+// about 5 to begin and end.  A stage's parts are 650 cycles of vector
+// instructions, 770 of matrix ones and 640 of LDS a SIMD or CU, of about 2000:
+// what is left is waiting between them.  Without zero points 64 tokens are
+// held to 128 registers, four waves a SIMD (300 x 1920 -> 5760 22.3 -> 19.2); with
+// them that spills (64 x 1920 -> 1920 9.5 -> 13.5).  Loads at the top of a stage
+// gain with one tile of tokens a wave (2 x 32768 -> 8192 37 -> 31) and cost
+// registers with two (64 x 1024 -> 65536 17.4 -> 20).  Not kept: two halves of K
+// in a workgroup of 16 waves (16.9 -> 16.2, shorter ones 5 to 10% slower), weights
+// four or six stages ahead (16.5 -> 16.8, 17.4), stages of 256 columns, DMA into
+// LDS (17).
 template <int MW, int MT, int NT, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(512, MT > 1 && !ZERO ? 4 : 2) void k_w4_shared(const W4Args g) {
   static_assert(NT * (8 / MW) == 8, "128 rows a workgroup");
