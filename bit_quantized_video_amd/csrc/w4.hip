@@ -294,19 +294,22 @@ __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
 // takes longer than a stage), none of them under a condition: the waits then
 // count the ones that may still be in flight.
 //
-// 64 x 12288 -> 4096: 15.2 to 16.8 us and 4 for the sums, 12 stages of 0.9 us and
+// 64 x 12288 -> 4096: 15.5 to 16.3 us and 4 for the sums, 12 stages of 0.9 us and
 // about 5 to begin and end.  A stage's parts are 650 cycles of vector
 // instructions, 770 of matrix ones and 640 of LDS a SIMD or CU, of about 2000:
-// what is left is waiting between them.  Without zero points 64 tokens are
-// held to 128 registers, four waves a SIMD (300 x 1920 -> 5760 22.3 -> 19.2); with
-// them that spills (64 x 1920 -> 1920 9.5 -> 13.5).  Loads at the top of a stage
+// what is left is waiting between them.  SIMD: waves a SIMD that the
+// registers leave room for.  Four (128 registers, a few of them spilled) are
+// faster for 64 tokens without zero points where a CU has a second workgroup to run
+// (2000 x 1920 -> 5760 95 -> 80, 64 x 1024 -> 65536 18.8 -> 17.8) and slower where not
+// (64 x 12288 -> 4096 15.9 -> 16.9); with zero points too much spills (64 x 1920 ->
+// 1920 9.5 -> 13.5).  Loads at the top of a stage
 // gain with one tile of tokens a wave (2 x 32768 -> 8192 37 -> 31) and cost
 // registers with two (64 x 1024 -> 65536 17.4 -> 20).  Not kept: two halves of K
 // in a workgroup of 16 waves (16.9 -> 16.2, shorter ones 5 to 10% slower), weights
 // four or six stages ahead (16.5 -> 16.8, 17.4), stages of 256 columns, DMA into
 // LDS (17).
-template <int MW, int MT, int NT, int GROUPS, bool ZERO, bool F32>
-__global__ __launch_bounds__(512, MT > 1 && !ZERO ? 4 : 2) void k_w4_shared(const W4Args g) {
+template <int MW, int MT, int NT, int SIMD, int GROUPS, bool ZERO, bool F32>
+__global__ __launch_bounds__(512, SIMD) void k_w4_shared(const W4Args g) {
   static_assert(NT * (8 / MW) == 8, "128 rows a workgroup");
   constexpr int TILES = MT * MW;            // of 16 tokens
   constexpr int PIECES = (TILES + 1) / 2;   // of the tokens a thread brings
@@ -550,12 +553,14 @@ void run(const W4Args& a, const W4Plan& p, hipStream_t s) {
     k_w4_direct<2, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
   else if (p.direct)
     k_w4_direct<4, GROUPS, ZERO, F32><<<grid, block, p.lds, s>>>(a);
+  else if (p.mt == 4 && !ZERO && p.grid_x * p.grid_y * p.split > kW4Groups)
+    k_w4_shared<2, 2, 2, ZERO ? 2 : 4, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 4)
-    k_w4_shared<2, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<2, 2, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else if (p.mt == 2)
-    k_w4_shared<2, 1, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<2, 1, 2, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
   else
-    k_w4_shared<1, 1, 1, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
+    k_w4_shared<1, 1, 1, 2, GROUPS, ZERO, F32><<<grid, block, 0, s>>>(a);
 }
 
 template <bool F32>

@@ -172,6 +172,7 @@ def test_serving_step(T):
     (7, 13000, 1920, 64), (16, 12300, 1920, 128), (3, 12305, 2080, 32), (2, 12289, 96, 32), (5, 26000, 640, 128),  # waves that share K
     (17, 100, 96, 32), (32, 1000, 2080, 32), (33, 70, 1920, 64), (64, 257, 1120, 32), (47, 4100, 640, 128),
     (16, 12288, 1920, 64), (1, 12288, 2560, 128), (1, 4096, 8192, 64), (12, 256, 8192, 128), (13, 256, 8192, 128),
+    (200, 12289, 160, 32), (70, 33000, 64, 64),   # more than a workgroup a CU
     (2, 500, 20480, 64), (33, 16, 8192, 128), (64, 2050, 1920, 32), (200, 129, 512, 64)])
 @pytest.mark.parametrize("zero", [False, True])
 def test_edges_of_the_forms(M, N, K, group, zero):
