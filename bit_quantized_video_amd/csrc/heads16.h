@@ -21,8 +21,6 @@
 namespace hdq {
 
 enum Rotation : int { kRotateNone = 0, kRotateSplit = 1, kRotatePairs = 2 };
-// The cache's Hadamard blocks: none, whole heads of 8 << (LL + 1) elements, or g.hb.
-enum Hadamard : int { kHadamardNone = 0, kHadamardWhole = 1, kHadamardAny = 2 };
 
 namespace {
 

@@ -3,8 +3,8 @@
 // rotation is its own inverse).  Bound by HBM: the codes and scales read
 // once, the elements written once.  17550 tokens of 30 heads of 64 from INT8 to
 // bf16 38 us, 5.5 TB/s (the codes partly from the memory-side cache; a copy
-// 4.9); 5400 tokens from INT4, rotated back, 14.5 us, 3.7 TB/s: 647 vector
-// instructions a wave, half of them the rotation, beside a short launch.
+// 4.9); 5400 tokens from INT4, rotated back, 13.4 us, 4.0 TB/s, a short launch with the
+// rotation's vector instructions beside it.
 #include "heads.h"
 
 namespace hdq {
@@ -54,12 +54,17 @@ __device__ __forceinline__ void store8(void* y, bool f32, int64_t at, const floa
 // A layer of the grid takes `steps` steps of the keys' heads, or of the
 // values'.  A lane holds one chunk of a head, or (PAIRS) chunks c and
 // c + dim / 16, as the kernels that write the cache; LL: log2 of a head's
-// lanes, or -1 for g.lane_bits.
-template <int FMT, int LL, bool PAIRS>
+// lanes, or -1 for g.lane_bits.  A Hadamard block of the whole head is a template
+// argument: under its conditions the compiler moved the elements between
+// registers (5400 tokens from INT4 14.6 -> 13.4 us, of 24 heads of 128 18.5 -> 17.4);
+// for blocks of 1 that gained nothing (17550 tokens from INT8 38.7 -> 41).
+template <int FMT, int LL, bool PAIRS, int HADAMARD>
 __global__ __launch_bounds__(64 * kWaves) void k_cache_read(const CacheReadArgs g) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ll = LL < 0 ? g.lane_bits : LL, sl = g.slot_bits;
-  const int far = PAIRS ? g.dim >> 4 : 0, hb1 = PAIRS ? min(g.hb, g.dim >> 1) : g.hb;
+  const int far = PAIRS ? g.dim >> 4 : 0;
+  const int hb = HADAMARD == kHadamardWhole ? 16 << LL : g.hb;
+  const int hb1 = HADAMARD == kHadamardWhole ? hb / 2 : PAIRS ? min(hb, g.dim >> 1) : hb;
   const int c = (int)fwht_src(lane & ((1 << ll) - 1), lane, hb1);
   const int hslot = (lane >> ll) & ((1 << sl) - 1);
   const int64_t group0 = ((int64_t)wide_block() * kWaves + wave) * (64 >> (ll + sl)), token = group0 + (lane >> (ll + sl));
@@ -100,11 +105,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_read(const CacheReadArgs 
     float x[8], w[8];
     v.a.to_f32(v.scale, x);
     if (PAIRS) v.b.to_f32(v.scale2, w);
-    if (g.hb > 1) {
+    if (hb > 1) {
       const float sc = fwht8(x, lane, hb1) * g.c_b;
       if (PAIRS) {
         fwht8(w, lane, hb1);
-        if (g.hb != hb1) {  // the last stage, half a head apart
+        if (hb != hb1) {  // the last stage, half a head apart
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float a = x[e], b = w[e];
@@ -143,17 +148,25 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_read(const CacheReadArgs 
   }
 }
 
+template <int FMT, int LL>
+void run_dim(const CacheReadArgs& g, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kWaves);
+  if (g.hb == g.dim)
+    k_cache_read<FMT, LL, true, kHadamardWhole><<<grid, block, 0, s>>>(g);
+  else
+    k_cache_read<FMT, LL, true, kHadamardAny><<<grid, block, 0, s>>>(g);
+}
+
 template <int FMT>
 void run(const CacheReadArgs& g, bool pairs, dim3 grid, hipStream_t s) {
-  const dim3 block(64 * kWaves);
   if (!pairs)
-    k_cache_read<FMT, -1, false><<<grid, block, 0, s>>>(g);
+    k_cache_read<FMT, -1, false, kHadamardAny><<<grid, dim3(64 * kWaves), 0, s>>>(g);
   else if (g.dim == 64)
-    k_cache_read<FMT, 2, true><<<grid, block, 0, s>>>(g);
+    run_dim<FMT, 2>(g, grid, s);
   else if (g.dim == 128)
-    k_cache_read<FMT, 3, true><<<grid, block, 0, s>>>(g);
+    run_dim<FMT, 3>(g, grid, s);
   else
-    k_cache_read<FMT, -1, true><<<grid, block, 0, s>>>(g);
+    k_cache_read<FMT, -1, true, kHadamardAny><<<grid, dim3(64 * kWaves), 0, s>>>(g);
 }
 
 }  // namespace
