@@ -12,6 +12,8 @@ enum HeadNorm : int { kHeadNormNone = 0, kHeadNormLayer = 1, kHeadNormRms = 2 };
 enum CacheFmt : int { kCacheInt8 = 0, kCacheFp8 = 1, kCacheInt4 = 2 };
 // The cache's Hadamard blocks, of kernels for heads of 16 << LL elements: none, whole heads, or g.hb.
 enum Hadamard : int { kHadamardNone = 0, kHadamardWhole = 1, kHadamardAny = 2 };
+// Its groups: a head each, within half a head, or g.group.
+enum Group : int { kGroupHead = 0, kGroupPart = 1, kGroupAny = 2 };
 
 // One of a call's tensors: [batch, length, heads, dim] elements, strides in elements.
 struct HeadRows {

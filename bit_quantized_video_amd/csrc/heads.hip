@@ -14,14 +14,14 @@
 // 17776 tokens, 60 heads of 64, layer norm and rotation: 62 us, 4.4 TB/s (a copy
 // 4.9); rotation of 30 of them 27 us, 5.0 TB/s (part from the memory-side cache);
 // 4050 tokens of 90 heads, queries written back, keys and values to FP8 in
-// blocks of 64: 23 us, 3.4 TB/s (too short a launch to reach more: 2.6 rounds
-// of waves, each beginning with positions, angles and loads).  One token: 4.2
-// us, a chain of latencies (arguments, positions, angles, norm) of which an
-// empty launch is 1.5.
+// blocks of 64: 20 us, 3.9 TB/s (a short launch: 2.6 rounds of waves, each
+// beginning with positions, angles and loads, a thousand vector instructions
+// each).  One token: 4 us, a chain of latencies (arguments, positions, angles,
+// norm) of which an empty launch is 1.5.
 //
 // Two forms: k_heads16 (heads16.h), 16 elements a lane, for heads of a multiple
 // of 16 in whole vectors, and k_heads here, 8 elements a lane, for the rest.
-// With one form of 8 elements the largest calls took 86 us (62) and 49 (23 to 32):
+// With one form of 8 elements the largest calls took 86 us (62) and 49 (32 then, 20 now):
 // a step's addresses, lane sums and tests served half as many elements.
 // Rounding: everything is float32 until the output's type or the code; angles are
 // float64 up to the fraction of a turn.

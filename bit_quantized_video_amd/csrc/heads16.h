@@ -2,10 +2,11 @@
 //
 // A lane holds chunks c and c + dim / 16 of a head, so both elements of a pair,
 // in either layout, are its own, and a step's addresses, reductions and tests
-// serve twice the elements.  Norm and rotation are the kernel's template
-// arguments and the values' waves a path of their own, so that a step is
-// straight code: under conditions the compiler moved every element between
-// registers.  Conditions: dim a multiple of 16, vectors throughout, the
+// serve twice the elements.  Norm, rotation and the cache's blocks and groups
+// are the kernel's template arguments and the values' waves a path of their own,
+// so that a step is straight code: under conditions the compiler moved every
+// element between registers (4050 tokens of 90 heads into the cache 32 -> 26 us
+// without those of norm and rotation, 23 of the blocks, 20 of the groups).  Conditions: dim a multiple of 16, vectors throughout, the
 // rotation none, interleaved in whole chunks or split over the whole head, a
 // Hadamard block and a group within half a head or the whole.
 //
@@ -25,7 +26,7 @@ enum Rotation : int { kRotateNone = 0, kRotateSplit = 1, kRotatePairs = 2 };
 namespace {
 
 // LL: log2 of a head's lanes, or -1 for g.lane_bits.
-template <bool F32, int LL, bool CACHE, bool NORM, int ROTATE, int HADAMARD>
+template <bool F32, int LL, bool CACHE, bool NORM, int ROTATE, int HADAMARD, int GROUP>
 __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   __shared__ __align__(16) float2 s_trig[kWaves][ROTATE != kRotateNone ? 2 * kMaxPairs : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
   // cache: the token's slot, the groups of the lane's chunks, and whether the lane is their first
   const int64_t slot = CACHE && in ? g.slots[token] : -1;
   const bool in_cache = slot >= 0 && slot < g.n_slots;
-  const bool whole = g.group == g.dim;
+  const bool whole = GROUP == kGroupAny ? g.group == g.dim : GROUP == kGroupHead;
   const int group1 = CACHE && !whole ? c * 8 / g.group : 0, group2 = CACHE && !whole ? (c + far) * 8 / g.group : 0;
   const bool heads_group = CACHE && (whole ? c == 0 : group1 * g.group == c * 8);
 
@@ -252,38 +253,46 @@ __global__ __launch_bounds__(64 * kWaves) void k_heads16(const HeadArgs g) {
     walk(std::false_type());
 }
 
-template <bool F32, int LL, bool CACHE, bool NORM, int HADAMARD>
+template <bool F32, int LL, bool CACHE, bool NORM, int HADAMARD, int GROUP>
 void run16_rotate(const HeadArgs& g, int rotate, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kWaves);
   if (rotate == kRotateNone)
-    k_heads16<F32, LL, CACHE, NORM, kRotateNone, HADAMARD><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotateNone, HADAMARD, GROUP><<<grid, block, 0, s>>>(g);
   else if (rotate == kRotateSplit)
-    k_heads16<F32, LL, CACHE, NORM, kRotateSplit, HADAMARD><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotateSplit, HADAMARD, GROUP><<<grid, block, 0, s>>>(g);
   else
-    k_heads16<F32, LL, CACHE, NORM, kRotatePairs, HADAMARD><<<grid, block, 0, s>>>(g);
+    k_heads16<F32, LL, CACHE, NORM, kRotatePairs, HADAMARD, GROUP><<<grid, block, 0, s>>>(g);
 }
 
-template <bool F32, int LL, bool CACHE, int HADAMARD>
+template <bool F32, int LL, bool CACHE, int HADAMARD, int GROUP>
 void run16_norm(const HeadArgs& g, dim3 grid, hipStream_t s) {
   const int rotate = g.half == 0 ? kRotateNone : g.split ? kRotateSplit : kRotatePairs;
   if (g.norm != kHeadNormNone)
-    run16_rotate<F32, LL, CACHE, true, HADAMARD>(g, rotate, grid, s);
+    run16_rotate<F32, LL, CACHE, true, HADAMARD, GROUP>(g, rotate, grid, s);
   else
-    run16_rotate<F32, LL, CACHE, false, HADAMARD>(g, rotate, grid, s);
+    run16_rotate<F32, LL, CACHE, false, HADAMARD, GROUP>(g, rotate, grid, s);
+}
+
+template <bool F32, int LL, bool CACHE, int HADAMARD>
+void run16_group(const HeadArgs& g, dim3 grid, hipStream_t s) {
+  if (g.group == g.dim)
+    run16_norm<F32, LL, CACHE, HADAMARD, kGroupHead>(g, grid, s);
+  else
+    run16_norm<F32, LL, CACHE, HADAMARD, kGroupPart>(g, grid, s);
 }
 
 template <bool F32, int LL, bool CACHE>
 void run16(const HeadArgs& g, dim3 grid, hipStream_t s) {
   if constexpr (!CACHE)
-    run16_norm<F32, LL, CACHE, kHadamardNone>(g, grid, s);
+    run16_norm<F32, LL, CACHE, kHadamardNone, kGroupHead>(g, grid, s);
   else if constexpr (LL < 0)
-    run16_norm<F32, LL, CACHE, kHadamardAny>(g, grid, s);
+    run16_norm<F32, LL, CACHE, kHadamardAny, kGroupAny>(g, grid, s);
   else if (g.hb == 1)
-    run16_norm<F32, LL, CACHE, kHadamardNone>(g, grid, s);
+    run16_group<F32, LL, CACHE, kHadamardNone>(g, grid, s);
   else if (g.hb == g.dim)
-    run16_norm<F32, LL, CACHE, kHadamardWhole>(g, grid, s);
+    run16_group<F32, LL, CACHE, kHadamardWhole>(g, grid, s);
   else
-    run16_norm<F32, LL, CACHE, kHadamardAny>(g, grid, s);
+    run16_group<F32, LL, CACHE, kHadamardAny>(g, grid, s);
 }
 
 }  // namespace
