@@ -14,7 +14,7 @@
 // 17776 tokens, 60 heads of 64, layer norm and rotation: 62 us, 4.4 TB/s (a copy
 // 4.9); rotation of 30 of them 27 us, 5.0 TB/s (part from the memory-side cache);
 // 4050 tokens of 90 heads, queries written back, keys and values to FP8 in
-// blocks of 64: 20 us, 3.9 TB/s (a short launch: 2.6 rounds of waves, each
+// blocks of 64: 20 us, 3.9 TB/s (a short launch: two rounds of waves, each
 // beginning with positions, angles and loads, a thousand vector instructions
 // each).  One token: 4 us, a chain of latencies (arguments, positions, angles,
 // norm) of which an empty launch is 1.5.

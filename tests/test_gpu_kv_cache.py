@@ -27,7 +27,7 @@ def filled(slots, heads, dim, fmt, group, had, seed):
 
 
 SHAPES = [(64, 64, 64), (64, 16, 1), (128, 32, 128), (128, 128, 16), (96, 96, 32), (96, 32, 8), (72, 72, 8), (256, 64, 128),
-          (512, 512, 128), (8, 8, 8), (40, 8, 1), (320, 64, 64), (80, 80, 1)]
+          (512, 512, 128), (64, 64, 1), (128, 128, 128), (64, 32, 16), (128, 64, 1), (64, 64, 16), (8, 8, 8), (40, 8, 1), (320, 64, 64), (80, 80, 1)]
 
 
 @pytest.mark.parametrize("dim,group,had", SHAPES)
