@@ -116,11 +116,13 @@ __device__ __forceinline__ int norm_exponent(float m, float eps) {
 // Whether a sum of squares is one that float32 holds well.
 __device__ __forceinline__ bool squares_hold(float ss, float eps) { return ss < 0x1p100f && (ss > 0x1p-80f || eps > 0x1p-60f); }
 
-// 1 / sqrt(mean square + eps); sums outside that range come scaled, so the
-// argument is normal (or 0: a head of zeros stays zero at eps 0).
+// 1 / sqrt(mean square + eps), a step past the instruction's accuracy (1 unit);
+// sums outside that range come scaled, so the argument is normal (or 0: a head
+// of zeros stays zero at eps 0).
 __device__ __forceinline__ float norm_scale(float ss, float inv_dim, float eps) {
   const float d = fmaf(ss, inv_dim, eps);
-  return d == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(d);
+  const float r = __builtin_amdgcn_rsqf(d);
+  return d == 0.0f ? 0.0f : fmaf(0.5f * r, fmaf(-(d * r), r, 1.0f), r);
 }
 
 // A head's scale and its centred values in place.  Sums that do not hold
@@ -163,10 +165,13 @@ __device__ __forceinline__ float2 pair_angle(const HeadArgs& g, int64_t p0, int6
   const double p = (double)(j < g.axis_end[0] ? p0 : j < g.axis_end[1] ? p1 : p2);
   const double f = g.turns[j];
   const double t = p * f, lost = fma(p, f, -t);  // the product in two parts
-  const float r = (float)((t - rint(t)) + lost);
+  // the fraction in two floats, the second in first order: rounded to one, it alone
+  // would be half of a rotated element's error
+  const double part = (t - rint(t)) + lost;
+  const float r = (float)part, rest = 6.2831853f * (float)(part - (double)r);
   float s, co;
   sincospif(2.0f * r, &s, &co);
-  return make_float2(co * g.scale, s * g.scale);
+  return make_float2(fmaf(-rest, s, co) * g.scale, fmaf(rest, co, s) * g.scale);
 }
 
 // A token's sequence and place in it; one past the last stands in the first.
