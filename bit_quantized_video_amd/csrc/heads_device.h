@@ -97,24 +97,36 @@ __device__ __forceinline__ float squares8(const float (&x)[8]) {
   return a + b;
 }
 
-// Centres the lane's n elements (layer) and returns the head's sum of squares.
-__device__ __forceinline__ float centred_squares(float (&x)[8], int n, bool layer, float inv_dim, int ll) {
-  if (layer) {
-    const float mean = lanes_sum(sum8(x), ll) * inv_dim;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] - mean : 0.0f;
-  }
-  return lanes_sum(squares8(x), ll);
-}
-
 // The power of two that brings a head of largest magnitude m, and eps with it, near 1.
 __device__ __forceinline__ int norm_exponent(float m, float eps) {
   const float big = fmaxf(m, sqrtf(eps));
   return big > 0.0f && big < __builtin_inff() ? ilogbf(big) + 1 : 0;
 }
 
-// Whether a sum of squares is one that float32 holds well.
-__device__ __forceinline__ bool squares_hold(float ss, float eps) { return ss < 0x1p100f && (ss > 0x1p-80f || eps > 0x1p-60f); }
+// Whether a sum of squares about `mean` is one that float32 holds well.  The mean's
+// error goes with the head's elements, so it has to lie within a deviation of 0:
+// heads further off (a constant one is, however small) are taken again.
+__device__ __forceinline__ bool squares_hold(float ss, float mean, float inv_dim, float eps) {
+  return ss < 0x1p100f && (ss > 0x1p-80f || eps > 0x1p-60f) && mean * mean <= ss * inv_dim;
+}
+
+// v of the first of the 2^bits lanes that hold a head (swizzles, which need no
+// register for an address).
+template <int BITS>
+__device__ __forceinline__ float first_of(float v) {
+  return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x1F & ~((1 << BITS) - 1)));
+}
+__device__ __forceinline__ float lanes_first(float v, int bits) {
+  switch (bits) {
+    case 0: return v;
+    case 1: return first_of<1>(v);
+    case 2: return first_of<2>(v);
+    case 3: return first_of<3>(v);
+    case 4: return first_of<4>(v);
+    case 5: return first_of<5>(v);
+    default: return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+  }
+}
 
 // 1 / sqrt(mean square + eps), a step past the instruction's accuracy (1 unit);
 // sums outside that range come scaled, so the argument is normal (or 0: a head
@@ -127,12 +139,24 @@ __device__ __forceinline__ float norm_scale(float ss, float inv_dim, float eps) 
 
 // A head's scale and its centred values in place.  Sums that do not hold
 // are taken again from values scaled by a power of two, which cancels in the
-// result; a head with a NaN or an infinity becomes NaN.
+// result, and about a mean in two steps: an element and the mean difference from
+// it (of a constant head 0), then the mean of what is left.  A head with a NaN or
+// an infinity becomes NaN.
 template <bool F32>
 __device__ __forceinline__ float head_norm(const Chunk<F32>& raw, float (&x)[8], int n, bool layer, float inv_dim,
                                            float eps, int ll) {
-  float ss = centred_squares(x, n, layer, inv_dim, ll);
-  const bool ok = squares_hold(ss, eps);
+  // the lane's n elements of v less c
+  auto less = [&](float (&v)[8], float c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] - c : 0.0f;
+  };
+  float mean = 0.0f;
+  if (layer) {
+    mean = lanes_sum(sum8(x), ll) * inv_dim;
+    less(x, mean);
+  }
+  float ss = lanes_sum(squares8(x), ll);
+  const bool ok = squares_hold(ss, mean, inv_dim, eps);
   if (__ballot(!ok) != 0) {
     float v[8], m = 0.0f;
     raw.to_f32(v);
@@ -142,7 +166,16 @@ __device__ __forceinline__ float head_norm(const Chunk<F32>& raw, float (&x)[8],
     const int k = norm_exponent(m, eps);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
-    const float again = centred_squares(v, n, layer, inv_dim, ll);
+    if (layer) {
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = v[e];
+      const float first = lanes_first(v[0], ll);
+      less(d, first);
+      less(v, first + lanes_sum(sum8(d), ll) * inv_dim);
+      less(v, lanes_sum(sum8(v), ll) * inv_dim);
+    }
+    const float again = lanes_sum(squares8(v), ll);
     if (!ok) {
       ss = again;
       eps = m < __builtin_inff() ? ldexpf(ldexpf(eps, -k), -k) : __builtin_nanf("");

@@ -736,8 +736,10 @@ typedef struct hdq_heads {
  * weight, bias: device fp32 [dim], or NULL for 1 and 0.  eps 0 to 1e30; a
  * head of zeros stays zero at eps 0.  Finite heads of any size are normed
  * (sums that leave float32's range are taken again, scaled); a NaN or an
- * infinity makes its head NaN.  A layer norm's deviations are those from the
- * mean rounded to float32. */
+ * infinity makes its head NaN.  A layer norm's mean is within a few float32
+ * roundings of the head's deviations, however far from 0 its elements are: a head
+ * further off than its deviation is taken again, about one of its elements, and
+ * a constant one gives the biases. */
 #define HDQ_HEAD_NORM_NONE 0
 #define HDQ_HEAD_NORM_LAYER 1
 #define HDQ_HEAD_NORM_RMS 2
