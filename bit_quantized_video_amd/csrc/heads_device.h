@@ -128,13 +128,14 @@ __device__ __forceinline__ float lanes_first(float v, int bits) {
   }
 }
 
-// 1 / sqrt(mean square + eps), a step past the instruction's accuracy (1 unit);
-// sums outside that range come scaled, so the argument is normal (or 0: a head
-// of zeros stays zero at eps 0).
+// 1 / sqrt(mean square + eps), a step past the instruction's accuracy (1 unit).
+// Sums outside squares_hold's range come scaled, with a largest element near 1, so
+// the argument is normal but for a head without deviations, whose eps may be 0, or
+// subnormal once scaled, which the instruction takes for 0: 0 for that one.
 __device__ __forceinline__ float norm_scale(float ss, float inv_dim, float eps) {
   const float d = fmaf(ss, inv_dim, eps);
   const float r = __builtin_amdgcn_rsqf(d);
-  return d == 0.0f ? 0.0f : fmaf(0.5f * r, fmaf(-(d * r), r, 1.0f), r);
+  return d < 0x1p-126f ? 0.0f : fmaf(0.5f * r, fmaf(-(d * r), r, 1.0f), r);
 }
 
 // A head's scale and its centred values in place.  Sums that do not hold

@@ -95,3 +95,26 @@ def test_constant_keys_into_the_cache(D, dtype):
     top = b.abs().max()
     assert torch.equal(c.k_scale.cpu(), (top / 127).expand(12, 3, 1))
     assert torch.equal(c.k_codes.view(torch.int8).cpu(), torch.round(b * (127 / top)).to(torch.int8).expand(12, 3, D))
+
+
+@pytest.mark.parametrize("D", [64, 80, 72, 21])
+@pytest.mark.parametrize("eps", [1e-38, 1e-30, 1e-20, 1e30])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_eps_next_to_a_heads_size(D, eps, kind):
+    """Finite heads with an eps far below their squares (whose scaled value leaves
+    float32's normals) or far above them: heads without deviations give the
+    biases, the others what the formula gives."""
+    g = torch.Generator().manual_seed(D + 5)
+    sizes = torch.tensor([3e38, 1e30, 1e10, 1.0, 1e-10, 1e-18])
+    x = torch.randn(1, 6, 4, D, generator=g).clamp(-1, 1) * sizes.view(1, 6, 1, 1)
+    x[:, :, 1] = sizes.view(1, 6, 1)
+    x[:, :, 2] = 0
+    b = torch.randn(D, generator=g)
+    y = hdq.qk_norm_rope(x.to(DEV), norm=KIND[kind], q_bias=b.to(DEV), eps=eps).cpu()
+    x64, e64 = x.double(), float(torch.tensor(eps))
+    d = x64 - x64.mean(-1, keepdim=True) if kind == "layer" else x64
+    d[:, :, 1] = 0 if kind == "layer" else d[:, :, 1]     # float64's own rounding of a constant head's mean
+    ref = d / torch.sqrt(d.square().mean(-1, keepdim=True) + e64)
+    # a float32 norm of 32 u (see test_offset_heads) and the sum with the bias
+    assert bool(((y.double() - (ref + b)).abs() <= 32 * U * (1 + ref.abs()) + U * (ref + b).abs()).all())
+    assert torch.equal(y[0, :, 2], b.expand(6, D))
