@@ -250,12 +250,14 @@ __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
   const int64_t tn = blockIdx.x;
   const int64_t group = tn * ((tiles_k + 3) >> 2) * (64 * GROUPS) + (k0 >> 2) * (64 * GROUPS) + (k0 & 3) * GROUPS;
   const uint8_t* codes = g.codes + (tn * tiles_k + k0) * 1024;
-  // rows of tokens that are not there repeat the first's, and are not stored; columns past the last read zeros
-  const uint32_t bytes = (uint32_t)(g.M * g.K * 2), k_bytes = (uint32_t)(g.K * 2);
+  // rows of tokens that are not there repeat the first's, and are not stored; columns past the last read zeros.
+  // All of an offset is the lane's and the instruction's: a scalar one may lie past the end of a single short
+  // token, and the range check takes it off the size.
+  const uint32_t bytes = (uint32_t)(g.M * g.K * 2), k_bytes = (uint32_t)(g.K * 2), lane0 = k0 * 256 + quad * 16;
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x, bytes);
   uint32_t from[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) from[m] = (16 * m + col < g.M ? 16 * m + col : 0) * k_bytes + quad * 16;
+  for (int m = 0; m < MT; ++m) from[m] = (16 * m + col < g.M ? 16 * m + col : 0) * k_bytes + lane0;
   v4u w[TILES][1];
   Groups<TILES * GROUPS, ZERO> of[1];
   uint4 x[TILES * 4][MT];
@@ -265,9 +267,9 @@ __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
     if (k0 + j < tiles_k) w[j][0] = reinterpret_cast<const v4u*>(codes + j * 1024)[lane];
 #pragma unroll
   for (int i = 0; i < TILES * 4; ++i) {
-    const uint32_t at = k0 * 256 + i * 64;  // bytes of a token before the fragment
+    const bool in = lane0 + i * 64 < k_bytes;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x[i][m] = buf_load16(xr, at + quad * 16 < k_bytes ? from[m] : bytes, at);
+    for (int m = 0; m < MT; ++m) x[i][m] = buf_load16(xr, (in ? from[m] : bytes) + i * 64, 0);
   }
   float y[1][MT][4] = {};
 #pragma unroll
