@@ -7,6 +7,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace {
 
 using namespace hdq;
@@ -32,6 +34,19 @@ bool valid_dtype(int32_t t) { return t == HDQ_DTYPE_F32 || t == HDQ_DTYPE_BF16; 
 // Strides past this cannot be those of device memory.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
+// Whether a view's heads lie apart: strides in order, each at least what the smaller ones span.
+bool apart(const hdq_heads& h, int64_t batch, int64_t length, int32_t dim) {
+  struct { int64_t stride, n; } d[3] = {{h.batch_stride, batch}, {h.token_stride, length}, {h.head_stride, h.heads}};
+  std::sort(d, d + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+  __int128 span = dim;
+  for (const auto& v : d) {
+    if (v.n == 1) continue;
+    if (v.stride < span) return false;
+    span += (__int128)(v.n - 1) * v.stride;
+  }
+  return true;
+}
+
 // A view's own checks; `out`: no two of its elements may be one.
 int check_heads(const hdq_heads& h, int64_t batch, int64_t length, int32_t dim, bool out) {
   if (h.data == nullptr) return HDQ_ERR_INVALID;
@@ -40,10 +55,14 @@ int check_heads(const hdq_heads& h, int64_t batch, int64_t length, int32_t dim, 
   if (!aligned(h.data, h.dtype == HDQ_DTYPE_F32 ? 4 : 2)) return HDQ_ERR_SHAPE;
   for (const int64_t s : {h.batch_stride, h.token_stride, h.head_stride})
     if (s < 0 || s > kMaxStride) return HDQ_ERR_SHAPE;
-  if (out && ((batch > 1 && h.batch_stride < dim) || (length > 1 && h.token_stride < dim) ||
-              (h.heads > 1 && h.head_stride < dim)))
-    return HDQ_ERR_SHAPE;
-  return HDQ_OK;
+  return out && !apart(h, batch, length, dim) ? HDQ_ERR_SHAPE : HDQ_OK;
+}
+
+// An output at its own input has the input's type and strides.
+bool in_place_ok(const hdq_heads& in, const hdq_heads& out, int64_t batch, int64_t length) {
+  return in.data != out.data || (in.dtype == out.dtype && (batch == 1 || in.batch_stride == out.batch_stride) &&
+                                 (length == 1 || in.token_stride == out.token_stride) &&
+                                 (in.heads == 1 || in.head_stride == out.head_stride));
 }
 
 // Whether the view's chunks of 8 elements are whole 16-byte words.
@@ -224,7 +243,10 @@ int hdq_qk_norm_rope(const hdq_heads* q, const hdq_heads* k, int64_t batch, int6
   if (k != nullptr) {
     if (k->dtype != q->dtype || k_out->dtype != q_out->dtype) return HDQ_ERR_UNSUPPORTED;
     if (k_out->heads != k->heads || k->heads > HDQ_HEAD_MAX_HEADS - q->heads) return HDQ_ERR_SHAPE;
+    if (!in_place_ok(*k, *k_out, batch, length)) return HDQ_ERR_SHAPE;
+    if (q_out->data == k->data || k_out->data == q->data || q_out->data == k_out->data) return HDQ_ERR_INVALID;
   }
+  if (!in_place_ok(*q, *q_out, batch, length)) return HDQ_ERR_SHAPE;
   HeadArgs g{};
   g.q = rows(q, q_out, norm ? norm->q_weight : nullptr, norm ? norm->q_bias : nullptr);
   g.k = rows(k, k_out, norm ? norm->k_weight : nullptr, norm ? norm->k_bias : nullptr);
@@ -258,7 +280,11 @@ int hdq_qkv_to_cache(const hdq_heads* q, const hdq_heads* k, const hdq_heads* v,
   }
   if (k->heads != cache->heads || v->heads != cache->heads) return HDQ_ERR_SHAPE;
   if (v->dtype != k->dtype || (q != nullptr && q->dtype != k->dtype)) return HDQ_ERR_UNSUPPORTED;
-  if (q != nullptr && (q_out->heads != q->heads || q->heads > HDQ_HEAD_MAX_HEADS - 2 * k->heads)) return HDQ_ERR_SHAPE;
+  if (q != nullptr) {
+    if (q_out->heads != q->heads || q->heads > HDQ_HEAD_MAX_HEADS - 2 * k->heads) return HDQ_ERR_SHAPE;
+    if (!in_place_ok(*q, *q_out, batch, length)) return HDQ_ERR_SHAPE;
+    if (q_out->data == k->data || q_out->data == v->data) return HDQ_ERR_INVALID;
+  }
   HeadArgs g{};
   g.q = rows(q, q_out, norm ? norm->q_weight : nullptr, norm ? norm->q_bias : nullptr);
   g.k = rows(k, nullptr, norm ? norm->k_weight : nullptr, norm ? norm->k_bias : nullptr);

@@ -719,15 +719,18 @@ size_t hdq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * strides of whole 16 bytes, and dim a multiple of 8, are the fast ones.
  * batch * length is 0 (nothing is done) to HDQ_FP8_MAX_ROWS, heads of a call
  * together at most HDQ_HEAD_MAX_HEADS.  An output may be its own input (same
- * type and strides); otherwise nothing written may overlap anything read. */
+ * type and strides); otherwise nothing written may overlap anything read or
+ * written.  An output's heads lie apart: of its dimensions longer than 1, each
+ * stride is at least what the smaller ones span.  Views that break this by
+ * their own strides or begin at one address are refused. */
 #define HDQ_HEAD_MAX_DIM 512
 #define HDQ_HEAD_MAX_HEADS (1 << 20)
 typedef struct hdq_heads {
   void *data;           /* device                                          */
   int32_t dtype;        /* HDQ_DTYPE_BF16 or HDQ_DTYPE_F32                 */
   int32_t heads;
-  int64_t batch_stride; /* in elements, >= 0; of an output that has more   */
-  int64_t token_stride; /* than one element along it, >= dim               */
+  int64_t batch_stride; /* in elements, >= 0                               */
+  int64_t token_stride;
   int64_t head_stride;
 } hdq_heads;
 
