@@ -1017,11 +1017,13 @@ def _head_norm(kind, eps, dim, dev, qw, qb, kw, kb):
 def _out_heads(out, x, shape, y_dtype, name, dev):
     """(out or a new contiguous tensor of y_dtype (None: x's), its hdq_heads)."""
     B, T, H, D = shape
+    dtype = x.dtype if y_dtype is None else _F32 if y_dtype == DTYPE_F32 else _BF16 if y_dtype == DTYPE_BF16 else None
+    if dtype is None or (out is not None and y_dtype is not None and out.dtype is not dtype):
+        raise ValueError(f"{name}: y_dtype {y_dtype}" + ("" if out is None else f" for a tensor of {out.dtype}"))
     if out is not None:
         if out.shape != x.shape:
             raise ValueError(f"{name} {tuple(out.shape)} for an input {tuple(x.shape)}")
         return out, _heads(out, name, H, D, dev)
-    dtype = x.dtype if y_dtype is None else _F32 if y_dtype == DTYPE_F32 else _BF16
     if dtype is not x.dtype:
         out = x.new_empty((B, T, H, D) if x.dim() == 4 else (T, H, D), dtype=dtype)
     else:                       # the quicker forms
@@ -1042,7 +1044,8 @@ def qk_norm_rope(q, k=None, norm=HEAD_NORM_NONE, q_weight=None, k_weight=None, q
     """hdq_qk_norm_rope: queries [batch, length, heads, dim] (or [length, heads,
     dim]) and, with their own number of heads, keys, normed over each head and
     rotated.  Any strides but the last; outputs are new contiguous tensors (of
-    y_dtype, None: the input's) or q_out and k_out (which may be q and k).
+    y_dtype, DTYPE_F32 or DTYPE_BF16; None: the input's) or q_out and k_out (which
+    may be q and k).
     Returns (q_out, k_out), or q_out alone without k."""
     shape, dev = _head_shape(q, "q"), q.device
     B, T, H, D = shape
