@@ -697,8 +697,8 @@ int hdq_w4_quantize(const void *w, const hdq_w4_tensor *out, void *stream);
  *   y : device [M, N], HDQ_DTYPE_BF16 or HDQ_DTYPE_F32, aligned to an element.
  * A group's sum is taken in float32 on the matrix instructions, as
  * sum (16 + u) x - (16 + z) sum x with exact products, and scaled and added in
- * float32; the error is that of a float32 sum over terms (32 + z) / |u - z| times
- * as large.  A token with a NaN or an infinity, or with such a sum past float32's
+ * float32; the error is that of a float32 sum over terms (32 + u + z) |s x| in
+ * place of |u - z| |s x|.  A token with a NaN or an infinity, or with such a sum past float32's
  * range, gets NaN or infinities; the others' outputs are not touched by it.
  *   ws, ws_bytes : device scratch, 256-byte aligned, >=
  *       hdq_w4_linear_workspace_bytes(M, N, K) (NULL where that is 0, as for one
