@@ -22,7 +22,10 @@
 // Two forms: k_heads16 (heads16.h), 16 elements a lane, for heads of a multiple
 // of 16 in whole vectors, and k_heads here, 8 elements a lane, for the rest.
 // With one form of 8 elements the largest calls took 86 us (62) and 49 (32 then, 20 now):
-// a step's addresses, lane sums and tests served half as many elements.
+// a step's addresses, lane sums and tests served half as many elements.  What is left to
+// k_heads: the rotation of 32 of 64 elements in halves, 17776 tokens of 30 heads, 28 us (a copy
+// 28); norm and rotation of 52 heads of 72 115 us, of 40 heads of 96 on 16 elements 72;
+// 4050 tokens into the cache, 72 heads of 80 in blocks of 16 41 us, 60 of 96 in blocks of 32 36.
 // Rounding: everything is float32 until the output's type or the code; angles are
 // float64 up to the fraction of a turn.
 #include "heads_device.h"

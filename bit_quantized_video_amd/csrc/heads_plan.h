@@ -29,11 +29,12 @@ inline int bits_for(int64_t n) {  // smallest b with 2^b >= n
   return b;
 }
 
-// Waves wanted before a wave takes more than one step, with angles to compute
-// (fewer, longer waves do that less often) and without: eight and 32 a CU.  With
-// 512 and 8192 in place of 2048, 1350 tokens of 60 heads took 9.7 and 9.7 us
-// (8.3), 4050 of 90 into the cache 22.7 and 25.3 (22.9, now 20); reading 5400 tokens of
-// 30 with 2048 and 32768 in place of 8192 14.5 and 16.1 (14.3).
+// Waves wanted before a wave takes more than one step, of the kernels that may have
+// angles to compute (fewer, longer waves do that less often; calls without angles
+// take the same) and of the cache's reader: eight and 32 a CU.  With 512 and 8192 in
+// place of 2048, 1350 tokens of 60 heads, rotated, took 9.7 and 9.7 us (8.3), 4050 of 90
+// into the cache 22.7 and 25.3 (22.9, now 20); reading 5400 tokens of 30 with 2048
+// and 32768 in place of 8192 14.5 and 16.1 (14.3).
 constexpr int64_t kHeadWaves = 2048, kReadWaves = 8192;
 
 // log2 of the lanes a group's maximum is taken over: all of a head's when the

@@ -239,8 +239,10 @@ __global__ __launch_bounds__(R == 4 ? 512 : 1024) void k_w4(const W4Args g) {
 // tokens once and LDS would serve no second reader; with 4 / MT tiles of K for
 // each wave (16 fragments of the tokens, 64 registers) all its loads are in
 // flight at once.  One launch where k_w4_shared takes two.  13 x 4096 -> 1921 in
-// groups of 32 6.8 us (k_w4_shared 5.4 + 2.5), bound by the tokens' way from L2,
-// 106 KB a CU; 16 x 1920 -> 1920 4.7 (k_w4 6.8).
+// groups of 32 6.7 us (k_w4_shared 5.4 + 2.5), 16 x 1920 -> 1920 4.7 (k_w4 6.8).
+// Bound by the tokens' way from L2 to the CU: 4096 -> 1921 takes 4.8 us with 1 token,
+// 5.2 with 4, 6.0 with 8, 7.2 with 16, so 0.16 us and 8 KB a token, 50 bytes a ns and
+// CU; a workgroup alone (16 rows) 3.5 with 1 token and 5.7 with 13, 256 of them 7.2.
 template <int MT, int GROUPS, bool ZERO, bool F32>
 __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
   constexpr int TILES = 4 / MT;  // of K, a wave's
@@ -297,7 +299,8 @@ __global__ __launch_bounds__(1024) void k_w4_direct(const W4Args g) {
 // takes longer than a stage), none of them under a condition: the waits then
 // count the ones that may still be in flight.
 //
-// 64 x 12288 -> 4096: 15.5 to 16.3 us and 4 for the sums, 12 stages of 0.9 us and
+// 64 x 12288 -> 4096: 15.5 to 16.3 us and 4 for the sums (16.5 to 17.2 a call in a row
+// of them, whose second launch overlaps the next call's first), 12 stages of 0.9 us and
 // about 5 to begin and end.  A stage's parts are 650 cycles of vector
 // instructions, 770 of matrix ones and 640 of LDS a SIMD or CU, of about 2000:
 // what is left is waiting between them.  SIMD: waves a SIMD that the
@@ -453,8 +456,9 @@ __global__ __launch_bounds__(256) void k_w4_join(const float* __restrict__ sums,
 // Position of column e of eight in a packed word.
 __device__ __forceinline__ int nibble(int e) { return (e >> 1) + 4 * (e & 1); }
 
-// Codes of checkpoints (bytes [N, K / 2], even columns in the low nibbles;
-// scales and zero points [N, K / group]) to tiles: a lane's 16 bytes each.
+// Codes in rows (bytes [N, K / 2], even columns in the low nibbles; scales and
+// zero points [N, K / group]) to tiles: a lane's 16 bytes each.  Done once for a
+// layer: 512 -> 345600 54 us, 3.5 TB/s; 12288 -> 4096 18.
 __global__ __launch_bounds__(256) void k_w4_pack(const uint8_t* __restrict__ src, const uint16_t* __restrict__ scale,
                                                  const uint8_t* __restrict__ zero, int64_t N, int64_t K, int group,
                                                  int64_t tiles_k, int64_t tiles, W4Out out) {
@@ -493,6 +497,9 @@ __global__ __launch_bounds__(256) void k_w4_pack(const uint8_t* __restrict__ src
 //   with                 s = bf16((max - min) / 15) (0 among the values),
 //                        z = rne(-min / s), u = clamp(rne(w / s) + z, 0, 15).
 // A group below 2^-100 gets s = 0; one with a NaN or an infinity s = NaN.
+// Done once for a layer, and simple: neighbouring lanes read a group apart, twice.
+// 12288 -> 12288 in groups of 32 190 us, 2.1 TB/s; 512 -> 345600 in groups of 64 755 us
+// and 12288 -> 4096 in groups of 128 240, 0.6 and 0.5 TB/s.
 __global__ __launch_bounds__(256) void k_w4_quantize(const uint16_t* __restrict__ src, int64_t N, int64_t K, int group,
                                                      int64_t tiles_n, int64_t tiles_k, W4Out out) {
   const int groups = 128 / group;

@@ -847,8 +847,8 @@ class W4Weights:
 
 def w4_pack(codes, scale, zero=None, stream=None):
     """hdq_w4_pack: codes uint8 [N, K / 2] (even columns in the low nibbles),
-    scale bf16 [N, K / group] and zero points uint8 [N, K / group] or None, as
-    4-bit checkpoints hold them, to W4Weights."""
+    scale bf16 [N, K / group] and zero points uint8 [N, K / group] or None, to
+    W4Weights."""
     if codes.dtype != torch.uint8 or codes.dim() != 2 or scale.dim() != 2 or scale.shape[1] == 0:
         raise ValueError("expected uint8 codes [N, K / 2] and scales [N, K / group]")
     (N, half), dev = codes.shape, codes.device
@@ -1081,7 +1081,8 @@ class KvCache:
     (None: the head), rotated in Hadamard blocks of had_block.  Buffers
     (k_codes and v_codes uint8 [slots, heads, dim], or dim / 2 for INT4;
     k_scale and v_scale float32 [slots, heads, dim / group]) are the given
-    ones or new ones on `device`, zeroed."""
+    ones or new ones on `device`, zeroed.  Calls with a cache of 0 slots, whose
+    buffers have no address, are refused."""
 
     def __init__(self, slots, heads, dim, fmt=CACHE_FP8, group=None, had_block=1, device=None, k_codes=None, k_scale=None,
                  v_codes=None, v_scale=None):

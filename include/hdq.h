@@ -673,9 +673,9 @@ typedef struct hdq_w4_tensor {
 size_t hdq_w4_bytes(int64_t N, int64_t K, int32_t group, int32_t buffer);
 
 /*
- * hdq_w4_pack -- weights as 4-bit checkpoints hold them, into tiles.
+ * hdq_w4_pack -- weights whose codes lie in rows, two a byte, into tiles.
  *   codes : device uint8 [N, K / 2], the even column in the low nibble.
- *   scale : device bf16 [N, K / group].
+ *   scale : device bf16 [N, K / group] (scales of other types are rounded to it first).
  *   zero  : device uint8 [N, K / group]; given exactly when out->zero is.
  *   out   : N, K, group and the buffers set by the caller.
  */
@@ -763,7 +763,8 @@ typedef struct hdq_head_norm {
  * the `axes` axes add up to dim).  A token with a negative position on any
  * axis is not rotated (text tokens in front of a video's).  p turns[j] is taken
  * in float64 in two parts, so its fraction is off by the rounding of turns[j]
- * alone, p 2^-53 turns[j]; cosine and sine are float32. */
+ * alone, p 2^-53 turns[j] (p up to 2^53; larger ones are rounded to float64);
+ * cosine and sine are float32. */
 #define HDQ_ROPE_INTERLEAVED 0
 #define HDQ_ROPE_HALF 1
 #define HDQ_ROPE_MAX_AXES 3
@@ -822,7 +823,9 @@ int hdq_qk_norm_rope(const hdq_heads *q, const hdq_heads *k, int64_t batch, int6
  * With y the rotated values and a = max|y| of a group: scale = fl32(a / top), code =
  * rne(y * fl32(top / a)), top 127, 448 (E4M3 nearest, ties to even) or 7.  A group
  * with a < 2^-100 gets scale 0 and zero codes, one with a NaN or an infinity
- * scale NaN and zero codes. */
+ * scale NaN and zero codes.  y comes from float32 butterflies and one product with
+ * 1 / sqrt(had_block): a sum of theirs past float32's range counts as an infinity.
+ * slots may be 0; the buffers are never NULL. */
 #define HDQ_CACHE_INT8 0
 #define HDQ_CACHE_FP8 1
 #define HDQ_CACHE_INT4 2
